@@ -1,4 +1,4 @@
-"""Ozaki Scheme II FP64 GEMM emulation for AMD MI355X (gfx950).
+"""Ozaki Scheme II FP64 GEMM emulation, and linear layers in 16 and 8 bits, for AMD MI355X (gfx950).
 
 The compute path is the HIP library ``liboz2.so`` (sources in ``csrc/``, C ABI in
 ``include/oz2.h``); ``binding`` is its thin ctypes binding.  The binding is loaded
@@ -16,6 +16,7 @@ _BINDING_NAMES = {
     "ozaki2_moduli", "ozaki2_tau", "ozaki2_status_string", "dgemm", "dgemm_debug",
     "colmajor", "empty_colmajor", "Oz2Error", "OZ2Dump", "OZ2_FAST", "OZ2_ACCU", "OZ2_OK",
     "OZ2_ERR_ARG", "OZ2_ERR_UNSUPPORTED", "OZ2_ERR_WORKSPACE", "OZ2_ERR_HIP",
+    "linear", "linear_backward", "dropout_add", "quantize_rows", "linear_i8",
 }
 
 

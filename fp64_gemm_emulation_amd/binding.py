@@ -2,7 +2,8 @@
 
 Argument marshalling only: every step of the computation runs in the HIP library.
 The functions named like the C entry points take plain integers / device pointers;
-``dgemm`` and ``dgemm_debug`` are conveniences over torch tensors (PyTorch supplies
+``dgemm`` and ``dgemm_debug``, and ``linear``, ``linear_backward``, ``dropout_add``,
+``quantize_rows`` and ``linear_i8``, are conveniences over torch tensors (PyTorch supplies
 device memory and the current stream, nothing else).
 
 Loading fails loudly if the library has not been built: there is no fallback.
@@ -22,6 +23,12 @@ OZ2_OP_N, OZ2_OP_T = 0, 1
 OZ2_FLAG_NONFINITE = 1
 OZ2_NOALLOC_SCRATCH_BYTES = 256 << 20
 MODES = {"fast": OZ2_FAST, "accu": OZ2_ACCU}
+OZ2_BF16, OZ2_F16, OZ2_F32 = 0, 1, 2
+OZ2_ACT_NONE, OZ2_ACT_RELU, OZ2_ACT_GELU, OZ2_ACT_GELU_TANH, OZ2_ACT_SILU = 0, 1, 2, 3, 4
+OZ2_LINEAR_FWD, OZ2_LINEAR_BWD, OZ2_LINEAR_I8 = 0, 1, 2
+OZ2_LINEAR_I8_MAX_Q = 131072
+ACTIVATIONS = {"none": OZ2_ACT_NONE, "relu": OZ2_ACT_RELU, "gelu": OZ2_ACT_GELU, "gelu_tanh": OZ2_ACT_GELU_TANH,
+               "silu": OZ2_ACT_SILU}
 
 
 class Oz2Error(RuntimeError):
@@ -36,6 +43,12 @@ class OZ2Dump(ctypes.Structure):
     _fields_ = [(name, ctypes.c_void_p) for name in
                 ("d", "b", "Ap", "Bp", "At", "Bt", "P", "R", "X",
                  "e", "f", "Abar", "Bbar", "rho", "gamma")]
+
+
+class OZ2Dropout(ctypes.Structure):
+    """Mirror of oz2_dropout_t."""
+
+    _fields_ = [("probability", ctypes.c_double), ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64)]
 
 
 def _load():
@@ -58,6 +71,12 @@ def _load():
         "ozaki2_moduli": (i, [i, ctypes.POINTER(i)]),
         "ozaki2_tau": (i, [i]),
         "ozaki2_status_string": (ctypes.c_char_p, [i]),
+        "ozaki2_linear": (i, [i, i, i, i, vp, i, vp, i, vp, i, vp, vp, i, vp, i, vp, i, vp, sz, vp]),
+        "ozaki2_linear_bwd": (i, [i, i, i, i, vp, i, vp, i, vp, i, vp, i, i, vp, vp, i, vp, i, vp, vp, sz, vp]),
+        "ozaki2_dropout_add": (i, [i, i, i, vp, i, vp, i, vp, vp, i, vp]),
+        "ozaki2_quantize_rows": (i, [i, i, i, vp, i, vp, i, vp, vp]),
+        "ozaki2_linear_i8": (i, [i, i, i, i, vp, i, vp, i, vp, vp, i, vp, i, vp, i, vp, sz, vp]),
+        "ozaki2_linear_workspace_size": (sz, [i, i, i, i, i]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -136,6 +155,38 @@ def ozaki2_tau(s: int) -> int:
 
 def ozaki2_status_string(status: int) -> str:
     return _LIB.ozaki2_status_string(status).decode()
+
+
+def _dropout_ref(dropout):
+    return ctypes.addressof(dropout) if dropout is not None else None
+
+
+def ozaki2_linear(type, p, q, r, X, ldx, W, ldw, bias, act, dropout: OZ2Dropout | None, R, ldr, Z, ldz, Y, ldy,
+                  work, work_bytes, stream) -> int:
+    return _LIB.ozaki2_linear(type, p, q, r, X, ldx, W, ldw, bias, act, _dropout_ref(dropout), R, ldr, Z, ldz, Y, ldy,
+                              work, work_bytes, stream)
+
+
+def ozaki2_linear_bwd(type, p, q, r, dY, lddy, X, ldx, W, ldw, Z, ldz, act, dropout: OZ2Dropout | None, dX, lddx,
+                      dW, lddw, dbias, work, work_bytes, stream) -> int:
+    return _LIB.ozaki2_linear_bwd(type, p, q, r, dY, lddy, X, ldx, W, ldw, Z, ldz, act, _dropout_ref(dropout), dX, lddx,
+                                  dW, lddw, dbias, work, work_bytes, stream)
+
+
+def ozaki2_dropout_add(type, p, r, X, ldx, R, ldr, dropout: OZ2Dropout | None, Y, ldy, stream) -> int:
+    return _LIB.ozaki2_dropout_add(type, p, r, X, ldx, R, ldr, _dropout_ref(dropout), Y, ldy, stream)
+
+
+def ozaki2_quantize_rows(type, p, q, X, ldx, Q, ldq, scale, stream) -> int:
+    return _LIB.ozaki2_quantize_rows(type, p, q, X, ldx, Q, ldq, scale, stream)
+
+
+def ozaki2_linear_i8(type, p, q, r, X, ldx, V, ldv, t, bias, act, R, ldr, Y, ldy, work, work_bytes, stream) -> int:
+    return _LIB.ozaki2_linear_i8(type, p, q, r, X, ldx, V, ldv, t, bias, act, R, ldr, Y, ldy, work, work_bytes, stream)
+
+
+def ozaki2_linear_workspace_size(call, type, p, q, r) -> int:
+    return _LIB.ozaki2_linear_workspace_size(call, type, p, q, r)
 
 
 # --- torch conveniences --------------------------------------------------------------
@@ -253,3 +304,231 @@ def dgemm_debug(A, B, s: int = 14, mode: str = "fast", want=DUMP_FIELDS, stream=
         bufs["Bp"] = bufs["Bp"].t()
     bufs["C"] = C
     return bufs
+
+
+# --- linear layers -------------------------------------------------------------------
+# Row-major 2-D tensors, one token per row (a 3-D batch is passed as its reshape(-1, q)).
+# Outputs and scratch are allocated on the stream of the call, so calls on different
+# streams share nothing; operands made on another stream have to be ready on this one.
+def _types():
+    import torch
+    return {torch.bfloat16: OZ2_BF16, torch.float16: OZ2_F16, torch.float32: OZ2_F32}
+
+
+def _element_type(t, name, f32=False):
+    code = _types().get(t.dtype)
+    if code is None or (code == OZ2_F32 and not f32):
+        raise ValueError(f"{name} must be bfloat16 or float16" + (" or float32" if f32 else "") + f", not {t.dtype}")
+    return code
+
+
+def _rows(t, name, shape, like, dtype=None):
+    """(pointer, leading dimension) of a row-major matrix on the device of `like`; (None, 1) for None."""
+    if t is None:
+        return None, 1
+    if t.dim() != 2 or tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
+    if t.dtype != (dtype or like.dtype):
+        raise ValueError(f"{name} must be {dtype or like.dtype}, not {t.dtype}")
+    if not t.is_cuda or t.device != like.device:
+        raise ValueError(f"{name} must be a CUDA tensor on the device of the other operands")
+    rows, cols = shape
+    if rows == 0 or cols == 0:
+        return t.data_ptr(), max(1, cols)
+    step, ld = t.stride(1), t.stride(0)
+    if (cols > 1 and step != 1) or (rows > 1 and ld < cols):
+        raise ValueError(f"{name} must be row-major (stride (ld >= columns, 1)), not stride {tuple(t.stride())}")
+    if rows == 1:
+        ld = cols
+    if ld >= 1 << 31:
+        raise ValueError(f"{name}: the row stride does not fit 32 bits")
+    return t.data_ptr(), ld
+
+
+def _vector(t, name, n, like, dtype=None):
+    if t is None:
+        return None
+    if t.dim() != 1 or t.shape[0] != n:
+        raise ValueError(f"{name} must have shape {(n,)}, not {tuple(t.shape)}")
+    if t.dtype != (dtype or like.dtype):
+        raise ValueError(f"{name} must be {dtype or like.dtype}, not {t.dtype}")
+    if not t.is_cuda or t.device != like.device:
+        raise ValueError(f"{name} must be a CUDA tensor on the device of the other operands")
+    if n > 1 and t.stride(0) != 1:
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _activation(name):
+    code = ACTIVATIONS.get(name)
+    if code is None:
+        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, not {name!r}")
+    return code
+
+
+def _make_dropout(dropout, seed, offset):
+    if dropout == 0.0:
+        return None
+    if not 0.0 <= dropout <= 1.0:
+        raise ValueError("dropout must be a probability")
+    if not (0 <= seed < 1 << 64 and 0 <= offset < 1 << 64):
+        raise ValueError("seed and offset must fit 64 bits")
+    return OZ2Dropout(dropout, seed, offset)
+
+
+class _Call:
+    """The device and the stream of one call: made current while outputs and scratch are
+    allocated and the library is entered."""
+
+    def __init__(self, like, stream):
+        import torch
+        if not like.is_cuda:
+            raise ValueError("operands must be CUDA tensors")
+        dev = like.device
+        if stream is not None and stream.device != dev:
+            raise ValueError("the stream belongs to another device than the operands")
+        self._ctx = None
+        if stream is not None:
+            self._ctx = torch.cuda.stream(stream)      # also makes the stream's device current
+        elif dev.index != torch.cuda.current_device():
+            self._ctx = torch.cuda.device(dev)
+        self.raw = stream.cuda_stream if stream is not None else torch.cuda.current_stream(dev).cuda_stream
+        self._dev = dev
+
+    def __enter__(self):
+        if self._ctx is not None:
+            self._ctx.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if self._ctx is not None:
+            self._ctx.__exit__(*exc)
+
+    def scratch(self, nbytes):
+        if nbytes == 0:
+            return None
+        import torch
+        return torch.empty(nbytes, dtype=torch.uint8, device=self._dev)
+
+
+def _ptr(t):
+    return t.data_ptr() if t is not None else None
+
+
+def _check(rc, what):
+    if rc != OZ2_OK:
+        raise Oz2Error(rc, what)
+
+
+def _two_dims(t, name):
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D tensor, not {t.dim()}-D")
+    return t.shape
+
+
+def linear(x, w, bias=None, activation: str = "none", residual=None, dropout: float = 0.0, seed: int = 0,
+           offset: int = 0, return_z: bool = False, out=None, stream=None):
+    """residual + D(act(x w^T + bias)) for x [p, q], w [r, q] in bfloat16 or float16, D the
+    dropout of the C header; with return_z, (y, z), z the pre-activation for
+    linear_backward.  `out` may be `residual` itself."""
+    import torch
+    p, q = _two_dims(x, "x")
+    r = _two_dims(w, "w")[0]
+    kind, act, drop = _element_type(x, "x"), _activation(activation), _make_dropout(dropout, seed, offset)
+    with _Call(x, stream) as call:
+        px, ldx = _rows(x, "x", (p, q), x)
+        pw, ldw = _rows(w, "w", (r, q), x)
+        pr, ldr = _rows(residual, "residual", (p, r), x)
+        pb = _vector(bias, "bias", r, x)
+        y = out if out is not None else torch.empty((p, r), dtype=x.dtype, device=x.device)
+        py, ldy = _rows(y, "out", (p, r), x)
+        z = torch.empty((p, r), dtype=x.dtype, device=x.device) if return_z else None
+        work = call.scratch(_LIB.ozaki2_linear_workspace_size(OZ2_LINEAR_FWD, kind, p, q, r))
+        rc = ozaki2_linear(kind, p, q, r, px, ldx, pw, ldw, pb, act, drop, pr, ldr, _ptr(z), max(1, r), py, ldy,
+                           _ptr(work), work.numel() if work is not None else 0, call.raw)
+    _check(rc, "ozaki2_linear")
+    return (y, z) if return_z else y
+
+
+def linear_backward(dy, x, w, z=None, activation: str = "none", dropout: float = 0.0, seed: int = 0, offset: int = 0,
+                    needs=("x", "w", "bias"), stream=None):
+    """(dx, dw, dbias) of linear from dy [p, r]; those not named in `needs` are None.  z is
+    linear's pre-activation, needed unless activation is "none"; dropout, seed and offset have
+    to be the forward call's.  The residual's gradient is dy itself."""
+    import torch
+    p, r = _two_dims(dy, "dy")
+    q = _two_dims(w, "w")[1]
+    kind, act, drop = _element_type(dy, "dy"), _activation(activation), _make_dropout(dropout, seed, offset)
+    unknown = set(needs) - {"x", "w", "bias"}
+    if unknown:
+        raise ValueError(f"needs names {sorted(unknown)}: only x, w and bias have gradients here")
+    if act != OZ2_ACT_NONE and z is None:
+        raise ValueError("the gradient of an activation needs z")
+    with _Call(dy, stream) as call:
+        pdy, lddy = _rows(dy, "dy", (p, r), dy)
+        px, ldx = _rows(x, "x", (p, q), dy)
+        pw, ldw = _rows(w, "w", (r, q), dy)
+        pz, ldz = _rows(z, "z", (p, r), dy)
+        new = lambda name, *shape: torch.empty(shape, dtype=dy.dtype, device=dy.device) if name in needs else None  # noqa: E731
+        dx, dw, db = new("x", p, q), new("w", r, q), new("bias", r)
+        work = call.scratch(_LIB.ozaki2_linear_workspace_size(OZ2_LINEAR_BWD, kind, p, q, r))
+        rc = ozaki2_linear_bwd(kind, p, q, r, pdy, lddy, px, ldx, pw, ldw, pz, ldz, act, drop, _ptr(dx), max(1, q),
+                               _ptr(dw), max(1, q), _ptr(db), _ptr(work), work.numel() if work is not None else 0,
+                               call.raw)
+    _check(rc, "ozaki2_linear_bwd")
+    return dx, dw, db
+
+
+def dropout_add(x, residual=None, dropout: float = 0.0, seed: int = 0, offset: int = 0, out=None, stream=None):
+    """residual + D(x) for x [p, r] in bfloat16, float16 or float32; the gradient with respect
+    to x is dropout_add(dy, None, ...) with the same dropout, seed and offset.  `out` may be x
+    or residual itself."""
+    import torch
+    p, r = _two_dims(x, "x")
+    kind, drop = _element_type(x, "x", f32=True), _make_dropout(dropout, seed, offset)
+    with _Call(x, stream) as call:
+        px, ldx = _rows(x, "x", (p, r), x)
+        pr, ldr = _rows(residual, "residual", (p, r), x)
+        y = out if out is not None else torch.empty((p, r), dtype=x.dtype, device=x.device)
+        py, ldy = _rows(y, "out", (p, r), x)
+        rc = ozaki2_dropout_add(kind, p, r, px, ldx, pr, ldr, drop, py, ldy, call.raw)
+    _check(rc, "ozaki2_dropout_add")
+    return y
+
+
+def quantize_rows(x, stream=None):
+    """(int8 tensor, float32 scale of each row) of x [p, q] in bfloat16, float16 or float32."""
+    import torch
+    p, q = _two_dims(x, "x")
+    kind = _element_type(x, "x", f32=True)
+    with _Call(x, stream) as call:
+        px, ldx = _rows(x, "x", (p, q), x)
+        out = torch.empty((p, q), dtype=torch.int8, device=x.device)
+        scale = torch.empty((p,), dtype=torch.float32, device=x.device)
+        rc = ozaki2_quantize_rows(kind, p, q, px, ldx, out.data_ptr(), max(1, q), scale.data_ptr(), call.raw)
+    _check(rc, "ozaki2_quantize_rows")
+    return out, scale
+
+
+def linear_i8(x, v, t, bias=None, activation: str = "none", residual=None, out=None, stream=None):
+    """residual + act(x w^T + bias) with w held as (v, t) = quantize_rows(w): x [p, q] in
+    bfloat16 or float16 is quantised by rows in the call.  `out` may be `residual` itself."""
+    import torch
+    p, q = _two_dims(x, "x")
+    r = _two_dims(v, "v")[0]
+    kind, act = _element_type(x, "x"), _activation(activation)
+    with _Call(x, stream) as call:
+        px, ldx = _rows(x, "x", (p, q), x)
+        pv, ldv = _rows(v, "v", (r, q), x, torch.int8)
+        pt = _vector(t, "t", r, x, torch.float32)
+        if pt is None:
+            raise ValueError("t is needed")
+        pr, ldr = _rows(residual, "residual", (p, r), x)
+        pb = _vector(bias, "bias", r, x)
+        y = out if out is not None else torch.empty((p, r), dtype=x.dtype, device=x.device)
+        py, ldy = _rows(y, "out", (p, r), x)
+        work = call.scratch(_LIB.ozaki2_linear_workspace_size(OZ2_LINEAR_I8, kind, p, q, r))
+        rc = ozaki2_linear_i8(kind, p, q, r, px, ldx, pv, ldv, pt, pb, act, pr, ldr, py, ldy, _ptr(work),
+                              work.numel() if work is not None else 0, call.raw)
+    _check(rc, "ozaki2_linear_i8")
+    return y

@@ -5,6 +5,7 @@
 #include <algorithm>
 #include <cstdint>
 #include <cstring>
+#include <new>
 #include <vector>
 
 #include "oz2.h"
@@ -182,6 +183,7 @@ struct Owned {
 
 struct State {
   std::vector<Owned> owned;  // library-owned workspace, one per device ordinal
+  std::vector<Owned> owned_linear;  // the same for the linear-layer calls
   void* user = nullptr;
   size_t user_bytes = 0;
   // timing
@@ -222,17 +224,13 @@ int scratch_workspace(char** base) {
   return OZ2_OK;
 }
 
-int acquire_workspace(size_t need, char** base) {
-  if (g.user != nullptr) {
-    if (g.user_bytes < need) return OZ2_ERR_WORKSPACE;
-    *base = static_cast<char*>(g.user);
-    return OZ2_OK;
-  }
-  // the buffer of the device current at this call (each device gets its own)
+// A library-owned buffer of at least `need` bytes on the device current at this call (each
+// device gets its own), allocated or grown on first need.
+int acquire_owned(std::vector<Owned>& owned, size_t need, char** base) {
   int dev = 0;
   if (hipGetDevice(&dev) != hipSuccess || dev < 0) return OZ2_ERR_HIP;
-  if (g.owned.size() <= static_cast<size_t>(dev)) g.owned.resize(static_cast<size_t>(dev) + 1);
-  Owned& o = g.owned[static_cast<size_t>(dev)];
+  if (owned.size() <= static_cast<size_t>(dev)) owned.resize(static_cast<size_t>(dev) + 1);
+  Owned& o = owned[static_cast<size_t>(dev)];
   if (o.bytes < need) {
     if (o.ptr != nullptr) {
       if (hipDeviceSynchronize() != hipSuccess) return OZ2_ERR_HIP;
@@ -249,6 +247,15 @@ int acquire_workspace(size_t need, char** base) {
   }
   *base = static_cast<char*>(o.ptr);
   return OZ2_OK;
+}
+
+int acquire_workspace(size_t need, char** base) {
+  if (g.user != nullptr) {
+    if (g.user_bytes < need) return OZ2_ERR_WORKSPACE;
+    *base = static_cast<char*>(g.user);
+    return OZ2_OK;
+  }
+  return acquire_owned(g.owned, need, base);
 }
 
 struct Recorder {
@@ -353,6 +360,23 @@ int run(const Call& c, void* stream, const oz2_dump_t* dump, bool use_scratch = 
 
 }  // namespace
 
+namespace oz2 {
+
+int acquire_linear_workspace(size_t need, char** base) {
+  if (g.user != nullptr) {
+    if (g.user_bytes < need + kLinearWorkspaceSkip) return OZ2_ERR_WORKSPACE;
+    *base = static_cast<char*>(g.user) + kLinearWorkspaceSkip;
+    return OZ2_OK;
+  }
+  try {
+    return acquire_owned(g.owned_linear, need, base);
+  } catch (const std::bad_alloc&) {  // the table of buffers
+    return OZ2_ERR_WORKSPACE;
+  }
+}
+
+}  // namespace oz2
+
 extern "C" {
 
 int ozaki2_dgemm(int p, int q, int r, const double* A, int lda, const double* B, int ldb, double* C, int ldc, int s,
@@ -397,17 +421,19 @@ int ozaki2_release(void) {
   int cur = 0;
   if (hipGetDevice(&cur) != hipSuccess) rc = OZ2_ERR_HIP;
   if (!g.events.empty() && hipDeviceSynchronize() != hipSuccess) rc = OZ2_ERR_HIP;
-  for (size_t dev = 0; dev < g.owned.size(); ++dev) {
-    Owned& o = g.owned[dev];
-    if (o.ptr == nullptr) continue;
-    // synchronize and free on the device that owns the buffer
-    if (hipSetDevice(static_cast<int>(dev)) != hipSuccess || hipDeviceSynchronize() != hipSuccess ||
-        hipFree(o.ptr) != hipSuccess)
-      rc = OZ2_ERR_HIP;
-    o.ptr = nullptr;
-    o.bytes = 0;
+  for (std::vector<Owned>* owned : {&g.owned, &g.owned_linear}) {
+    for (size_t dev = 0; dev < owned->size(); ++dev) {
+      Owned& o = (*owned)[dev];
+      if (o.ptr == nullptr) continue;
+      // synchronize and free on the device that owns the buffer
+      if (hipSetDevice(static_cast<int>(dev)) != hipSuccess || hipDeviceSynchronize() != hipSuccess ||
+          hipFree(o.ptr) != hipSuccess)
+        rc = OZ2_ERR_HIP;
+      o.ptr = nullptr;
+      o.bytes = 0;
+    }
+    if (!owned->empty() && hipSetDevice(cur) != hipSuccess) rc = OZ2_ERR_HIP;
   }
-  if (!g.owned.empty() && hipSetDevice(cur) != hipSuccess) rc = OZ2_ERR_HIP;
   for (hipEvent_t e : g.events) (void)hipEventDestroy(e);
   g.events.clear();
   g.timing = false;

@@ -76,6 +76,13 @@ hipError_t launch_gemm(const Work& w, int epi, const DumpPtrs& dump, hipStream_t
 hipError_t launch_crt(const Work& w, double* C, long ldc, double alpha, double beta, const DumpPtrs& dump,
                       hipStream_t st);
 
+// Workspace of the linear-layer calls: the caller's (ozaki2_set_workspace) beyond its first
+// kLinearWorkspaceSkip bytes, where the flag word of the last dgemm call stays readable, else
+// a library-owned buffer of its own (growing it never moves the dgemm calls' buffer, whose
+// address captured graphs and the flag word keep).  Returns an OZ2_* status.
+constexpr size_t kLinearWorkspaceSkip = 256;
+int acquire_linear_workspace(size_t need, char** base);
+
 // validation helper: operand planes in the tile-contiguous layout (padded) -> dst
 // [planes][rows][q], plain row-major
 hipError_t launch_unpack_operands(const int8_t* src, long plane_stride, int planes, int rows, int q, int q_pad,

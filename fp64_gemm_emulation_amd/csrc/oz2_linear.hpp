@@ -1,0 +1,211 @@
+// oz2_linear.hpp -- what the linear-layer kernels share: 16-bit element types, eight-element
+// loads and stores, activations and their slopes, the counter-based dropout mask, and the
+// epilogue that turns eight accumulators of one output row into stored results; and the host
+// launch interface between oz2_linear_api.hip and the kernels.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+namespace oz2 {
+
+typedef __bf16 bf16;
+typedef _Float16 f16;
+
+enum { kTypeBf16 = 0, kTypeF16 = 1, kTypeF32 = 2 };                            // mirror of oz2_type_t
+enum { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4 };  // mirror of oz2_act_t
+
+// Dropout as the kernels see it: keep where the 16-bit draw is at least t, times scale.
+struct Drop {
+  uint32_t t = 0;  // rint(2^16 p); 0: everything kept, 2^16: nothing
+  float scale = 1.0f;  // 2^16 / (2^16 - t), the reciprocal of the exact keep probability
+  uint32_t k0 = 0, k1 = 0;  // key: the seed's halves
+  uint32_t c2 = 0, c3 = 0;  // upper counter words: the offset's halves
+};
+
+// Epilogue of one product: out = res + drop(act(acc * xs[m] * ws[n] + bias[n])).
+struct Epilogue {
+  const void* bias = nullptr;  // [n], the operands' type
+  int act = kActNone;
+  Drop drop;
+  const void* res = nullptr;  // residual, row stride ldr (may be y itself)
+  long ldr = 0;
+  void* z = nullptr;  // pre-activation output, row stride ldz
+  long ldz = 0;
+  void* y = nullptr;  // output, row stride ldy
+  long ldy = 0;
+  const float* xs = nullptr;  // int8 products: scale of each row of the left operand
+  const float* ws = nullptr;  //               and of each row of the right one
+};
+
+// out[m][n] = sum_k left[m][k] right[n][k], m < rows, n < cols, k < depth; element (i, k) of
+// an operand is at ptr[i * row + k * step].
+struct Product {
+  int type;   // element type of operands (unless int8) and outputs
+  bool i8;    // int8 operands
+  int rows, cols, depth;
+  const void* left;
+  long left_row, left_step;
+  const void* right;
+  long right_row, right_step;
+  Epilogue epi;
+};
+
+hipError_t launch_product(const Product& pr, hipStream_t st);
+hipError_t launch_dropout_add(int type, int p, int r, const void* x, long ldx, const void* res, long ldr,
+                              const Drop& drop, void* y, long ldy, hipStream_t st);
+// dz = drop(dy) act'(z) in the operands' type (skipped when dz is null) and, when db is not
+// null, db = its column sums, by way of part: grad_row_blocks(p) x r floats.
+int grad_row_blocks(int p);
+hipError_t launch_grad_rows(int type, int p, int r, const void* dy, long lddy, const void* z, long ldz, int act,
+                            const Drop& drop, void* dz, long lddz, void* db, float* part, hipStream_t st);
+hipError_t launch_quantize_rows(int type, int p, int q, const void* x, long ldx, int8_t* out, long ldo, float* scale,
+                                hipStream_t st);
+
+#ifdef __HIP_DEVICE_COMPILE__
+#define OZ2_UNROLL _Pragma("unroll")
+#else
+#define OZ2_UNROLL
+#endif
+
+// ---- eight consecutive elements ------------------------------------------------------
+// Rows may start at any element, so these are unaligned vector accesses (the hardware's
+// unaligned mode) where all eight lie inside the row, and single elements at its end.
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, int valid, float (&v)[8]) {
+  T t[8];
+  if (valid >= 8) {
+    __builtin_memcpy(t, p, sizeof(t));
+  } else {
+    OZ2_UNROLL
+    for (int i = 0; i < 8; ++i) t[i] = i < valid ? p[i] : static_cast<T>(0.0f);
+  }
+  OZ2_UNROLL
+  for (int i = 0; i < 8; ++i) v[i] = static_cast<float>(t[i]);
+}
+
+template <typename T>
+__device__ __forceinline__ void store8(T* p, int valid, const float (&v)[8]) {
+  T t[8];
+  OZ2_UNROLL
+  for (int i = 0; i < 8; ++i) t[i] = static_cast<T>(v[i]);
+  if (valid >= 8) {
+    __builtin_memcpy(p, t, sizeof(t));
+  } else {
+    OZ2_UNROLL
+    for (int i = 0; i < 8; ++i)
+      if (i < valid) p[i] = t[i];
+  }
+}
+
+// ---- activations -----------------------------------------------------------------------
+// gelu(a) = a Phi(a), Phi the normal distribution function; gelu_tanh is its tanh form,
+// a sigmoid(2 c (a + k a^3)) with c = sqrt(2 / pi), k = 0.044715; silu(a) = a sigmoid(a).
+constexpr float kSqrtHalf = 0.70710678118654752f;
+constexpr float kInvSqrt2Pi = 0.39894228040143268f;
+constexpr float kGelu2C = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+constexpr float kGeluK = 0.044715f;
+
+__device__ __forceinline__ float sigmoid(float v) { return 1.0f / (1.0f + expf(-v)); }
+
+__device__ __forceinline__ float activate(float a, int act) {
+  switch (act) {
+    case kActRelu:
+      return a <= 0.0f ? 0.0f : a;  // NaN stays NaN
+    case kActGelu:
+      return 0.5f * a * (1.0f + erff(a * kSqrtHalf));
+    case kActGeluTanh:
+      return a * sigmoid(kGelu2C * (a + kGeluK * a * a * a));
+    case kActSilu:
+      return a * sigmoid(a);
+    default:
+      return a;
+  }
+}
+
+__device__ __forceinline__ float activation_slope(float z, int act) {
+  switch (act) {
+    case kActRelu:
+      return z > 0.0f ? 1.0f : 0.0f;
+    case kActGelu:
+      return 0.5f * (1.0f + erff(z * kSqrtHalf)) + z * kInvSqrt2Pi * expf(-0.5f * z * z);
+    case kActGeluTanh: {
+      const float s = sigmoid(kGelu2C * (z + kGeluK * z * z * z));
+      return s + z * s * (1.0f - s) * kGelu2C * (1.0f + 3.0f * kGeluK * z * z);
+    }
+    case kActSilu: {
+      const float s = sigmoid(z);
+      return s * (1.0f + z * (1.0f - s));
+    }
+    default:
+      return 1.0f;
+  }
+}
+
+// ---- dropout -----------------------------------------------------------------------------
+// Philox4x32-10 (Salmon, Moraes, Dror, Shaw, "Parallel random numbers: as easy as 1, 2, 3",
+// 2011).  One block serves eight consecutive elements of one row, 16 bits each: the keep
+// probability is then a multiple of 2^-16, and its exact value sets the scale, so the
+// expectation is exact; two blocks of 32-bit draws would double the generator's cost, which
+// is what bounds it (20 full-width multiplies at a quarter of the vector rate per block).
+__host__ __device__ __forceinline__ void philox_block(uint32_t (&c)[4], uint32_t k0, uint32_t k1) {
+  for (int i = 0; i < 10; ++i) {
+    const uint64_t a = static_cast<uint64_t>(c[0]) * 0xD2511F53u;
+    const uint64_t b = static_cast<uint64_t>(c[2]) * 0xCD9E8D57u;
+    const uint32_t n0 = static_cast<uint32_t>(b >> 32) ^ c[1] ^ k0;
+    const uint32_t n2 = static_cast<uint32_t>(a >> 32) ^ c[3] ^ k1;
+    c[0] = n0;
+    c[1] = static_cast<uint32_t>(b);
+    c[2] = n2;
+    c[3] = static_cast<uint32_t>(a);
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+}
+
+// v[i] <- element 8 block8 + i of its row, dropped or scaled.  A dropped element is 0
+// whatever it held (Inf and NaN too).
+__device__ __forceinline__ void drop8(float (&v)[8], const Drop& d, long row, int cols, int block8) {
+  const uint64_t n = static_cast<uint64_t>(row) * static_cast<uint64_t>((cols + 7) >> 3) + static_cast<uint64_t>(block8);
+  uint32_t c[4] = {static_cast<uint32_t>(n), static_cast<uint32_t>(n >> 32), d.c2, d.c3};
+  philox_block(c, d.k0, d.k1);
+  OZ2_UNROLL
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t u = (i & 1) ? c[i >> 1] >> 16 : c[i >> 1] & 0xFFFFu;
+    v[i] = u >= d.t ? v[i] * d.scale : 0.0f;
+  }
+}
+
+// ---- epilogue ------------------------------------------------------------------------------
+// Eight accumulators of row m, columns n .. n + 7 (n a multiple of 8, n < cols).
+template <typename T>
+__device__ __forceinline__ void finish8(float (&v)[8], const Epilogue& e, long m, int n, int cols) {
+  const int valid = cols - n;
+  float t[8];
+  if (e.xs != nullptr) {
+    const float s = e.xs[m];
+    load8(e.ws + n, valid, t);
+    OZ2_UNROLL
+    for (int i = 0; i < 8; ++i) v[i] = v[i] * s * t[i];
+  }
+  if (e.bias != nullptr) {
+    load8(static_cast<const T*>(e.bias) + n, valid, t);
+    OZ2_UNROLL
+    for (int i = 0; i < 8; ++i) v[i] += t[i];
+  }
+  if (e.z != nullptr) store8(static_cast<T*>(e.z) + m * e.ldz + n, valid, v);
+  if (e.act != kActNone) {
+    OZ2_UNROLL
+    for (int i = 0; i < 8; ++i) v[i] = activate(v[i], e.act);
+  }
+  if (e.drop.t != 0) drop8(v, e.drop, m, cols, n >> 3);
+  if (e.res != nullptr) {
+    load8(static_cast<const T*>(e.res) + m * e.ldr + n, valid, t);
+    OZ2_UNROLL
+    for (int i = 0; i < 8; ++i) v[i] += t[i];
+  }
+  store8(static_cast<T*>(e.y) + m * e.ldy + n, valid, v);
+}
+
+}  // namespace oz2

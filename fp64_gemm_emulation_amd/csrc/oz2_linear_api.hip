@@ -1,0 +1,275 @@
+// oz2_linear_api.hip -- the linear-layer entry points declared in include/oz2.h: argument
+// checks, workspace layout and launches on the caller's stream.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "oz2.h"
+#include "oz2_internal.hpp"
+#include "oz2_linear.hpp"
+
+namespace {
+
+constexpr size_t kAlign = 256;
+constexpr long kMaxDim = 1L << 23;  // as for the FP64 products
+
+static_assert(OZ2_BF16 == oz2::kTypeBf16 && OZ2_F16 == oz2::kTypeF16 && OZ2_F32 == oz2::kTypeF32, "types");
+static_assert(OZ2_ACT_RELU == oz2::kActRelu && OZ2_ACT_GELU == oz2::kActGelu &&
+                  OZ2_ACT_GELU_TANH == oz2::kActGeluTanh && OZ2_ACT_SILU == oz2::kActSilu,
+              "activations");
+
+// One matrix argument: rows x cols elements, row stride ld.
+struct Mat {
+  const void* ptr;
+  long rows, cols, ld;
+  size_t elem;
+  bool empty() const { return ptr == nullptr || rows == 0 || cols == 0; }
+  size_t bytes() const { return elem * (static_cast<size_t>(ld) * (rows - 1) + cols); }
+};
+
+// Whether two matrices share an element: their address ranges meet, and, where their rows have
+// the same stride, so do the columns they take of it (two column ranges of one wide buffer are
+// apart although their address ranges interleave).
+bool overlap(const Mat& a, const Mat& b) {
+  if (a.empty() || b.empty()) return false;
+  const auto pa = reinterpret_cast<uintptr_t>(a.ptr), pb = reinterpret_cast<uintptr_t>(b.ptr);
+  if (pa >= pb + b.bytes() || pb >= pa + a.bytes()) return false;
+  const size_t pitch = a.elem * a.ld;
+  if (pitch != b.elem * b.ld) return true;
+  const size_t d = pb >= pa ? (pb - pa) % pitch : (pitch - (pa - pb) % pitch) % pitch;
+  return d < a.elem * a.cols || d + b.elem * b.cols > pitch;
+}
+
+bool same(const Mat& a, const Mat& b) { return a.ptr == b.ptr && a.ld == b.ld; }
+
+bool sizes_ok(int p, int q, int r) {
+  return p >= 0 && q >= 0 && r >= 0 && p <= kMaxDim && q <= kMaxDim && r <= kMaxDim;
+}
+
+bool ld_ok(const Mat& m) { return m.ptr == nullptr || m.ld >= std::max(1L, m.cols); }
+
+// One launch puts every 64 x 64 output tile along grid x (256 work-items each): that work-item
+// count has to stay in 32 bits.
+bool grid_ok(long rows, long cols) {
+  return static_cast<uint64_t>((rows + 63) / 64) * static_cast<uint64_t>((cols + 63) / 64) * 256u < (1ull << 32);
+}
+
+size_t elem_of(int type) { return type == OZ2_F32 ? 4 : 2; }
+
+bool drop_ok(const oz2_dropout_t* d) { return d == nullptr || (d->probability >= 0.0 && d->probability <= 1.0); }
+
+oz2::Drop make_drop(const oz2_dropout_t* d) {
+  oz2::Drop o;
+  if (d == nullptr) return o;
+  o.t = static_cast<uint32_t>(std::nearbyint(d->probability * 65536.0));
+  o.scale = o.t < 65536u ? 65536.0f / static_cast<float>(65536u - o.t) : 0.0f;
+  o.k0 = static_cast<uint32_t>(d->seed);
+  o.k1 = static_cast<uint32_t>(d->seed >> 32);
+  o.c2 = static_cast<uint32_t>(d->offset);
+  o.c3 = static_cast<uint32_t>(d->offset >> 32);
+  return o;
+}
+
+// Workspace: consecutive aligned pieces of `base` (null while only the size is asked for).
+struct Carver {
+  char* base = nullptr;
+  size_t used = 0;
+  void* take(size_t bytes) {
+    void* const p = base != nullptr ? base + used : nullptr;
+    used += (bytes + kAlign - 1) / kAlign * kAlign;
+    return p;
+  }
+};
+
+struct BwdWork {
+  void* dz;
+  float* part;
+};
+
+BwdWork carve_bwd(Carver& c, int type, long p, long r) {
+  BwdWork w;
+  w.dz = c.take(elem_of(type) * p * r);
+  w.part = static_cast<float*>(c.take(sizeof(float) * oz2::grad_row_blocks(static_cast<int>(p)) * r));
+  return w;
+}
+
+struct I8Work {
+  int8_t* q;
+  float* scale;
+};
+
+I8Work carve_i8(Carver& c, long p, long q) {
+  I8Work w;
+  w.q = static_cast<int8_t*>(c.take(p * q));
+  w.scale = static_cast<float*>(c.take(sizeof(float) * p));
+  return w;
+}
+
+// The call's workspace: the caller's if given, else the library's.
+int workspace(void* work, size_t work_bytes, size_t need, char** base) {
+  *base = static_cast<char*>(work);
+  if (need == 0) return OZ2_OK;
+  if (work == nullptr) return oz2::acquire_linear_workspace(need, base);
+  if (reinterpret_cast<uintptr_t>(work) % kAlign != 0) return OZ2_ERR_ARG;
+  return work_bytes < need ? OZ2_ERR_WORKSPACE : OZ2_OK;
+}
+
+int status(hipError_t e) { return e == hipSuccess ? OZ2_OK : OZ2_ERR_HIP; }
+
+}  // namespace
+
+extern "C" {
+
+int ozaki2_linear(int type, int p, int q, int r, const void* X, int ldx, const void* W, int ldw, const void* bias,
+                  int act, const oz2_dropout_t* dropout, const void* R, int ldr, void* Z, int ldz, void* Y, int ldy,
+                  void* work, size_t work_bytes, void* stream) {
+  if (type != OZ2_BF16 && type != OZ2_F16) return OZ2_ERR_ARG;
+  if (act < OZ2_ACT_NONE || act > OZ2_ACT_SILU || !drop_ok(dropout) || !sizes_ok(p, q, r)) return OZ2_ERR_ARG;
+  const size_t e = elem_of(type);
+  const Mat x{X, p, q, ldx, e}, w{W, r, q, ldw, e}, b{bias, 1, r, r, e}, res{R, p, r, ldr, e}, z{Z, p, r, ldz, e},
+      y{Y, p, r, ldy, e};
+  if (!ld_ok(x) || !ld_ok(w) || !ld_ok(res) || !ld_ok(z) || !ld_ok(y)) return OZ2_ERR_ARG;
+  if (p == 0 || r == 0) return OZ2_OK;
+  if (Y == nullptr || (q > 0 && (X == nullptr || W == nullptr))) return OZ2_ERR_ARG;
+  if (!grid_ok(p, r)) return OZ2_ERR_UNSUPPORTED;
+  if (overlap(y, x) || overlap(y, w) || overlap(y, b) || overlap(y, z) || (overlap(y, res) && !same(y, res))) return OZ2_ERR_ARG;
+  if (overlap(z, x) || overlap(z, w) || overlap(z, b) || overlap(z, res)) return OZ2_ERR_ARG;
+  (void)work;
+  (void)work_bytes;
+  oz2::Product pr{type, false, p, r, q, X, ldx, 1, W, ldw, 1, {}};
+  pr.epi.bias = bias;
+  pr.epi.act = act;
+  pr.epi.drop = make_drop(dropout);
+  pr.epi.res = R;
+  pr.epi.ldr = ldr;
+  pr.epi.z = Z;
+  pr.epi.ldz = ldz;
+  pr.epi.y = Y;
+  pr.epi.ldy = ldy;
+  return status(oz2::launch_product(pr, static_cast<hipStream_t>(stream)));
+}
+
+int ozaki2_linear_bwd(int type, int p, int q, int r, const void* dY, int lddy, const void* X, int ldx, const void* W,
+                      int ldw, const void* Z, int ldz, int act, const oz2_dropout_t* dropout, void* dX, int lddx,
+                      void* dW, int lddw, void* dbias, void* work, size_t work_bytes, void* stream) {
+  if (type != OZ2_BF16 && type != OZ2_F16) return OZ2_ERR_ARG;
+  if (act < OZ2_ACT_NONE || act > OZ2_ACT_SILU || !drop_ok(dropout) || !sizes_ok(p, q, r)) return OZ2_ERR_ARG;
+  const size_t e = elem_of(type);
+  const Mat dy{dY, p, r, lddy, e}, x{X, p, q, ldx, e}, w{W, r, q, ldw, e}, z{Z, p, r, ldz, e}, dx{dX, p, q, lddx, e},
+      dw{dW, r, q, lddw, e}, db{dbias, 1, r, r, e};
+  if (!ld_ok(dy) || !ld_ok(x) || !ld_ok(w) || !ld_ok(z) || !ld_ok(dx) || !ld_ok(dw)) return OZ2_ERR_ARG;
+  const bool want_dx = dX != nullptr && p > 0 && q > 0, want_dw = dW != nullptr && r > 0 && q > 0;
+  const bool want_db = dbias != nullptr && r > 0;
+  if (!want_dx && !want_dw && !want_db) return OZ2_OK;
+  if (p > 0 && r > 0) {
+    if (dY == nullptr || (act != OZ2_ACT_NONE && Z == nullptr)) return OZ2_ERR_ARG;
+    if ((want_dx && W == nullptr) || (want_dw && X == nullptr)) return OZ2_ERR_ARG;
+  }
+  if ((want_dx && !grid_ok(p, q)) || (want_dw && !grid_ok(r, q))) return OZ2_ERR_UNSUPPORTED;
+  const Mat* const outs[] = {&dx, &dw, &db};
+  const Mat* const ins[] = {&dy, &x, &w, &z};
+  for (const Mat* o : outs) {
+    for (const Mat* i : ins)
+      if (overlap(*o, *i)) return OZ2_ERR_ARG;
+    for (const Mat* o2 : outs)
+      if (o != o2 && overlap(*o, *o2)) return OZ2_ERR_ARG;
+  }
+  const size_t need = ozaki2_linear_workspace_size(OZ2_LINEAR_BWD, type, p, q, r);
+  Carver c;
+  int rc = workspace(work, work_bytes, need, &c.base);
+  if (rc != OZ2_OK) return rc;
+  const BwdWork ws = carve_bwd(c, type, p, r);
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  const oz2::Drop drop = make_drop(dropout);
+  // dZ is dY itself without activation and dropout
+  const bool make_dz = (act != OZ2_ACT_NONE || drop.t != 0) && (want_dx || want_dw);
+  if (make_dz || want_db) {
+    rc = status(oz2::launch_grad_rows(type, p, r, dY, lddy, Z, ldz, act, drop, make_dz ? ws.dz : nullptr, r,
+                                      want_db ? dbias : nullptr, ws.part, st));
+    if (rc != OZ2_OK) return rc;
+  }
+  const void* const dz = make_dz ? ws.dz : dY;
+  const long lddz = make_dz ? r : lddy;
+  if (want_dx) {
+    oz2::Product pr{type, false, p, q, r, dz, lddz, 1, W, 1, ldw, {}};
+    pr.epi.y = dX;
+    pr.epi.ldy = lddx;
+    if ((rc = status(oz2::launch_product(pr, st))) != OZ2_OK) return rc;
+  }
+  if (want_dw) {
+    oz2::Product pr{type, false, r, q, p, dz, 1, lddz, X, 1, ldx, {}};
+    pr.epi.y = dW;
+    pr.epi.ldy = lddw;
+    if ((rc = status(oz2::launch_product(pr, st))) != OZ2_OK) return rc;
+  }
+  return OZ2_OK;
+}
+
+int ozaki2_dropout_add(int type, int p, int r, const void* X, int ldx, const void* R, int ldr,
+                       const oz2_dropout_t* dropout, void* Y, int ldy, void* stream) {
+  if (type < OZ2_BF16 || type > OZ2_F32 || !drop_ok(dropout) || !sizes_ok(p, 0, r)) return OZ2_ERR_ARG;
+  const size_t e = elem_of(type);
+  const Mat x{X, p, r, ldx, e}, res{R, p, r, ldr, e}, y{Y, p, r, ldy, e};
+  if (!ld_ok(x) || !ld_ok(res) || !ld_ok(y)) return OZ2_ERR_ARG;
+  if (p == 0 || r == 0) return OZ2_OK;
+  if (X == nullptr || Y == nullptr) return OZ2_ERR_ARG;
+  if ((overlap(y, x) && !same(y, x)) || (overlap(y, res) && !same(y, res))) return OZ2_ERR_ARG;
+  return status(oz2::launch_dropout_add(type, p, r, X, ldx, R, ldr, make_drop(dropout), Y, ldy,
+                                        static_cast<hipStream_t>(stream)));
+}
+
+int ozaki2_quantize_rows(int type, int p, int q, const void* X, int ldx, int8_t* Q, int ldq, float* scale, void* stream) {
+  if (type < OZ2_BF16 || type > OZ2_F32 || !sizes_ok(p, q, 0)) return OZ2_ERR_ARG;
+  const Mat x{X, p, q, ldx, elem_of(type)}, out{Q, p, q, ldq, 1}, sc{scale, 1, p, p, sizeof(float)};
+  if (!ld_ok(x) || !ld_ok(out)) return OZ2_ERR_ARG;
+  if (p == 0) return OZ2_OK;
+  if (scale == nullptr || (q > 0 && (X == nullptr || Q == nullptr))) return OZ2_ERR_ARG;
+  if (overlap(out, x) || overlap(sc, x) || overlap(sc, out)) return OZ2_ERR_ARG;
+  return status(oz2::launch_quantize_rows(type, p, q, X, ldx, Q, ldq, scale, static_cast<hipStream_t>(stream)));
+}
+
+int ozaki2_linear_i8(int type, int p, int q, int r, const void* X, int ldx, const int8_t* V, int ldv, const float* t,
+                     const void* bias, int act, const void* R, int ldr, void* Y, int ldy, void* work,
+                     size_t work_bytes, void* stream) {
+  if (type != OZ2_BF16 && type != OZ2_F16) return OZ2_ERR_ARG;
+  if (act < OZ2_ACT_NONE || act > OZ2_ACT_SILU || !sizes_ok(p, q, r)) return OZ2_ERR_ARG;
+  const size_t e = elem_of(type);
+  const Mat x{X, p, q, ldx, e}, v{V, r, q, ldv, 1}, sc{t, 1, r, r, sizeof(float)}, b{bias, 1, r, r, e},
+      res{R, p, r, ldr, e}, y{Y, p, r, ldy, e};
+  if (!ld_ok(x) || !ld_ok(v) || !ld_ok(res) || !ld_ok(y)) return OZ2_ERR_ARG;
+  if (p == 0 || r == 0) return OZ2_OK;
+  if (q > OZ2_LINEAR_I8_MAX_Q || !grid_ok(p, r)) return OZ2_ERR_UNSUPPORTED;
+  if (Y == nullptr || t == nullptr || (q > 0 && (X == nullptr || V == nullptr))) return OZ2_ERR_ARG;
+  if (overlap(y, x) || overlap(y, v) || overlap(y, sc) || overlap(y, b) || (overlap(y, res) && !same(y, res))) return OZ2_ERR_ARG;
+  const size_t need = ozaki2_linear_workspace_size(OZ2_LINEAR_I8, type, p, q, r);
+  Carver c;
+  int rc = workspace(work, work_bytes, need, &c.base);
+  if (rc != OZ2_OK) return rc;
+  const I8Work ws = carve_i8(c, p, q);
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  if ((rc = status(oz2::launch_quantize_rows(type, p, q, X, ldx, ws.q, q, ws.scale, st))) != OZ2_OK) return rc;
+  oz2::Product pr{type, true, p, r, q, ws.q, q, 1, V, ldv, 1, {}};
+  pr.epi.bias = bias;
+  pr.epi.act = act;
+  pr.epi.res = R;
+  pr.epi.ldr = ldr;
+  pr.epi.y = Y;
+  pr.epi.ldy = ldy;
+  pr.epi.xs = ws.scale;
+  pr.epi.ws = t;
+  return status(oz2::launch_product(pr, st));
+}
+
+size_t ozaki2_linear_workspace_size(int call, int type, int p, int q, int r) {
+  if ((type != OZ2_BF16 && type != OZ2_F16) || !sizes_ok(p, q, r)) return 0;
+  Carver c;
+  if (call == OZ2_LINEAR_BWD)
+    carve_bwd(c, type, p, r);
+  else if (call == OZ2_LINEAR_I8)
+    carve_i8(c, p, q);
+  return c.used;
+}
+
+}  // extern "C"

@@ -1,0 +1,173 @@
+// oz2_linear_rows.hip -- the row-wise passes around the linear-layer products: dropout with
+// residual, the gradient before the products with its column sums, and the quantisation of
+// rows to int8.
+#include "oz2_common.hpp"
+#include "oz2_linear.hpp"
+
+namespace oz2 {
+
+// y = res + drop(x): one thread per eight consecutive elements of a row, so one generator
+// block per thread.  A workgroup covers cx column groups (a power of two) of 256 / cx rows.
+template <typename T>
+__global__ __launch_bounds__(256) void dropout_add_kernel(int p, int r, int cx_log2, const T* x, long ldx, const T* res,
+                                                          long ldr, Drop d, T* y, long ldy) {
+  const int b = (blockIdx.x << cx_log2) + (threadIdx.x & ((1 << cx_log2) - 1));
+  const int valid = r - 8 * b;
+  if (valid <= 0) return;
+  const int ry = 256 >> cx_log2;
+  for (long row = static_cast<long>(blockIdx.y) * ry + (threadIdx.x >> cx_log2); row < p;
+       row += static_cast<long>(gridDim.y) * ry) {
+    float v[8], t[8];
+    load8(x + row * ldx + 8 * b, valid, v);
+    if (d.t != 0) drop8(v, d, row, r, b);
+    if (res != nullptr) {
+      load8(res + row * ldr + 8 * b, valid, t);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] += t[i];
+    }
+    store8(y + row * ldy + 8 * b, valid, v);
+  }
+}
+
+template <typename T>
+static hipError_t dropout_add(int p, int r, const void* x, long ldx, const void* res, long ldr, const Drop& d, void* y,
+                              long ldy, hipStream_t st) {
+  const int groups = (r + 7) >> 3;
+  int cx_log2 = 0;
+  while (cx_log2 < 8 && (1 << cx_log2) < groups) ++cx_log2;
+  const int ry = 256 >> cx_log2;
+  const long row_blocks = (static_cast<long>(p) + ry - 1) / ry;
+  const dim3 grid((groups + (1 << cx_log2) - 1) >> cx_log2, static_cast<unsigned>(row_blocks < 65535 ? row_blocks : 65535));
+  hipLaunchKernelGGL(dropout_add_kernel<T>, grid, dim3(256), 0, st, p, r, cx_log2, static_cast<const T*>(x), ldx,
+                     static_cast<const T*>(res), ldr, d, static_cast<T*>(y), ldy);
+  return hipGetLastError();
+}
+
+hipError_t launch_dropout_add(int type, int p, int r, const void* x, long ldx, const void* res, long ldr,
+                              const Drop& drop, void* y, long ldy, hipStream_t st) {
+  if (type == kTypeBf16) return dropout_add<bf16>(p, r, x, ldx, res, ldr, drop, y, ldy, st);
+  if (type == kTypeF16) return dropout_add<f16>(p, r, x, ldx, res, ldr, drop, y, ldy, st);
+  return dropout_add<float>(p, r, x, ldx, res, ldr, drop, y, ldy, st);
+}
+
+// dz = drop(dy) act'(z): a workgroup takes kGradRows rows of 256 columns, a thread eight
+// consecutive columns of every eighth row.  Column sums are of the unrounded f32 values, in
+// a fixed order: over the thread's rows, over the eight threads of a column group, and (in
+// column_sums_kernel) over the row blocks.
+constexpr int kGradRows = 64;
+constexpr int kGradCols = 256;
+
+int grad_row_blocks(int p) { return (p + kGradRows - 1) / kGradRows; }
+
+template <typename T>
+__global__ __launch_bounds__(256) void grad_rows_kernel(int p, int r, const T* dy, long lddy, const T* z, long ldz,
+                                                        int act, Drop d, T* dz, long lddz, float* part) {
+  __shared__ float sums[8][kGradCols];
+  const int g = threadIdx.x & 31, rr = threadIdx.x >> 5;
+  const int col = blockIdx.y * kGradCols + 8 * g;
+  const int valid = r - col;
+  const long row0 = static_cast<long>(blockIdx.x) * kGradRows;
+  float sum[8] = {};
+  if (valid > 0) {
+    for (long row = row0 + rr; row < min(row0 + kGradRows, static_cast<long>(p)); row += 8) {
+      float v[8], t[8];
+      load8(dy + row * lddy + col, valid, v);
+      if (d.t != 0) drop8(v, d, row, r, col >> 3);
+      if (act != kActNone) {
+        load8(z + row * ldz + col, valid, t);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= activation_slope(t[i], act);
+      }
+      if (dz != nullptr) store8(dz + row * lddz + col, valid, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[i] += v[i];
+    }
+  }
+  if (part == nullptr) return;  // uniform over the launch
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sums[rr][8 * g + i] = sum[i];
+  __syncthreads();
+  const int c = blockIdx.y * kGradCols + threadIdx.x;
+  float s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s += sums[i][threadIdx.x];
+  if (c < r) part[static_cast<long>(blockIdx.x) * r + c] = s;
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void column_sums_kernel(int blocks, int r, const float* part, T* db) {
+  const int c = blockIdx.x * 256 + threadIdx.x;
+  if (c >= r) return;
+  float s = 0.0f;
+  for (int b = 0; b < blocks; ++b) s += part[static_cast<long>(b) * r + c];
+  db[c] = static_cast<T>(s);
+}
+
+template <typename T>
+static hipError_t grad_rows(int p, int r, const void* dy, long lddy, const void* z, long ldz, int act, const Drop& d,
+                            void* dz, long lddz, void* db, float* part, hipStream_t st) {
+  const dim3 grid(grad_row_blocks(p), (r + kGradCols - 1) / kGradCols);
+  if (p > 0 && r > 0) {  // without rows the column sums are zeros
+    hipLaunchKernelGGL(grad_rows_kernel<T>, grid, dim3(256), 0, st, p, r, static_cast<const T*>(dy), lddy,
+                       static_cast<const T*>(z), ldz, act, d, static_cast<T*>(dz), lddz, db != nullptr ? part : nullptr);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+  }
+  if (db == nullptr) return hipSuccess;
+  hipLaunchKernelGGL(column_sums_kernel<T>, dim3((r + 255) / 256), dim3(256), 0, st, grad_row_blocks(p), r, part,
+                     static_cast<T*>(db));
+  return hipGetLastError();
+}
+
+hipError_t launch_grad_rows(int type, int p, int r, const void* dy, long lddy, const void* z, long ldz, int act,
+                            const Drop& drop, void* dz, long lddz, void* db, float* part, hipStream_t st) {
+  if (type == kTypeBf16) return grad_rows<bf16>(p, r, dy, lddy, z, ldz, act, drop, dz, lddz, db, part, st);
+  return grad_rows<f16>(p, r, dy, lddy, z, ldz, act, drop, dz, lddz, db, part, st);
+}
+
+// Row quantisation: scale = max|x| / 127, q = rint(x (127 / max|x|)); a row whose
+// largest magnitude is below kTinyRow (127 / it would overflow) is taken for zeros, with scale
+// 0, and one that holds Inf or NaN gets the scale NaN, so its products are NaN.  One
+// workgroup per row.
+constexpr float kTinyRow = 1e-36f;
+
+template <typename T>
+__global__ __launch_bounds__(256) void quantize_rows_kernel(int q, const T* x, long ldx, int8_t* out, long ldo, float* scale) {
+  __shared__ float tops[4];
+  const long row = blockIdx.x;
+  const T* const src = x + row * ldx;
+  float top = 0.0f;
+  bool bad = false;
+  for (int k = threadIdx.x; k < q; k += 256) {
+    const float a = fabsf(static_cast<float>(src[k]));
+    bad = bad || a != a;
+    top = fmaxf(top, a);
+  }
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, kWave));
+  if (__any(bad)) top = __builtin_inff();
+  if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
+  __syncthreads();
+  top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+  const bool finite = top <= 3.4028234e38f;
+  const float inv = top >= kTinyRow && finite ? 127.0f / top : 0.0f;
+  for (int k = threadIdx.x; k < q; k += 256) {
+    const float v = rintf(static_cast<float>(src[k]) * inv);
+    out[row * ldo + k] = static_cast<int8_t>(finite ? static_cast<int>(v) : 0);
+  }
+  if (threadIdx.x == 0) scale[row] = inv == 0.0f && finite ? 0.0f : finite ? top / 127.0f : __builtin_nanf("");
+}
+
+hipError_t launch_quantize_rows(int type, int p, int q, const void* x, long ldx, int8_t* out, long ldo, float* scale,
+                                hipStream_t st) {
+  const dim3 grid(static_cast<unsigned>(p));
+  if (type == kTypeBf16)
+    hipLaunchKernelGGL(quantize_rows_kernel<bf16>, grid, dim3(256), 0, st, q, static_cast<const bf16*>(x), ldx, out, ldo, scale);
+  else if (type == kTypeF16)
+    hipLaunchKernelGGL(quantize_rows_kernel<f16>, grid, dim3(256), 0, st, q, static_cast<const f16*>(x), ldx, out, ldo, scale);
+  else
+    hipLaunchKernelGGL(quantize_rows_kernel<float>, grid, dim3(256), 0, st, q, static_cast<const float*>(x), ldx, out, ldo, scale);
+  return hipGetLastError();
+}
+
+}  // namespace oz2

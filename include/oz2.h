@@ -221,6 +221,116 @@ int ozaki2_get_flags(unsigned* flags);
 int ozaki2_moduli(int s, int* out);
 int ozaki2_tau(int s);
 
+/* ------------------------------------------------------------------------------------------
+ * Linear layers in 16 and 8 bits: products with the whole epilogue of a model's layer in them,
+ * their gradients, and counter-based dropout, on the same matrix cores.
+ *
+ * Conventions of this section, beside those above (device pointers, `stream`, asynchronous,
+ * arguments checked before anything is launched, status codes):
+ *   - Matrices are ROW-major, one token per row: element (i, k) of X is X[i * ldx + k], with
+ *     ldx >= the row's length (at least 1).  The letters are those of the FP64 products: X is
+ *     p x q (p tokens), W is r x q (one row per output feature), Y is p x r.
+ *   - Any sizes, leading dimensions and element-aligned pointers are accepted; rows that start
+ *     on 16-byte boundaries (and q a multiple of 16 bytes) are read fastest.
+ *   - Sums are held in 32 bits (f32; int32, exact, for int8 operands) and each result is
+ *     rounded once to its type, to nearest even.  Calls are deterministic: the same arguments
+ *     give the same bits.
+ *   - Outputs must not share elements with inputs or with each other, except that Y may be the
+ *     residual R itself (same pointer and leading dimension), and dropout_add's Y also X.
+ *   - `work` / `work_bytes`: scratch of at least ozaki2_linear_workspace_size bytes, 256-byte
+ *     aligned, whose contents do not matter and that nothing else uses until the call's work
+ *     is done.  NULL uses the buffer of ozaki2_set_workspace, beyond its first 256 bytes, else
+ *     one that the library owns (per device, apart from the dgemm calls', freed by
+ *     ozaki2_release); calls on different streams that share one must be ordered by the caller.
+ *     With a caller's `work`, or once the library's buffer has its size, calls enqueue kernels
+ *     only and can be captured in a HIP graph.
+ */
+
+/* Element types of the linear-layer calls. */
+typedef enum {
+  OZ2_BF16 = 0,
+  OZ2_F16 = 1,
+  OZ2_F32 = 2 /* ozaki2_dropout_add and ozaki2_quantize_rows only */
+} oz2_type_t;
+
+/* Activations.  gelu(a) = a Phi(a) with the normal distribution function Phi; gelu_tanh(a) =
+ * a / 2 (1 + tanh(sqrt(2 / pi) (a + 0.044715 a^3))); silu(a) = a / (1 + exp(-a)). */
+typedef enum {
+  OZ2_ACT_NONE = 0,
+  OZ2_ACT_RELU = 1,
+  OZ2_ACT_GELU = 2,
+  OZ2_ACT_GELU_TANH = 3,
+  OZ2_ACT_SILU = 4
+} oz2_act_t;
+
+/* Dropout D of a matrix with r columns, from a counter-based generator (Philox4x32-10: Salmon,
+ * Moraes, Dror, Shaw, "Parallel random numbers: as easy as 1, 2, 3", 2011).  The mask is a
+ * function of (seed, offset, row, column, r) and is never stored: the forward and the backward
+ * call compute it anew.  Element (i, j) draws u, the 16-bit lane j % 8 (low half of word 0
+ * first) of the block with the 128-bit counter (i ceil(r / 8) + j / 8, offset), low 64 bits
+ * first, and the key seed.  With T = rint(2^16 probability) it becomes x 2^16 / (2^16 - T) if
+ * u >= T, and 0, whatever x holds, if not.  A probability that rounds to T = 2^16 drops all. */
+typedef struct oz2_dropout {
+  double probability; /* in [0, 1] */
+  uint64_t seed;
+  uint64_t offset; /* another mask for each: advance it from step to step and layer to layer */
+} oz2_dropout_t;
+
+/*
+ * ozaki2_linear -- Y = R + D(act(A)), A = X W^T + bias, one product with its whole epilogue.
+ *   type    : OZ2_BF16 or OZ2_F16, of X, W, bias, R, Z and Y.
+ *   bias    : r elements, or NULL.         act : oz2_act_t.
+ *   dropout : D, or NULL for none.         R   : p x r, or NULL.
+ *   Z       : NULL, or p x r that receives A (rounded), which ozaki2_linear_bwd needs when
+ *             act is not OZ2_ACT_NONE.  The activation is of the unrounded A.
+ * p == 0 or r == 0 is a no-op; q == 0 makes A = bias.
+ */
+int ozaki2_linear(int type, int p, int q, int r, const void* X, int ldx, const void* W, int ldw, const void* bias,
+                  int act, const oz2_dropout_t* dropout, const void* R, int ldr, void* Z, int ldz, void* Y, int ldy,
+                  void* work, size_t work_bytes, void* stream);
+
+/*
+ * ozaki2_linear_bwd -- gradients of ozaki2_linear from dY (p x r):
+ *   dZ = D(dY) act'(Z),   dX = dZ W,   dW = dZ^T X,   dbias = column sums of dZ
+ * (the residual's gradient is dY itself).  Outputs that are NULL are not computed; X is needed
+ * for dW only, W for dX only, Z only when act is not OZ2_ACT_NONE; `dropout` has to be the
+ * forward call's.  dZ is rounded to `type` before the two products, which is what feeds the
+ * matrix cores; dbias sums the unrounded values.  Empty sizes give zero gradients.
+ */
+int ozaki2_linear_bwd(int type, int p, int q, int r, const void* dY, int lddy, const void* X, int ldx, const void* W,
+                      int ldw, const void* Z, int ldz, int act, const oz2_dropout_t* dropout, void* dX, int lddx,
+                      void* dW, int lddw, void* dbias, void* work, size_t work_bytes, void* stream);
+
+/* ozaki2_dropout_add -- Y = R + D(X) (R may be NULL, `dropout` NULL or any), type OZ2_BF16,
+ * OZ2_F16 or OZ2_F32.  The gradient with respect to X is the same call on dY without R. */
+int ozaki2_dropout_add(int type, int p, int r, const void* X, int ldx, const void* R, int ldr,
+                       const oz2_dropout_t* dropout, void* Y, int ldy, void* stream);
+
+/* ozaki2_quantize_rows -- each row of X (p x q) to int8 and an f32 scale: with m the row's
+ * largest magnitude, Q = rint(x (127 / m)) and scale = m / 127, so x ~ Q scale.  A row with
+ * m < 1e-36 gives zeros and scale 0; one that holds Inf or NaN gives zeros and scale NaN. */
+int ozaki2_quantize_rows(int type, int p, int q, const void* X, int ldx, int8_t* Q, int ldq, float* scale, void* stream);
+
+/* Largest q of ozaki2_linear_i8: 127^2 q stays below 2^31. */
+#define OZ2_LINEAR_I8_MAX_Q 131072
+/*
+ * ozaki2_linear_i8 -- Y = R + act(A), A_ij = s_i t_j (Q V^T)_ij + bias_j, for serving with int8
+ * weights: V (r x q) and its row scales t (r floats, both as ozaki2_quantize_rows makes them
+ * from W) are given; the rows of X are quantised to Q, s in the call by the same rule.  The
+ * int8 products are summed exactly in int32.  Other arguments as in ozaki2_linear.
+ * q > OZ2_LINEAR_I8_MAX_Q gives OZ2_ERR_UNSUPPORTED.
+ */
+int ozaki2_linear_i8(int type, int p, int q, int r, const void* X, int ldx, const int8_t* V, int ldv, const float* t,
+                     const void* bias, int act, const void* R, int ldr, void* Y, int ldy, void* work,
+                     size_t work_bytes, void* stream);
+
+/* The calls ozaki2_linear_workspace_size answers for. */
+typedef enum { OZ2_LINEAR_FWD = 0, OZ2_LINEAR_BWD = 1, OZ2_LINEAR_I8 = 2 } oz2_linear_call_t;
+
+/* Bytes of workspace the call needs for these sizes, whatever its other arguments (0 for
+ * invalid arguments, no work, or none needed). */
+size_t ozaki2_linear_workspace_size(int call, int type, int p, int q, int r);
+
 /* Static description of a status code. */
 const char* ozaki2_status_string(int status);
 
