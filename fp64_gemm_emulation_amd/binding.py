@@ -25,7 +25,7 @@ OZ2_NOALLOC_SCRATCH_BYTES = 256 << 20
 MODES = {"fast": OZ2_FAST, "accu": OZ2_ACCU}
 OZ2_BF16, OZ2_F16, OZ2_F32 = 0, 1, 2
 OZ2_ACT_NONE, OZ2_ACT_RELU, OZ2_ACT_GELU, OZ2_ACT_GELU_TANH, OZ2_ACT_SILU = 0, 1, 2, 3, 4
-OZ2_LINEAR_FWD, OZ2_LINEAR_BWD, OZ2_LINEAR_I8 = 0, 1, 2
+OZ2_LINEAR_FWD, OZ2_LINEAR_BWD, OZ2_LINEAR_I8, OZ2_LINEAR_ALIGNED = 0, 1, 2, 16
 OZ2_LINEAR_I8_MAX_Q = 131072
 ACTIVATIONS = {"none": OZ2_ACT_NONE, "relu": OZ2_ACT_RELU, "gelu": OZ2_ACT_GELU, "gelu_tanh": OZ2_ACT_GELU_TANH,
                "silu": OZ2_ACT_SILU}
@@ -411,6 +411,13 @@ class _Call:
         return torch.empty(nbytes, dtype=torch.uint8, device=self._dev)
 
 
+def _aligned(len_bytes, *rows):
+    """OZ2_LINEAR_ALIGNED if every (pointer, row stride in bytes) of rows of len_bytes bytes is."""
+    if len_bytes % 16 == 0 and all(p is None or (p % 16 == 0 and ld % 16 == 0 and ld < 1 << 24) for p, ld in rows):
+        return OZ2_LINEAR_ALIGNED
+    return 0
+
+
 def _ptr(t):
     return t.data_ptr() if t is not None else None
 
@@ -443,7 +450,7 @@ def linear(x, w, bias=None, activation: str = "none", residual=None, dropout: fl
         y = out if out is not None else torch.empty((p, r), dtype=x.dtype, device=x.device)
         py, ldy = _rows(y, "out", (p, r), x)
         z = torch.empty((p, r), dtype=x.dtype, device=x.device) if return_z else None
-        work = call.scratch(_LIB.ozaki2_linear_workspace_size(OZ2_LINEAR_FWD, kind, p, q, r))
+        work = call.scratch(_LIB.ozaki2_linear_workspace_size(OZ2_LINEAR_FWD | _aligned(2 * q, (px, 2 * ldx), (pw, 2 * ldw)), kind, p, q, r))
         rc = ozaki2_linear(kind, p, q, r, px, ldx, pw, ldw, pb, act, drop, pr, ldr, _ptr(z), max(1, r), py, ldy,
                            _ptr(work), work.numel() if work is not None else 0, call.raw)
     _check(rc, "ozaki2_linear")
@@ -471,7 +478,7 @@ def linear_backward(dy, x, w, z=None, activation: str = "none", dropout: float =
         pz, ldz = _rows(z, "z", (p, r), dy)
         new = lambda name, *shape: torch.empty(shape, dtype=dy.dtype, device=dy.device) if name in needs else None  # noqa: E731
         dx, dw, db = new("x", p, q), new("w", r, q), new("bias", r)
-        work = call.scratch(_LIB.ozaki2_linear_workspace_size(OZ2_LINEAR_BWD, kind, p, q, r))
+        work = call.scratch(_LIB.ozaki2_linear_workspace_size(OZ2_LINEAR_BWD | _aligned(2 * q, (px, 2 * ldx), (pw, 2 * ldw)), kind, p, q, r))
         rc = ozaki2_linear_bwd(kind, p, q, r, pdy, lddy, px, ldx, pw, ldw, pz, ldz, act, drop, _ptr(dx), max(1, q),
                                _ptr(dw), max(1, q), _ptr(db), _ptr(work), work.numel() if work is not None else 0,
                                call.raw)
@@ -527,7 +534,7 @@ def linear_i8(x, v, t, bias=None, activation: str = "none", residual=None, out=N
         pb = _vector(bias, "bias", r, x)
         y = out if out is not None else torch.empty((p, r), dtype=x.dtype, device=x.device)
         py, ldy = _rows(y, "out", (p, r), x)
-        work = call.scratch(_LIB.ozaki2_linear_workspace_size(OZ2_LINEAR_I8, kind, p, q, r))
+        work = call.scratch(_LIB.ozaki2_linear_workspace_size(OZ2_LINEAR_I8 | _aligned(q, (pv, ldv)), kind, p, q, r))
         rc = ozaki2_linear_i8(kind, p, q, r, px, ldx, pv, ldv, pt, pb, act, pr, ldr, py, ldy, _ptr(work),
                               work.numel() if work is not None else 0, call.raw)
     _check(rc, "ozaki2_linear_i8")

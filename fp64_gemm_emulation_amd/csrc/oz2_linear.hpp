@@ -39,29 +39,44 @@ struct Epilogue {
   const float* ws = nullptr;  //               and of each row of the right one
 };
 
-// out[m][n] = sum_k left[m][k] right[n][k], m < rows, n < cols, k < depth; element (i, k) of
-// an operand is at ptr[i * row + k * step].
+// out[m][n] = epilogue(sum_k left(m, k) right(n, k)), m < rows, n < cols, k < depth.  An operand
+// lies along the depth (element (i, k) at i * ld + k) or along its index (at k * ld + i; products
+// without an epilogue only).  Rows must be as rows_aligned says.
 struct Product {
   int type;   // element type of operands (unless int8) and outputs
   bool i8;    // int8 operands
   int rows, cols, depth;
   const void* left;
-  long left_row, left_step;
+  long left_ld;
+  bool left_along_index;
   const void* right;
-  long right_row, right_step;
+  long right_ld;
+  bool right_along_index;
   Epilogue epi;
 };
+
+// Whether the product kernels can take an operand as it lies: every row starts on a 16-byte
+// boundary and is a multiple of 16 bytes long, and 256 rows stay within 32-bit offsets.
+inline bool rows_aligned(const void* ptr, long ld, long len, int elem) {
+  return reinterpret_cast<uintptr_t>(ptr) % 16 == 0 && ld * elem % 16 == 0 && len * elem % 16 == 0 &&
+         ld * elem < (1L << 24);
+}
+// Row stride of a packed copy: a multiple of 16 bytes.
+inline long packed_ld(long len, int elem) { return (len * elem + 15) / 16 * 16 / elem; }
+hipError_t launch_pack_rows(int elem, long rows, int cols, const void* src, long ld, void* dst, long ld_out, hipStream_t st);
 
 hipError_t launch_product(const Product& pr, hipStream_t st);
 hipError_t launch_dropout_add(int type, int p, int r, const void* x, long ldx, const void* res, long ldr,
                               const Drop& drop, void* y, long ldy, hipStream_t st);
-// dz = drop(dy) act'(z) in the operands' type (skipped when dz is null) and, when db is not
+// dz = drop(dy) act'(z) in the operands' type, its rows padded with zeros to a multiple of 8
+// (skipped when dz is null), and, when db is not
 // null, db = its column sums, by way of part: grad_row_blocks(p) x r floats.
 int grad_row_blocks(int p);
 hipError_t launch_grad_rows(int type, int p, int r, const void* dy, long lddy, const void* z, long ldz, int act,
                             const Drop& drop, void* dz, long lddz, void* db, float* part, hipStream_t st);
-hipError_t launch_quantize_rows(int type, int p, int q, const void* x, long ldx, int8_t* out, long ldo, float* scale,
-                                hipStream_t st);
+// columns q .. fill - 1 of out are set to zero
+hipError_t launch_quantize_rows(int type, int p, int q, const void* x, long ldx, int8_t* out, long ldo, int fill,
+                                float* scale, hipStream_t st);
 
 #ifdef __HIP_DEVICE_COMPILE__
 #define OZ2_UNROLL _Pragma("unroll")
@@ -102,44 +117,61 @@ __device__ __forceinline__ void store8(T* p, int valid, const float (&v)[8]) {
 // ---- activations -----------------------------------------------------------------------
 // gelu(a) = a Phi(a), Phi the normal distribution function; gelu_tanh is its tanh form,
 // a sigmoid(2 c (a + k a^3)) with c = sqrt(2 / pi), k = 0.044715; silu(a) = a sigmoid(a).
-constexpr float kSqrtHalf = 0.70710678118654752f;
-constexpr float kInvSqrt2Pi = 0.39894228040143268f;
-constexpr float kGelu2C = 1.5957691216057308f;  // 2 sqrt(2 / pi)
-constexpr float kGeluK = 0.044715f;
+// In a product's epilogue these are work that the matrix cores wait for, so they are built
+// from the hardware's exponential and reciprocal (each within 2^-23, relative).
+__device__ __forceinline__ float exp_fast(float v) { return __builtin_amdgcn_exp2f(v * 1.4426950408889634f); }
+__device__ __forceinline__ float sigmoid(float v) { return __builtin_amdgcn_rcpf(1.0f + exp_fast(-v)); }
+__device__ __forceinline__ float sigmoid_gelu_tanh(float a) {
+  return sigmoid(a * __builtin_fmaf(1.5957691216057308f * 0.044715f, a * a, 1.5957691216057308f));
+}
 
-__device__ __forceinline__ float sigmoid(float v) { return 1.0f / (1.0f + expf(-v)); }
+// Phi(-|a|) = erfc(|a| / sqrt 2) / 2 and e = exp(-a^2 / 2), by formula 7.1.26 of Abramowitz and
+// Stegun, "Handbook of Mathematical Functions" (a fifth-degree polynomial in
+// 1 / (1 + 0.3275911 x) times exp(-x^2), within 1.5e-7): a third of the instructions of erff.
+__device__ __forceinline__ float normal_tail(float a, float& e) {
+  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3275911f * 0.70710678118654752f, fabsf(a), 1.0f));
+  float p = __builtin_fmaf(t, 0.5f * 1.061405429f, 0.5f * -1.453152027f);
+  p = __builtin_fmaf(t, p, 0.5f * 1.421413741f);
+  p = __builtin_fmaf(t, p, 0.5f * -0.284496736f);
+  p = __builtin_fmaf(t, p, 0.5f * 0.254829592f);
+  e = exp_fast(-0.5f * a * a);
+  return t * p * e;
+}
 
-__device__ __forceinline__ float activate(float a, int act) {
-  switch (act) {
-    case kActRelu:
-      return a <= 0.0f ? 0.0f : a;  // NaN stays NaN
-    case kActGelu:
-      return 0.5f * a * (1.0f + erff(a * kSqrtHalf));
-    case kActGeluTanh:
-      return a * sigmoid(kGelu2C * (a + kGeluK * a * a * a));
-    case kActSilu:
-      return a * sigmoid(a);
-    default:
-      return a;
+template <int ACT>
+__device__ __forceinline__ float activate(float a) {
+  if constexpr (ACT == kActRelu) {
+    return a <= 0.0f ? 0.0f : a;  // NaN stays NaN
+  } else if constexpr (ACT == kActGelu) {
+    // max(a, 0) - |a| Phi(-|a|); the minimum keeps +Inf from meeting its factor 0
+    float e;
+    const float h = normal_tail(a, e);
+    return __builtin_fmaf(-fabsf(fminf(a, 65536.0f)), h, fmaxf(a, 0.0f));
+  } else if constexpr (ACT == kActGeluTanh) {
+    return a * sigmoid_gelu_tanh(a);
+  } else if constexpr (ACT == kActSilu) {
+    return a * sigmoid(a);
+  } else {
+    return a;
   }
 }
 
-__device__ __forceinline__ float activation_slope(float z, int act) {
-  switch (act) {
-    case kActRelu:
-      return z > 0.0f ? 1.0f : 0.0f;
-    case kActGelu:
-      return 0.5f * (1.0f + erff(z * kSqrtHalf)) + z * kInvSqrt2Pi * expf(-0.5f * z * z);
-    case kActGeluTanh: {
-      const float s = sigmoid(kGelu2C * (z + kGeluK * z * z * z));
-      return s + z * s * (1.0f - s) * kGelu2C * (1.0f + 3.0f * kGeluK * z * z);
-    }
-    case kActSilu: {
-      const float s = sigmoid(z);
-      return s * (1.0f + z * (1.0f - s));
-    }
-    default:
-      return 1.0f;
+template <int ACT>
+__device__ __forceinline__ float activation_slope(float z) {
+  if constexpr (ACT == kActRelu) {
+    return z > 0.0f ? 1.0f : 0.0f;
+  } else if constexpr (ACT == kActGelu) {
+    float e;
+    const float h = normal_tail(z, e);
+    return __builtin_fmaf(z * 0.39894228040143268f, e, z > 0.0f ? 1.0f - h : h);
+  } else if constexpr (ACT == kActGeluTanh) {
+    const float s = sigmoid_gelu_tanh(z);
+    return s + z * s * (1.0f - s) * 1.5957691216057308f * __builtin_fmaf(3.0f * 0.044715f, z * z, 1.0f);
+  } else if constexpr (ACT == kActSilu) {
+    const float s = sigmoid(z);
+    return s * (1.0f + z * (1.0f - s));
+  } else {
+    return 1.0f;
   }
 }
 
@@ -150,6 +182,9 @@ __device__ __forceinline__ float activation_slope(float z, int act) {
 // expectation is exact; two blocks of 32-bit draws would double the generator's cost, which
 // is what bounds it (20 full-width multiplies at a quarter of the vector rate per block).
 __host__ __device__ __forceinline__ void philox_block(uint32_t (&c)[4], uint32_t k0, uint32_t k1) {
+  // a loop: unrolled into every eight outputs of an epilogue, the rounds alone outgrow the
+  // instruction cache
+#pragma unroll 1
   for (int i = 0; i < 10; ++i) {
     const uint64_t a = static_cast<uint64_t>(c[0]) * 0xD2511F53u;
     const uint64_t b = static_cast<uint64_t>(c[2]) * 0xCD9E8D57u;
@@ -178,10 +213,11 @@ __device__ __forceinline__ void drop8(float (&v)[8], const Drop& d, long row, in
 }
 
 // ---- epilogue ------------------------------------------------------------------------------
-// Eight accumulators of row m, columns n .. n + 7 (n a multiple of 8, n < cols).
-template <typename T>
+// Eight accumulators of row m, columns n .. n + 7 (n a multiple of 8, n < cols).  FULL: the
+// columns are a multiple of 8, so no group is cut (a quarter of the code).
+template <typename T, int ACT, bool FULL>
 __device__ __forceinline__ void finish8(float (&v)[8], const Epilogue& e, long m, int n, int cols) {
-  const int valid = cols - n;
+  const int valid = FULL ? 8 : cols - n;
   float t[8];
   if (e.xs != nullptr) {
     const float s = e.xs[m];
@@ -195,9 +231,9 @@ __device__ __forceinline__ void finish8(float (&v)[8], const Epilogue& e, long m
     for (int i = 0; i < 8; ++i) v[i] += t[i];
   }
   if (e.z != nullptr) store8(static_cast<T*>(e.z) + m * e.ldz + n, valid, v);
-  if (e.act != kActNone) {
+  if constexpr (ACT != kActNone) {
     OZ2_UNROLL
-    for (int i = 0; i < 8; ++i) v[i] = activate(v[i], e.act);
+    for (int i = 0; i < 8; ++i) v[i] = activate<ACT>(v[i]);
   }
   if (e.drop.t != 0) drop8(v, e.drop, m, cols, n >> 3);
   if (e.res != nullptr) {

@@ -50,10 +50,10 @@ bool sizes_ok(int p, int q, int r) {
 
 bool ld_ok(const Mat& m) { return m.ptr == nullptr || m.ld >= std::max(1L, m.cols); }
 
-// One launch puts every 64 x 64 output tile along grid x (256 work-items each): that work-item
+// One launch puts every 128 x 128 output tile along grid x (256 work-items each): that work-item
 // count has to stay in 32 bits.
 bool grid_ok(long rows, long cols) {
-  return static_cast<uint64_t>((rows + 63) / 64) * static_cast<uint64_t>((cols + 63) / 64) * 256u < (1ull << 32);
+  return static_cast<uint64_t>((rows + 127) / 128) * static_cast<uint64_t>((cols + 127) / 128) * 256u < (1ull << 32);
 }
 
 size_t elem_of(int type) { return type == OZ2_F32 ? 4 : 2; }
@@ -83,27 +83,42 @@ struct Carver {
   }
 };
 
+// The workspace of each call: copies of operands that need packing, and what it makes itself.
+struct FwdWork {
+  void *x, *w;
+};
+
+FwdWork carve_fwd(Carver& c, long p, long q, long r, bool pack_x, bool pack_w) {
+  FwdWork w{};
+  if (pack_x) w.x = c.take(2 * p * oz2::packed_ld(q, 2));
+  if (pack_w) w.w = c.take(2 * r * oz2::packed_ld(q, 2));
+  return w;
+}
+
 struct BwdWork {
-  void* dz;
+  void *dz, *x, *w;
   float* part;
 };
 
-BwdWork carve_bwd(Carver& c, int type, long p, long r) {
-  BwdWork w;
-  w.dz = c.take(elem_of(type) * p * r);
+BwdWork carve_bwd(Carver& c, long p, long q, long r, bool make_dz, bool pack_x, bool pack_w) {
+  BwdWork w{};
+  if (make_dz) w.dz = c.take(2 * p * oz2::packed_ld(r, 2));
+  if (pack_x) w.x = c.take(2 * p * oz2::packed_ld(q, 2));
+  if (pack_w) w.w = c.take(2 * r * oz2::packed_ld(q, 2));
   w.part = static_cast<float*>(c.take(sizeof(float) * oz2::grad_row_blocks(static_cast<int>(p)) * r));
   return w;
 }
 
 struct I8Work {
-  int8_t* q;
+  int8_t *q, *v;
   float* scale;
 };
 
-I8Work carve_i8(Carver& c, long p, long q) {
-  I8Work w;
-  w.q = static_cast<int8_t*>(c.take(p * q));
+I8Work carve_i8(Carver& c, long p, long q, long r, bool pack_v) {
+  I8Work w{};
+  w.q = static_cast<int8_t*>(c.take(p * oz2::packed_ld(q, 1)));
   w.scale = static_cast<float*>(c.take(sizeof(float) * p));
+  if (pack_v) w.v = static_cast<int8_t*>(c.take(r * oz2::packed_ld(q, 1)));
   return w;
 }
 
@@ -136,9 +151,18 @@ int ozaki2_linear(int type, int p, int q, int r, const void* X, int ldx, const v
   if (!grid_ok(p, r)) return OZ2_ERR_UNSUPPORTED;
   if (overlap(y, x) || overlap(y, w) || overlap(y, b) || overlap(y, z) || (overlap(y, res) && !same(y, res))) return OZ2_ERR_ARG;
   if (overlap(z, x) || overlap(z, w) || overlap(z, b) || overlap(z, res)) return OZ2_ERR_ARG;
-  (void)work;
-  (void)work_bytes;
-  oz2::Product pr{type, false, p, r, q, X, ldx, 1, W, ldw, 1, {}};
+  const bool pack_x = !oz2::rows_aligned(X, ldx, q, 2), pack_w = !oz2::rows_aligned(W, ldw, q, 2);
+  Carver need, c;
+  carve_fwd(need, p, q, r, pack_x, pack_w);
+  int rc = workspace(work, work_bytes, need.used, &c.base);
+  if (rc != OZ2_OK) return rc;
+  const FwdWork ws = carve_fwd(c, p, q, r, pack_x, pack_w);
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  const long lp = oz2::packed_ld(q, 2);
+  if (pack_x && (rc = status(oz2::launch_pack_rows(2, p, q, X, ldx, ws.x, lp, st))) != OZ2_OK) return rc;
+  if (pack_w && (rc = status(oz2::launch_pack_rows(2, r, q, W, ldw, ws.w, lp, st))) != OZ2_OK) return rc;
+  oz2::Product pr{type,  false, p, r, pack_x || pack_w ? static_cast<int>(lp) : q, pack_x ? ws.x : X, pack_x ? lp : ldx,
+                  false, pack_w ? ws.w : W, pack_w ? lp : ldw, false, {}};
   pr.epi.bias = bias;
   pr.epi.act = act;
   pr.epi.drop = make_drop(dropout);
@@ -148,7 +172,7 @@ int ozaki2_linear(int type, int p, int q, int r, const void* X, int ldx, const v
   pr.epi.ldz = ldz;
   pr.epi.y = Y;
   pr.epi.ldy = ldy;
-  return status(oz2::launch_product(pr, static_cast<hipStream_t>(stream)));
+  return status(oz2::launch_product(pr, st));
 }
 
 int ozaki2_linear_bwd(int type, int p, int q, int r, const void* dY, int lddy, const void* X, int ldx, const void* W,
@@ -176,30 +200,38 @@ int ozaki2_linear_bwd(int type, int p, int q, int r, const void* dY, int lddy, c
     for (const Mat* o2 : outs)
       if (o != o2 && overlap(*o, *o2)) return OZ2_ERR_ARG;
   }
-  const size_t need = ozaki2_linear_workspace_size(OZ2_LINEAR_BWD, type, p, q, r);
-  Carver c;
-  int rc = workspace(work, work_bytes, need, &c.base);
-  if (rc != OZ2_OK) return rc;
-  const BwdWork ws = carve_bwd(c, type, p, r);
-  const hipStream_t st = static_cast<hipStream_t>(stream);
   const oz2::Drop drop = make_drop(dropout);
-  // dZ is dY itself without activation and dropout
-  const bool make_dz = (act != OZ2_ACT_NONE || drop.t != 0) && (want_dx || want_dw);
+  // dZ is dY itself without activation and dropout, if its rows are aligned; making it packs it
+  const bool product = want_dx || want_dw;
+  const bool make_dz = product && p > 0 && r > 0 && (act != OZ2_ACT_NONE || drop.t != 0 || !oz2::rows_aligned(dY, lddy, r, 2));
+  const bool pack_x = want_dw && p > 0 && !oz2::rows_aligned(X, ldx, q, 2);
+  const bool pack_w = want_dx && r > 0 && !oz2::rows_aligned(W, ldw, q, 2);
+  Carver need, c;
+  carve_bwd(need, p, q, r, make_dz, pack_x, pack_w);
+  int rc = workspace(work, work_bytes, need.used, &c.base);
+  if (rc != OZ2_OK) return rc;
+  const BwdWork ws = carve_bwd(c, p, q, r, make_dz, pack_x, pack_w);
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  const long lq = oz2::packed_ld(q, 2), lr = oz2::packed_ld(r, 2);
   if (make_dz || want_db) {
-    rc = status(oz2::launch_grad_rows(type, p, r, dY, lddy, Z, ldz, act, drop, make_dz ? ws.dz : nullptr, r,
+    rc = status(oz2::launch_grad_rows(type, p, r, dY, lddy, Z, ldz, act, drop, make_dz ? ws.dz : nullptr, lr,
                                       want_db ? dbias : nullptr, ws.part, st));
     if (rc != OZ2_OK) return rc;
   }
   const void* const dz = make_dz ? ws.dz : dY;
-  const long lddz = make_dz ? r : lddy;
+  const long lddz = make_dz ? lr : lddy;
+  // columns beyond r of a packed dZ are zeros, so they may count as depth or as outputs; of W
+  // and X likewise beyond q
   if (want_dx) {
-    oz2::Product pr{type, false, p, q, r, dz, lddz, 1, W, 1, ldw, {}};
+    if (pack_w && (rc = status(oz2::launch_pack_rows(2, r, q, W, ldw, ws.w, lq, st))) != OZ2_OK) return rc;
+    oz2::Product pr{type, false, p, q, r, dz, lddz, false, pack_w ? ws.w : W, pack_w ? lq : ldw, true, {}};
     pr.epi.y = dX;
     pr.epi.ldy = lddx;
     if ((rc = status(oz2::launch_product(pr, st))) != OZ2_OK) return rc;
   }
   if (want_dw) {
-    oz2::Product pr{type, false, r, q, p, dz, 1, lddz, X, 1, ldx, {}};
+    if (pack_x && (rc = status(oz2::launch_pack_rows(2, p, q, X, ldx, ws.x, lq, st))) != OZ2_OK) return rc;
+    oz2::Product pr{type, false, r, q, p, dz, lddz, true, pack_x ? ws.x : X, pack_x ? lq : ldx, true, {}};
     pr.epi.y = dW;
     pr.epi.ldy = lddw;
     if ((rc = status(oz2::launch_product(pr, st))) != OZ2_OK) return rc;
@@ -227,7 +259,7 @@ int ozaki2_quantize_rows(int type, int p, int q, const void* X, int ldx, int8_t*
   if (p == 0) return OZ2_OK;
   if (scale == nullptr || (q > 0 && (X == nullptr || Q == nullptr))) return OZ2_ERR_ARG;
   if (overlap(out, x) || overlap(sc, x) || overlap(sc, out)) return OZ2_ERR_ARG;
-  return status(oz2::launch_quantize_rows(type, p, q, X, ldx, Q, ldq, scale, static_cast<hipStream_t>(stream)));
+  return status(oz2::launch_quantize_rows(type, p, q, X, ldx, Q, ldq, q, scale, static_cast<hipStream_t>(stream)));
 }
 
 int ozaki2_linear_i8(int type, int p, int q, int r, const void* X, int ldx, const int8_t* V, int ldv, const float* t,
@@ -243,14 +275,17 @@ int ozaki2_linear_i8(int type, int p, int q, int r, const void* X, int ldx, cons
   if (q > OZ2_LINEAR_I8_MAX_Q || !grid_ok(p, r)) return OZ2_ERR_UNSUPPORTED;
   if (Y == nullptr || t == nullptr || (q > 0 && (X == nullptr || V == nullptr))) return OZ2_ERR_ARG;
   if (overlap(y, x) || overlap(y, v) || overlap(y, sc) || overlap(y, b) || (overlap(y, res) && !same(y, res))) return OZ2_ERR_ARG;
-  const size_t need = ozaki2_linear_workspace_size(OZ2_LINEAR_I8, type, p, q, r);
-  Carver c;
-  int rc = workspace(work, work_bytes, need, &c.base);
+  const bool pack_v = !oz2::rows_aligned(V, ldv, q, 1);
+  Carver need, c;
+  carve_i8(need, p, q, r, pack_v);
+  int rc = workspace(work, work_bytes, need.used, &c.base);
   if (rc != OZ2_OK) return rc;
-  const I8Work ws = carve_i8(c, p, q);
+  const I8Work ws = carve_i8(c, p, q, r, pack_v);
   const hipStream_t st = static_cast<hipStream_t>(stream);
-  if ((rc = status(oz2::launch_quantize_rows(type, p, q, X, ldx, ws.q, q, ws.scale, st))) != OZ2_OK) return rc;
-  oz2::Product pr{type, true, p, r, q, ws.q, q, 1, V, ldv, 1, {}};
+  const long lq = oz2::packed_ld(q, 1);
+  if ((rc = status(oz2::launch_quantize_rows(type, p, q, X, ldx, ws.q, lq, static_cast<int>(lq), ws.scale, st))) != OZ2_OK) return rc;
+  if (pack_v && (rc = status(oz2::launch_pack_rows(1, r, q, V, ldv, ws.v, lq, st))) != OZ2_OK) return rc;
+  oz2::Product pr{type, true, p, r, static_cast<int>(lq), ws.q, lq, false, pack_v ? ws.v : V, pack_v ? lq : ldv, false, {}};
   pr.epi.bias = bias;
   pr.epi.act = act;
   pr.epi.res = R;
@@ -265,10 +300,18 @@ int ozaki2_linear_i8(int type, int p, int q, int r, const void* X, int ldx, cons
 size_t ozaki2_linear_workspace_size(int call, int type, int p, int q, int r) {
   if ((type != OZ2_BF16 && type != OZ2_F16) || !sizes_ok(p, q, r)) return 0;
   Carver c;
-  if (call == OZ2_LINEAR_BWD)
-    carve_bwd(c, type, p, r);
-  else if (call == OZ2_LINEAR_I8)
-    carve_i8(c, p, q);
+  const bool aligned = (call & OZ2_LINEAR_ALIGNED) != 0;
+  switch (call & ~OZ2_LINEAR_ALIGNED) {
+    case OZ2_LINEAR_FWD:
+      carve_fwd(c, p, q, r, !aligned, !aligned);
+      break;
+    case OZ2_LINEAR_BWD:
+      carve_bwd(c, p, q, r, true, !aligned, !aligned);
+      break;
+    case OZ2_LINEAR_I8:
+      carve_i8(c, p, q, r, !aligned);
+      break;
+  }
   return c.used;
 }
 

@@ -59,9 +59,9 @@ constexpr int kGradCols = 256;
 
 int grad_row_blocks(int p) { return (p + kGradRows - 1) / kGradRows; }
 
-template <typename T>
+template <typename T, int ACT>
 __global__ __launch_bounds__(256) void grad_rows_kernel(int p, int r, const T* dy, long lddy, const T* z, long ldz,
-                                                        int act, Drop d, T* dz, long lddz, float* part) {
+                                                        Drop d, T* dz, long lddz, float* part) {
   __shared__ float sums[8][kGradCols];
   const int g = threadIdx.x & 31, rr = threadIdx.x >> 5;
   const int col = blockIdx.y * kGradCols + 8 * g;
@@ -73,12 +73,13 @@ __global__ __launch_bounds__(256) void grad_rows_kernel(int p, int r, const T* d
       float v[8], t[8];
       load8(dy + row * lddy + col, valid, v);
       if (d.t != 0) drop8(v, d, row, r, col >> 3);
-      if (act != kActNone) {
+      if constexpr (ACT != kActNone) {
         load8(z + row * ldz + col, valid, t);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= activation_slope(t[i], act);
+        for (int i = 0; i < 8; ++i) v[i] *= activation_slope<ACT>(t[i]);
       }
-      if (dz != nullptr) store8(dz + row * lddz + col, valid, v);
+      // dz's rows are padded to multiples of 8 with zeros (load8's)
+      if (dz != nullptr) store8(dz + row * lddz + col, 8, v);
 #pragma unroll
       for (int i = 0; i < 8; ++i) sum[i] += v[i];
     }
@@ -108,8 +109,17 @@ static hipError_t grad_rows(int p, int r, const void* dy, long lddy, const void*
                             void* dz, long lddz, void* db, float* part, hipStream_t st) {
   const dim3 grid(grad_row_blocks(p), (r + kGradCols - 1) / kGradCols);
   if (p > 0 && r > 0) {  // without rows the column sums are zeros
-    hipLaunchKernelGGL(grad_rows_kernel<T>, grid, dim3(256), 0, st, p, r, static_cast<const T*>(dy), lddy,
-                       static_cast<const T*>(z), ldz, act, d, static_cast<T*>(dz), lddz, db != nullptr ? part : nullptr);
+    auto launch = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, p, r, static_cast<const T*>(dy), lddy,
+                         static_cast<const T*>(z), ldz, d, static_cast<T*>(dz), lddz, db != nullptr ? part : nullptr);
+    };
+    switch (act) {
+      case kActRelu: launch(grad_rows_kernel<T, kActRelu>); break;
+      case kActGelu: launch(grad_rows_kernel<T, kActGelu>); break;
+      case kActGeluTanh: launch(grad_rows_kernel<T, kActGeluTanh>); break;
+      case kActSilu: launch(grad_rows_kernel<T, kActSilu>); break;
+      default: launch(grad_rows_kernel<T, kActNone>); break;
+    }
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
   }
@@ -132,7 +142,7 @@ hipError_t launch_grad_rows(int type, int p, int r, const void* dy, long lddy, c
 constexpr float kTinyRow = 1e-36f;
 
 template <typename T>
-__global__ __launch_bounds__(256) void quantize_rows_kernel(int q, const T* x, long ldx, int8_t* out, long ldo, float* scale) {
+__global__ __launch_bounds__(256) void quantize_rows_kernel(int q, const T* x, long ldx, int8_t* out, long ldo, int fill, float* scale) {
   __shared__ float tops[4];
   const long row = blockIdx.x;
   const T* const src = x + row * ldx;
@@ -155,18 +165,19 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(int q, const T* x, l
     const float v = rintf(static_cast<float>(src[k]) * inv);
     out[row * ldo + k] = static_cast<int8_t>(finite ? static_cast<int>(v) : 0);
   }
+  for (int k = q + threadIdx.x; k < fill; k += 256) out[row * ldo + k] = 0;
   if (threadIdx.x == 0) scale[row] = inv == 0.0f && finite ? 0.0f : finite ? top / 127.0f : __builtin_nanf("");
 }
 
-hipError_t launch_quantize_rows(int type, int p, int q, const void* x, long ldx, int8_t* out, long ldo, float* scale,
-                                hipStream_t st) {
+hipError_t launch_quantize_rows(int type, int p, int q, const void* x, long ldx, int8_t* out, long ldo, int fill,
+                                float* scale, hipStream_t st) {
   const dim3 grid(static_cast<unsigned>(p));
   if (type == kTypeBf16)
-    hipLaunchKernelGGL(quantize_rows_kernel<bf16>, grid, dim3(256), 0, st, q, static_cast<const bf16*>(x), ldx, out, ldo, scale);
+    hipLaunchKernelGGL(quantize_rows_kernel<bf16>, grid, dim3(256), 0, st, q, static_cast<const bf16*>(x), ldx, out, ldo, fill, scale);
   else if (type == kTypeF16)
-    hipLaunchKernelGGL(quantize_rows_kernel<f16>, grid, dim3(256), 0, st, q, static_cast<const f16*>(x), ldx, out, ldo, scale);
+    hipLaunchKernelGGL(quantize_rows_kernel<f16>, grid, dim3(256), 0, st, q, static_cast<const f16*>(x), ldx, out, ldo, fill, scale);
   else
-    hipLaunchKernelGGL(quantize_rows_kernel<float>, grid, dim3(256), 0, st, q, static_cast<const float*>(x), ldx, out, ldo, scale);
+    hipLaunchKernelGGL(quantize_rows_kernel<float>, grid, dim3(256), 0, st, q, static_cast<const float*>(x), ldx, out, ldo, fill, scale);
   return hipGetLastError();
 }
 

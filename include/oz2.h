@@ -324,11 +324,15 @@ int ozaki2_linear_i8(int type, int p, int q, int r, const void* X, int ldx, cons
                      const void* bias, int act, const void* R, int ldr, void* Y, int ldy, void* work,
                      size_t work_bytes, void* stream);
 
-/* The calls ozaki2_linear_workspace_size answers for. */
-typedef enum { OZ2_LINEAR_FWD = 0, OZ2_LINEAR_BWD = 1, OZ2_LINEAR_I8 = 2 } oz2_linear_call_t;
+/* The calls ozaki2_linear_workspace_size answers for, and a flag to add to one of them: the
+ * rows of X and W (V) start on 16-byte boundaries, q elements are a multiple of 16 bytes, and
+ * leading dimensions are below 2^24 bytes.  Operands that are not so are first copied, row by
+ * row, into the workspace. */
+typedef enum { OZ2_LINEAR_FWD = 0, OZ2_LINEAR_BWD = 1, OZ2_LINEAR_I8 = 2, OZ2_LINEAR_ALIGNED = 16 } oz2_linear_call_t;
 
 /* Bytes of workspace the call needs for these sizes, whatever its other arguments (0 for
- * invalid arguments, no work, or none needed). */
+ * invalid arguments, no work, or none needed).  A call with less is refused only if it does
+ * need more. */
 size_t ozaki2_linear_workspace_size(int call, int type, int p, int q, int r);
 
 /* Static description of a status code. */
