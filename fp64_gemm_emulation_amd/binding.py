@@ -310,33 +310,56 @@ def dgemm_debug(A, B, s: int = 14, mode: str = "fast", want=DUMP_FIELDS, stream=
 # Row-major 2-D tensors, one token per row (a 3-D batch is passed as its reshape(-1, q)).
 # Outputs and scratch are allocated on the stream of the call, so calls on different
 # streams share nothing; operands made on another stream have to be ready on this one.
-def _types():
+# A single token's layer takes a few microseconds on the GPU, so these functions look up
+# attributes once, and torch itself on first use only.
+_torch = None
+_KINDS = {}          # torch dtype -> oz2_type_t
+_raw_stream = None   # device index -> hipStream_t of its current stream
+
+
+def _use_torch():
+    global _torch, _raw_stream
     import torch
-    return {torch.bfloat16: OZ2_BF16, torch.float16: OZ2_F16, torch.float32: OZ2_F32}
+    _KINDS.update({torch.bfloat16: OZ2_BF16, torch.float16: OZ2_F16, torch.float32: OZ2_F32})
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+        (lambda index: torch.cuda.current_stream(index).cuda_stream)
+    _torch = torch
+    return torch
 
 
-def _element_type(t, name, f32=False):
-    code = _types().get(t.dtype)
+def _shape2(t, name):
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be a 2-D tensor, not {len(shape)}-D")
+    return shape
+
+
+def _kind(t, name, f32=False):
+    code = _KINDS.get(t.dtype)
     if code is None or (code == OZ2_F32 and not f32):
         raise ValueError(f"{name} must be bfloat16 or float16" + (" or float32" if f32 else "") + f", not {t.dtype}")
     return code
 
 
-def _rows(t, name, shape, like, dtype=None):
-    """(pointer, leading dimension) of a row-major matrix on the device of `like`; (None, 1) for None."""
-    if t is None:
-        return None, 1
-    if t.dim() != 2 or tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
-    if t.dtype != (dtype or like.dtype):
-        raise ValueError(f"{name} must be {dtype or like.dtype}, not {t.dtype}")
-    if not t.is_cuda or t.device != like.device:
+def _check_operand(t, name, shape, dtype, dev):
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if dev < 0 or t.get_device() != dev:
         raise ValueError(f"{name} must be a CUDA tensor on the device of the other operands")
+
+
+def _rows(t, name, shape, dtype, dev):
+    """(pointer, leading dimension) of a row-major matrix; (None, columns) for None."""
     rows, cols = shape
+    if t is None:
+        return None, cols or 1
+    _check_operand(t, name, shape, dtype, dev)
     if rows == 0 or cols == 0:
-        return t.data_ptr(), max(1, cols)
-    step, ld = t.stride(1), t.stride(0)
-    if (cols > 1 and step != 1) or (rows > 1 and ld < cols):
+        return t.data_ptr(), cols or 1
+    ld, step = t.stride()
+    if (step != 1 and cols > 1) or (ld < cols and rows > 1):
         raise ValueError(f"{name} must be row-major (stride (ld >= columns, 1)), not stride {tuple(t.stride())}")
     if rows == 1:
         ld = cols
@@ -345,15 +368,10 @@ def _rows(t, name, shape, like, dtype=None):
     return t.data_ptr(), ld
 
 
-def _vector(t, name, n, like, dtype=None):
+def _vector(t, name, n, dtype, dev):
     if t is None:
         return None
-    if t.dim() != 1 or t.shape[0] != n:
-        raise ValueError(f"{name} must have shape {(n,)}, not {tuple(t.shape)}")
-    if t.dtype != (dtype or like.dtype):
-        raise ValueError(f"{name} must be {dtype or like.dtype}, not {t.dtype}")
-    if not t.is_cuda or t.device != like.device:
-        raise ValueError(f"{name} must be a CUDA tensor on the device of the other operands")
+    _check_operand(t, name, (n,), dtype, dev)
     if n > 1 and t.stride(0) != 1:
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
@@ -376,61 +394,46 @@ def _make_dropout(dropout, seed, offset):
     return OZ2Dropout(dropout, seed, offset)
 
 
-class _Call:
-    """The device and the stream of one call: made current while outputs and scratch are
-    allocated and the library is entered."""
-
-    def __init__(self, like, stream):
-        import torch
-        if not like.is_cuda:
-            raise ValueError("operands must be CUDA tensors")
-        dev = like.device
-        if stream is not None and stream.device != dev:
-            raise ValueError("the stream belongs to another device than the operands")
-        self._ctx = None
-        if stream is not None:
-            self._ctx = torch.cuda.stream(stream)      # also makes the stream's device current
-        elif dev.index != torch.cuda.current_device():
-            self._ctx = torch.cuda.device(dev)
-        self.raw = stream.cuda_stream if stream is not None else torch.cuda.current_stream(dev).cuda_stream
-        self._dev = dev
-
+class _NoContext:
     def __enter__(self):
-        if self._ctx is not None:
-            self._ctx.__enter__()
-        return self
+        pass
 
     def __exit__(self, *exc):
-        if self._ctx is not None:
-            self._ctx.__exit__(*exc)
-
-    def scratch(self, nbytes):
-        if nbytes == 0:
-            return None
-        import torch
-        return torch.empty(nbytes, dtype=torch.uint8, device=self._dev)
+        pass
 
 
-def _aligned(len_bytes, *rows):
-    """OZ2_LINEAR_ALIGNED if every (pointer, row stride in bytes) of rows of len_bytes bytes is."""
-    if len_bytes % 16 == 0 and all(p is None or (p % 16 == 0 and ld % 16 == 0 and ld < 1 << 24) for p, ld in rows):
-        return OZ2_LINEAR_ALIGNED
-    return 0
+_NO_CONTEXT = _NoContext()
 
 
-def _ptr(t):
-    return t.data_ptr() if t is not None else None
+def _entered(dev, stream):
+    """Context that makes the call's device and stream current while outputs and scratch are
+    allocated and the library is entered (none where they are)."""
+    if dev < 0:
+        raise ValueError("operands must be CUDA tensors")
+    if stream is not None:
+        if stream.device.index != dev:
+            raise ValueError("the stream belongs to another device than the operands")
+        return _torch.cuda.stream(stream)
+    return _NO_CONTEXT if dev == _torch.cuda.current_device() else _torch.cuda.device(dev)
 
 
-def _check(rc, what):
-    if rc != OZ2_OK:
-        raise Oz2Error(rc, what)
+def _aligned(row_bytes, *rows):
+    """OZ2_LINEAR_ALIGNED if every (pointer, row stride in bytes) of rows of row_bytes is."""
+    if row_bytes % 16:
+        return 0
+    for p, ld in rows:
+        if p is not None and (p % 16 or ld % 16 or ld >= 1 << 24):
+            return 0
+    return OZ2_LINEAR_ALIGNED
 
 
-def _two_dims(t, name):
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be a 2-D tensor, not {t.dim()}-D")
-    return t.shape
+def _scratch(call, kind, p, q, r, device):
+    """(tensor, pointer, bytes) of the call's workspace."""
+    n = _LIB.ozaki2_linear_workspace_size(call, kind, p, q, r)
+    if n == 0:
+        return None, None, 0
+    t = _torch.empty(n, dtype=_torch.uint8, device=device)
+    return t, t.data_ptr(), n
 
 
 def linear(x, w, bias=None, activation: str = "none", residual=None, dropout: float = 0.0, seed: int = 0,
@@ -438,22 +441,24 @@ def linear(x, w, bias=None, activation: str = "none", residual=None, dropout: fl
     """residual + D(act(x w^T + bias)) for x [p, q], w [r, q] in bfloat16 or float16, D the
     dropout of the C header; with return_z, (y, z), z the pre-activation for
     linear_backward.  `out` may be `residual` itself."""
-    import torch
-    p, q = _two_dims(x, "x")
-    r = _two_dims(w, "w")[0]
-    kind, act, drop = _element_type(x, "x"), _activation(activation), _make_dropout(dropout, seed, offset)
-    with _Call(x, stream) as call:
-        px, ldx = _rows(x, "x", (p, q), x)
-        pw, ldw = _rows(w, "w", (r, q), x)
-        pr, ldr = _rows(residual, "residual", (p, r), x)
-        pb = _vector(bias, "bias", r, x)
-        y = out if out is not None else torch.empty((p, r), dtype=x.dtype, device=x.device)
-        py, ldy = _rows(y, "out", (p, r), x)
-        z = torch.empty((p, r), dtype=x.dtype, device=x.device) if return_z else None
-        work = call.scratch(_LIB.ozaki2_linear_workspace_size(OZ2_LINEAR_FWD | _aligned(2 * q, (px, 2 * ldx), (pw, 2 * ldw)), kind, p, q, r))
-        rc = ozaki2_linear(kind, p, q, r, px, ldx, pw, ldw, pb, act, drop, pr, ldr, _ptr(z), max(1, r), py, ldy,
-                           _ptr(work), work.numel() if work is not None else 0, call.raw)
-    _check(rc, "ozaki2_linear")
+    torch = _torch or _use_torch()
+    p, q = shape = _shape2(x, "x")
+    r = _shape2(w, "w")[0]
+    kind, act, drop = _kind(x, "x"), _activation(activation), _make_dropout(dropout, seed, offset)
+    dtype, dev, device = x.dtype, x.get_device(), x.device
+    with _entered(dev, stream):
+        px, ldx = _rows(x, "x", shape, dtype, dev)
+        pw, ldw = _rows(w, "w", (r, q), dtype, dev)
+        pr, ldr = _rows(residual, "residual", (p, r), dtype, dev)
+        pb = _vector(bias, "bias", r, dtype, dev)
+        y = out if out is not None else torch.empty((p, r), dtype=dtype, device=device)
+        py, ldy = _rows(y, "out", (p, r), dtype, dev) if out is not None else (y.data_ptr(), r or 1)
+        z = torch.empty((p, r), dtype=dtype, device=device) if return_z else None
+        work, pwork, nwork = _scratch(OZ2_LINEAR_FWD | _aligned(2 * q, (px, 2 * ldx), (pw, 2 * ldw)), kind, p, q, r, device)
+        rc = _LIB.ozaki2_linear(kind, p, q, r, px, ldx, pw, ldw, pb, act, _dropout_ref(drop), pr, ldr,
+                                z.data_ptr() if return_z else None, r or 1, py, ldy, pwork, nwork, _raw_stream(dev))
+    if rc != OZ2_OK:
+        raise Oz2Error(rc, "ozaki2_linear")
     return (y, z) if return_z else y
 
 
@@ -462,27 +467,31 @@ def linear_backward(dy, x, w, z=None, activation: str = "none", dropout: float =
     """(dx, dw, dbias) of linear from dy [p, r]; those not named in `needs` are None.  z is
     linear's pre-activation, needed unless activation is "none"; dropout, seed and offset have
     to be the forward call's.  The residual's gradient is dy itself."""
-    import torch
-    p, r = _two_dims(dy, "dy")
-    q = _two_dims(w, "w")[1]
-    kind, act, drop = _element_type(dy, "dy"), _activation(activation), _make_dropout(dropout, seed, offset)
+    torch = _torch or _use_torch()
+    p, r = shape = _shape2(dy, "dy")
+    q = _shape2(w, "w")[1]
+    kind, act, drop = _kind(dy, "dy"), _activation(activation), _make_dropout(dropout, seed, offset)
     unknown = set(needs) - {"x", "w", "bias"}
     if unknown:
         raise ValueError(f"needs names {sorted(unknown)}: only x, w and bias have gradients here")
     if act != OZ2_ACT_NONE and z is None:
         raise ValueError("the gradient of an activation needs z")
-    with _Call(dy, stream) as call:
-        pdy, lddy = _rows(dy, "dy", (p, r), dy)
-        px, ldx = _rows(x, "x", (p, q), dy)
-        pw, ldw = _rows(w, "w", (r, q), dy)
-        pz, ldz = _rows(z, "z", (p, r), dy)
-        new = lambda name, *shape: torch.empty(shape, dtype=dy.dtype, device=dy.device) if name in needs else None  # noqa: E731
-        dx, dw, db = new("x", p, q), new("w", r, q), new("bias", r)
-        work = call.scratch(_LIB.ozaki2_linear_workspace_size(OZ2_LINEAR_BWD | _aligned(2 * q, (px, 2 * ldx), (pw, 2 * ldw)), kind, p, q, r))
-        rc = ozaki2_linear_bwd(kind, p, q, r, pdy, lddy, px, ldx, pw, ldw, pz, ldz, act, drop, _ptr(dx), max(1, q),
-                               _ptr(dw), max(1, q), _ptr(db), _ptr(work), work.numel() if work is not None else 0,
-                               call.raw)
-    _check(rc, "ozaki2_linear_bwd")
+    dtype, dev, device = dy.dtype, dy.get_device(), dy.device
+    with _entered(dev, stream):
+        pdy, lddy = _rows(dy, "dy", shape, dtype, dev)
+        px, ldx = _rows(x, "x", (p, q), dtype, dev)
+        pw, ldw = _rows(w, "w", (r, q), dtype, dev)
+        pz, ldz = _rows(z, "z", shape, dtype, dev)
+        dx = torch.empty((p, q), dtype=dtype, device=device) if "x" in needs else None
+        dw = torch.empty((r, q), dtype=dtype, device=device) if "w" in needs else None
+        db = torch.empty((r,), dtype=dtype, device=device) if "bias" in needs else None
+        work, pwork, nwork = _scratch(OZ2_LINEAR_BWD | _aligned(2 * q, (px, 2 * ldx), (pw, 2 * ldw)), kind, p, q, r, device)
+        rc = _LIB.ozaki2_linear_bwd(kind, p, q, r, pdy, lddy, px, ldx, pw, ldw, pz, ldz, act, _dropout_ref(drop),
+                                    dx.data_ptr() if dx is not None else None, q or 1,
+                                    dw.data_ptr() if dw is not None else None, q or 1,
+                                    db.data_ptr() if db is not None else None, pwork, nwork, _raw_stream(dev))
+    if rc != OZ2_OK:
+        raise Oz2Error(rc, "ozaki2_linear_bwd")
     return dx, dw, db
 
 
@@ -490,52 +499,58 @@ def dropout_add(x, residual=None, dropout: float = 0.0, seed: int = 0, offset: i
     """residual + D(x) for x [p, r] in bfloat16, float16 or float32; the gradient with respect
     to x is dropout_add(dy, None, ...) with the same dropout, seed and offset.  `out` may be x
     or residual itself."""
-    import torch
-    p, r = _two_dims(x, "x")
-    kind, drop = _element_type(x, "x", f32=True), _make_dropout(dropout, seed, offset)
-    with _Call(x, stream) as call:
-        px, ldx = _rows(x, "x", (p, r), x)
-        pr, ldr = _rows(residual, "residual", (p, r), x)
-        y = out if out is not None else torch.empty((p, r), dtype=x.dtype, device=x.device)
-        py, ldy = _rows(y, "out", (p, r), x)
-        rc = ozaki2_dropout_add(kind, p, r, px, ldx, pr, ldr, drop, py, ldy, call.raw)
-    _check(rc, "ozaki2_dropout_add")
+    torch = _torch or _use_torch()
+    p, r = shape = _shape2(x, "x")
+    kind, drop = _kind(x, "x", f32=True), _make_dropout(dropout, seed, offset)
+    dtype, dev = x.dtype, x.get_device()
+    with _entered(dev, stream):
+        px, ldx = _rows(x, "x", shape, dtype, dev)
+        pr, ldr = _rows(residual, "residual", shape, dtype, dev)
+        y = out if out is not None else torch.empty((p, r), dtype=dtype, device=x.device)
+        py, ldy = _rows(y, "out", shape, dtype, dev) if out is not None else (y.data_ptr(), r or 1)
+        rc = _LIB.ozaki2_dropout_add(kind, p, r, px, ldx, pr, ldr, _dropout_ref(drop), py, ldy, _raw_stream(dev))
+    if rc != OZ2_OK:
+        raise Oz2Error(rc, "ozaki2_dropout_add")
     return y
 
 
 def quantize_rows(x, stream=None):
     """(int8 tensor, float32 scale of each row) of x [p, q] in bfloat16, float16 or float32."""
-    import torch
-    p, q = _two_dims(x, "x")
-    kind = _element_type(x, "x", f32=True)
-    with _Call(x, stream) as call:
-        px, ldx = _rows(x, "x", (p, q), x)
-        out = torch.empty((p, q), dtype=torch.int8, device=x.device)
-        scale = torch.empty((p,), dtype=torch.float32, device=x.device)
-        rc = ozaki2_quantize_rows(kind, p, q, px, ldx, out.data_ptr(), max(1, q), scale.data_ptr(), call.raw)
-    _check(rc, "ozaki2_quantize_rows")
+    torch = _torch or _use_torch()
+    p, q = shape = _shape2(x, "x")
+    kind = _kind(x, "x", f32=True)
+    dev, device = x.get_device(), x.device
+    with _entered(dev, stream):
+        px, ldx = _rows(x, "x", shape, x.dtype, dev)
+        out = torch.empty((p, q), dtype=torch.int8, device=device)
+        scale = torch.empty((p,), dtype=torch.float32, device=device)
+        rc = _LIB.ozaki2_quantize_rows(kind, p, q, px, ldx, out.data_ptr(), q or 1, scale.data_ptr(), _raw_stream(dev))
+    if rc != OZ2_OK:
+        raise Oz2Error(rc, "ozaki2_quantize_rows")
     return out, scale
 
 
 def linear_i8(x, v, t, bias=None, activation: str = "none", residual=None, out=None, stream=None):
     """residual + act(x w^T + bias) with w held as (v, t) = quantize_rows(w): x [p, q] in
     bfloat16 or float16 is quantised by rows in the call.  `out` may be `residual` itself."""
-    import torch
-    p, q = _two_dims(x, "x")
-    r = _two_dims(v, "v")[0]
-    kind, act = _element_type(x, "x"), _activation(activation)
-    with _Call(x, stream) as call:
-        px, ldx = _rows(x, "x", (p, q), x)
-        pv, ldv = _rows(v, "v", (r, q), x, torch.int8)
-        pt = _vector(t, "t", r, x, torch.float32)
-        if pt is None:
-            raise ValueError("t is needed")
-        pr, ldr = _rows(residual, "residual", (p, r), x)
-        pb = _vector(bias, "bias", r, x)
-        y = out if out is not None else torch.empty((p, r), dtype=x.dtype, device=x.device)
-        py, ldy = _rows(y, "out", (p, r), x)
-        work = call.scratch(_LIB.ozaki2_linear_workspace_size(OZ2_LINEAR_I8 | _aligned(q, (pv, ldv)), kind, p, q, r))
-        rc = ozaki2_linear_i8(kind, p, q, r, px, ldx, pv, ldv, pt, pb, act, pr, ldr, py, ldy, _ptr(work),
-                              work.numel() if work is not None else 0, call.raw)
-    _check(rc, "ozaki2_linear_i8")
+    torch = _torch or _use_torch()
+    p, q = shape = _shape2(x, "x")
+    r = _shape2(v, "v")[0]
+    kind, act = _kind(x, "x"), _activation(activation)
+    if t is None:
+        raise ValueError("t, the scales of v's rows, is needed")
+    dtype, dev, device = x.dtype, x.get_device(), x.device
+    with _entered(dev, stream):
+        px, ldx = _rows(x, "x", shape, dtype, dev)
+        pv, ldv = _rows(v, "v", (r, q), torch.int8, dev)
+        pt = _vector(t, "t", r, torch.float32, dev)
+        pr, ldr = _rows(residual, "residual", (p, r), dtype, dev)
+        pb = _vector(bias, "bias", r, dtype, dev)
+        y = out if out is not None else torch.empty((p, r), dtype=dtype, device=device)
+        py, ldy = _rows(y, "out", (p, r), dtype, dev) if out is not None else (y.data_ptr(), r or 1)
+        work, pwork, nwork = _scratch(OZ2_LINEAR_I8 | _aligned(q, (pv, ldv)), kind, p, q, r, device)
+        rc = _LIB.ozaki2_linear_i8(kind, p, q, r, px, ldx, pv, ldv, pt, pb, act, pr, ldr, py, ldy, pwork, nwork,
+                                   _raw_stream(dev))
+    if rc != OZ2_OK:
+        raise Oz2Error(rc, "ozaki2_linear_i8")
     return y

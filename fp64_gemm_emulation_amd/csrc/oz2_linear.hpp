@@ -39,9 +39,20 @@ struct Epilogue {
   const float* ws = nullptr;  //               and of each row of the right one
 };
 
+// Which kernel computes a product, and over how many parts of the depth.
+enum { kTile256 = 0, kTile128 = 1, kTile64 = 2, kFew = 3 };
+struct Plan {
+  int tile = kTile128;
+  int splits = 1;
+};
+Plan plan_product(bool i8, long rows, long cols, long depth, bool left_along_index, bool right_along_index);
+inline size_t partial_bytes(const Plan& plan, long rows, long cols) {
+  return plan.splits > 1 ? 4 * static_cast<size_t>(plan.splits) * rows * ((cols + 7) / 8 * 8) : 0;
+}
+
 // out[m][n] = epilogue(sum_k left(m, k) right(n, k)), m < rows, n < cols, k < depth.  An operand
 // lies along the depth (element (i, k) at i * ld + k) or along its index (at k * ld + i; products
-// without an epilogue only).  Rows must be as rows_aligned says.
+// without an epilogue only).  Rows must be as rows_aligned says, except for kFew.
 struct Product {
   int type;   // element type of operands (unless int8) and outputs
   bool i8;    // int8 operands
@@ -53,6 +64,8 @@ struct Product {
   long right_ld;
   bool right_along_index;
   Epilogue epi;
+  Plan plan;
+  void* partial;  // partial_bytes of it
 };
 
 // Whether the product kernels can take an operand as it lies: every row starts on a 16-byte
@@ -66,6 +79,9 @@ inline long packed_ld(long len, int elem) { return (len * elem + 15) / 16 * 16 /
 hipError_t launch_pack_rows(int elem, long rows, int cols, const void* src, long ld, void* dst, long ld_out, hipStream_t st);
 
 hipError_t launch_product(const Product& pr, hipStream_t st);
+hipError_t launch_product_bf16(const Product& pr, hipStream_t st);
+hipError_t launch_product_f16(const Product& pr, hipStream_t st);
+hipError_t launch_product_i8(const Product& pr, hipStream_t st);
 hipError_t launch_dropout_add(int type, int p, int r, const void* x, long ldx, const void* res, long ldr,
                               const Drop& drop, void* y, long ldy, hipStream_t st);
 // dz = drop(dy) act'(z) in the operands' type, its rows padded with zeros to a multiple of 8

@@ -85,40 +85,53 @@ struct Carver {
 
 // The workspace of each call: copies of operands that need packing, and what it makes itself.
 struct FwdWork {
-  void *x, *w;
+  oz2::Plan plan;
+  void *x, *w, *partial;
 };
 
 FwdWork carve_fwd(Carver& c, long p, long q, long r, bool pack_x, bool pack_w) {
   FwdWork w{};
+  w.plan = oz2::plan_product(false, p, r, q, false, false);
+  if (w.plan.tile == oz2::kFew) return w;  // takes any rows
   if (pack_x) w.x = c.take(2 * p * oz2::packed_ld(q, 2));
   if (pack_w) w.w = c.take(2 * r * oz2::packed_ld(q, 2));
+  w.partial = c.take(oz2::partial_bytes(w.plan, p, r));
   return w;
 }
 
 struct BwdWork {
-  void *dz, *x, *w;
-  float* part;
+  oz2::Plan dx, dw;
+  void *dz, *x, *w, *partial;
+  float* sums;
 };
 
 BwdWork carve_bwd(Carver& c, long p, long q, long r, bool make_dz, bool pack_x, bool pack_w) {
   BwdWork w{};
+  w.dx = oz2::plan_product(false, p, q, r, false, true);
+  w.dw = oz2::plan_product(false, r, q, p, true, true);
   if (make_dz) w.dz = c.take(2 * p * oz2::packed_ld(r, 2));
   if (pack_x) w.x = c.take(2 * p * oz2::packed_ld(q, 2));
   if (pack_w) w.w = c.take(2 * r * oz2::packed_ld(q, 2));
-  w.part = static_cast<float*>(c.take(sizeof(float) * oz2::grad_row_blocks(static_cast<int>(p)) * r));
+  w.partial = c.take(std::max(oz2::partial_bytes(w.dx, p, q), oz2::partial_bytes(w.dw, r, q)));
+  w.sums = static_cast<float*>(c.take(sizeof(float) * oz2::grad_row_blocks(static_cast<int>(p)) * r));
   return w;
 }
 
 struct I8Work {
+  oz2::Plan plan;
   int8_t *q, *v;
   float* scale;
+  void* partial;
 };
 
 I8Work carve_i8(Carver& c, long p, long q, long r, bool pack_v) {
   I8Work w{};
+  w.plan = oz2::plan_product(true, p, r, q, false, false);
   w.q = static_cast<int8_t*>(c.take(p * oz2::packed_ld(q, 1)));
   w.scale = static_cast<float*>(c.take(sizeof(float) * p));
+  if (w.plan.tile == oz2::kFew) return w;  // takes any rows
   if (pack_v) w.v = static_cast<int8_t*>(c.take(r * oz2::packed_ld(q, 1)));
+  w.partial = c.take(oz2::partial_bytes(w.plan, p, r));
   return w;
 }
 
@@ -159,10 +172,11 @@ int ozaki2_linear(int type, int p, int q, int r, const void* X, int ldx, const v
   const FwdWork ws = carve_fwd(c, p, q, r, pack_x, pack_w);
   const hipStream_t st = static_cast<hipStream_t>(stream);
   const long lp = oz2::packed_ld(q, 2);
-  if (pack_x && (rc = status(oz2::launch_pack_rows(2, p, q, X, ldx, ws.x, lp, st))) != OZ2_OK) return rc;
-  if (pack_w && (rc = status(oz2::launch_pack_rows(2, r, q, W, ldw, ws.w, lp, st))) != OZ2_OK) return rc;
-  oz2::Product pr{type,  false, p, r, pack_x || pack_w ? static_cast<int>(lp) : q, pack_x ? ws.x : X, pack_x ? lp : ldx,
-                  false, pack_w ? ws.w : W, pack_w ? lp : ldw, false, {}};
+  if (ws.x != nullptr && (rc = status(oz2::launch_pack_rows(2, p, q, X, ldx, ws.x, lp, st))) != OZ2_OK) return rc;
+  if (ws.w != nullptr && (rc = status(oz2::launch_pack_rows(2, r, q, W, ldw, ws.w, lp, st))) != OZ2_OK) return rc;
+  const bool packed = ws.x != nullptr || ws.w != nullptr;  // then the depth may count its zeros
+  oz2::Product pr{type,  false, p, r, packed ? static_cast<int>(lp) : q, ws.x != nullptr ? ws.x : X, ws.x != nullptr ? lp : ldx,
+                  false, ws.w != nullptr ? ws.w : W, ws.w != nullptr ? lp : ldw, false, {}, ws.plan, ws.partial};
   pr.epi.bias = bias;
   pr.epi.act = act;
   pr.epi.drop = make_drop(dropout);
@@ -215,7 +229,7 @@ int ozaki2_linear_bwd(int type, int p, int q, int r, const void* dY, int lddy, c
   const long lq = oz2::packed_ld(q, 2), lr = oz2::packed_ld(r, 2);
   if (make_dz || want_db) {
     rc = status(oz2::launch_grad_rows(type, p, r, dY, lddy, Z, ldz, act, drop, make_dz ? ws.dz : nullptr, lr,
-                                      want_db ? dbias : nullptr, ws.part, st));
+                                      want_db ? dbias : nullptr, ws.sums, st));
     if (rc != OZ2_OK) return rc;
   }
   const void* const dz = make_dz ? ws.dz : dY;
@@ -224,14 +238,14 @@ int ozaki2_linear_bwd(int type, int p, int q, int r, const void* dY, int lddy, c
   // and X likewise beyond q
   if (want_dx) {
     if (pack_w && (rc = status(oz2::launch_pack_rows(2, r, q, W, ldw, ws.w, lq, st))) != OZ2_OK) return rc;
-    oz2::Product pr{type, false, p, q, r, dz, lddz, false, pack_w ? ws.w : W, pack_w ? lq : ldw, true, {}};
+    oz2::Product pr{type, false, p, q, r, dz, lddz, false, pack_w ? ws.w : W, pack_w ? lq : ldw, true, {}, ws.dx, ws.partial};
     pr.epi.y = dX;
     pr.epi.ldy = lddx;
     if ((rc = status(oz2::launch_product(pr, st))) != OZ2_OK) return rc;
   }
   if (want_dw) {
     if (pack_x && (rc = status(oz2::launch_pack_rows(2, p, q, X, ldx, ws.x, lq, st))) != OZ2_OK) return rc;
-    oz2::Product pr{type, false, r, q, p, dz, lddz, true, pack_x ? ws.x : X, pack_x ? lq : ldx, true, {}};
+    oz2::Product pr{type, false, r, q, p, dz, lddz, true, pack_x ? ws.x : X, pack_x ? lq : ldx, true, {}, ws.dw, ws.partial};
     pr.epi.y = dW;
     pr.epi.ldy = lddw;
     if ((rc = status(oz2::launch_product(pr, st))) != OZ2_OK) return rc;
@@ -284,8 +298,10 @@ int ozaki2_linear_i8(int type, int p, int q, int r, const void* X, int ldx, cons
   const hipStream_t st = static_cast<hipStream_t>(stream);
   const long lq = oz2::packed_ld(q, 1);
   if ((rc = status(oz2::launch_quantize_rows(type, p, q, X, ldx, ws.q, lq, static_cast<int>(lq), ws.scale, st))) != OZ2_OK) return rc;
-  if (pack_v && (rc = status(oz2::launch_pack_rows(1, r, q, V, ldv, ws.v, lq, st))) != OZ2_OK) return rc;
-  oz2::Product pr{type, true, p, r, static_cast<int>(lq), ws.q, lq, false, pack_v ? ws.v : V, pack_v ? lq : ldv, false, {}};
+  if (ws.v != nullptr && (rc = status(oz2::launch_pack_rows(1, r, q, V, ldv, ws.v, lq, st))) != OZ2_OK) return rc;
+  // where V is read as it lies at any length, so is Q; else both rows end in zeros
+  oz2::Product pr{type,  true, p, r, ws.plan.tile == oz2::kFew ? q : static_cast<int>(lq), ws.q, lq,
+                  false, ws.v != nullptr ? ws.v : V, ws.v != nullptr ? lq : ldv, false, {}, ws.plan, ws.partial};
   pr.epi.bias = bias;
   pr.epi.act = act;
   pr.epi.res = R;

@@ -1,0 +1,10 @@
+// oz2_linear_bf16.hip -- the linear-layer products on bf16 operands.
+#include "oz2_linear_tile.hpp"
+
+namespace oz2 {
+
+hipError_t launch_product_bf16(const Product& pr, hipStream_t st) {
+  return launch_type<MmaBf16, bf16>(pr, st);
+}
+
+}  // namespace oz2

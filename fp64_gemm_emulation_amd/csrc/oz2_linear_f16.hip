@@ -1,0 +1,10 @@
+// oz2_linear_f16.hip -- the linear-layer products on f16 operands.
+#include "oz2_linear_tile.hpp"
+
+namespace oz2 {
+
+hipError_t launch_product_f16(const Product& pr, hipStream_t st) {
+  return launch_type<MmaF16, f16>(pr, st);
+}
+
+}  // namespace oz2

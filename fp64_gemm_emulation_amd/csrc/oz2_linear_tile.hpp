@@ -1,0 +1,618 @@
+// oz2_linear_tile.hpp -- out = epilogue(left right^T), the products of the linear layer and of
+// its gradient: bf16 and f16 operands with f32 accumulators, int8 operands with int32 ones
+// (exact: 127^2 times the depth stays below 2^31 up to the 2^17 the entry points accept).
+// A header, so that each operand type is a translation unit of its own.
+#pragma once
+
+#include <type_traits>
+
+#include "oz2_common.hpp"
+#include "oz2_linear.hpp"
+
+namespace oz2 {
+
+typedef bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef f16 f16x8 __attribute__((ext_vector_type(8)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+// One 16 x 16 block over 64 bytes of depth per operand row: 32 16-bit or 64 int8 elements,
+// lane l holding 16 bytes of row l % 16.  D register v of lane l is row 4 (l / 16) + v of the
+// first operand and row l % 16 of the second.
+struct MmaBf16 {
+  typedef bf16 elem;
+  typedef f32x4 acc;
+  static __device__ __forceinline__ acc mma(i32x4 a, i32x4 b, acc c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  }
+};
+struct MmaF16 {
+  typedef f16 elem;
+  typedef f32x4 acc;
+  static __device__ __forceinline__ acc mma(i32x4 a, i32x4 b, acc c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  }
+};
+struct MmaI8 {
+  typedef int8_t elem;
+  typedef i32x4 acc;
+  static __device__ __forceinline__ acc mma(i32x4 a, i32x4 b, acc c) {
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
+  }
+};
+
+#define OZ2_WAIT_VMCNT(N) __builtin_amdgcn_s_waitcnt(((N) & 0xF) | (((N) >> 4) << 14) | (0x7 << 4) | (0xF << 8))
+#define OZ2_WAIT_LGKMCNT(N) __builtin_amdgcn_s_waitcnt(0xF | (0x3 << 14) | (0x7 << 4) | (((N) & 0xF) << 8))
+#define OZ2_SCHED_FENCE() __builtin_amdgcn_sched_barrier(0)
+
+typedef __attribute__((address_space(3))) void* lds_ptr_t;
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+// What the tile kernel does with its accumulators: the whole epilogue; rounding and storing
+// only; or storing them as they are, one of several sums over parts of the depth, which
+// join_kernel adds up and finishes.
+enum { kOutEpilogue = 0, kOutPlain = 1, kOutPartial = 2 };
+
+// How an operand lies in memory: along the depth (element (i, k) at i * ld + k), or along its
+// own index (at k * ld + i), as W does in dX = dZ W and both operands do in dW = dZ^T X.
+enum { kAlongDepth = 0, kAlongIndex = 1 };
+
+// f(activation) for the activation as a compile-time constant.
+template <typename F>
+__host__ __device__ __forceinline__ void with_activation(int act, F f) {
+  switch (act) {
+    case kActRelu: f(std::integral_constant<int, kActRelu>{}); break;
+    case kActGelu: f(std::integral_constant<int, kActGelu>{}); break;
+    case kActGeluTanh: f(std::integral_constant<int, kActGeluTanh>{}); break;
+    case kActSilu: f(std::integral_constant<int, kActSilu>{}); break;
+    default: f(std::integral_constant<int, kActNone>{}); break;
+  }
+}
+
+// ---- tile kernel ---------------------------------------------------------------------
+// BM x BN outputs per workgroup, its waves in a grid of WM x WN.  Depth advances in
+// stages of 128 bytes, so that every row of an operand along the depth brings whole cache
+// lines; two stages are held in LDS, filled with 1 KiB copies straight from memory.
+//
+// Per stage and wave, two halves of 64 bytes of depth (one matrix instruction deep):
+//   first half:  MFMAs on the first fragments, the second half's fragments read between them;
+//   middle:      every wave has read the stage: wait for the copies of the next stage (issued
+//                one stage ago), barrier;
+//   second half: MFMAs on the second fragments, between them the copies of the stage after
+//                next into the buffer just released, and the next stage's first fragments.
+// So there is one barrier per stage, and a copy has a whole stage of MFMAs to arrive.
+//
+// LDS layouts and bank conflicts.  Along the depth: rows of 128 bytes, 16-byte chunk c of row
+// i at chunk c ^ s(i).  The 16 lanes that read one chunk of 16 rows then hit 16 different
+// 16-byte bank groups (64 banks of 4 bytes): rows alternate between the halves of the banks
+// by their lowest bit, and s takes 8 values over those with the same one.  The right operand's
+// rows are dealt to the fragments so that a lane ends up with eight consecutive output
+// columns (block b of a pair takes rows 8 g + 4 b + v of 32, g = 0..3, v = 0..3), and its s is
+// chosen for that set.  Along the index: depth rows of BM (BN) elements, 32-byte block c of row
+// k at block c ^ f(k), read with the transposing LDS read: 16 lanes fetch 4 depth rows x 16
+// indices, each lane 8 bytes, and each receives one index's 4 depths.  f takes 16 (256
+// elements) or, within either half of the wave, as many as there are blocks (8 or 4) values
+// over the rows one read touches.
+template <int BM_, int BN_, int WM_, int WN_, int PER_CU_>
+struct Tile {
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
+  static constexpr int PER_CU = PER_CU_;        // workgroups that fit a CU's LDS
+  static constexpr int WAVES = WM * WN;
+  static constexpr int MB = BM / (16 * WM);     // 16-row blocks per wave
+  static constexpr int NB = BN / (16 * WN);     // 16-column blocks per wave
+  static constexpr int LEFT = BM * 128;         // bytes of the left operand's stage, the right one's behind it
+  static constexpr int STAGE = (BM + BN) * 128;
+  static constexpr int LCOPIES = BM / 8 / WAVES, RCOPIES = BN / 8 / WAVES;  // 1 KiB copies per wave
+  static_assert(BM % (8 * WAVES) == 0 && BN % (8 * WAVES) == 0 && NB % 2 == 0, "tile shape");
+};
+// 128 x 64 outputs per wave, two waves to a SIMD
+typedef Tile<256, 256, 2, 4, 1> Tile256;
+typedef Tile<128, 128, 2, 2, 2> Tile128;
+typedef Tile<64, 128, 1, 4, 3> Tile64;
+
+// s(i) of an operand along the depth.
+template <bool RIGHT>
+__device__ __forceinline__ int chunk_swizzle(int i) {
+  return RIGHT ? (((i >> 3) & 3) << 1) | ((i >> 1) & 1) : (i >> 1) & 7;
+}
+// f(k) of an operand along the index, depth rows of B elements.
+template <int B>
+__device__ __forceinline__ int block_swizzle(int k) {
+  return B >= 256 ? (k & 3) | (((k >> 3) & 3) << 2) : B >= 128 ? (k & 3) | (((k >> 3) & 1) << 2) : (k & 3);
+}
+
+// Byte offset, from the operand's tile origin in a stage, of the 16 bytes that lane `lane`
+// copies with the 1 KiB unit u.  Of a stage with `valid` elements of depth, chunks beyond them
+// read something inside the operand (and are zeroed in LDS afterwards); so do rows beyond the
+// last, and columns beyond the last chunk, which only reach outputs that are not stored.
+template <int B, int E, int LAYOUT, bool RIGHT>
+__device__ __forceinline__ unsigned copy_offset(int u, int lane, unsigned ld, int last_index, int valid) {
+  if constexpr (LAYOUT == kAlongDepth) {
+    const int i = 8 * u + (lane >> 3);
+    const int c = (lane & 7) ^ chunk_swizzle<RIGHT>(i);
+    return static_cast<unsigned>(min(i, last_index)) * ld * E + (c * (16 / E) < valid ? 16 * c : 0);
+  } else {
+    constexpr int kRow = B * E, kPerRow = kRow / 16;  // bytes and 16-byte chunks of a depth row
+    const int k = u * (1024 / kRow) + lane / kPerRow;
+    const int pc = lane % kPerRow;
+    const int c = 2 * ((pc >> 1) ^ block_swizzle<B>(k)) + (pc & 1);
+    return static_cast<unsigned>(min(k, valid - 1)) * ld * E + min(16 * c, last_index / (16 / E) * 16);
+  }
+}
+
+__device__ __forceinline__ void tile_of(unsigned wg, int tiles_m, int tiles_n, int& ti, int& tj) {
+  // workgroups go round-robin over the 8 XCDs: give each XCD a contiguous range of tiles, and
+  // walk it in groups of 4 tile rows, so the workgroups on one XCD's L2 share operand panels
+  constexpr unsigned kXcds = 8, kGroup = 4;
+  const unsigned n = static_cast<unsigned>(tiles_m) * static_cast<unsigned>(tiles_n);
+  const unsigned x = wg % kXcds, per = n / kXcds, rem = n % kXcds;
+  const unsigned id = x * per + min(x, rem) + wg / kXcds;
+  const unsigned group = id / (kGroup * tiles_n), in_group = id % (kGroup * tiles_n);
+  const unsigned rows = min(static_cast<unsigned>(tiles_m) - group * kGroup, kGroup);
+  ti = static_cast<int>(group * kGroup + in_group % rows);
+  tj = static_cast<int>(in_group / rows);
+}
+
+// The transposing read of 8 bytes per lane.  A function with a restrict pointer, so that the
+// load carries aliasing information: without any, the compiler makes it wait for every copy
+// into LDS that is still in flight.
+__device__ __forceinline__ s16x4 read_transposed(__attribute__((address_space(3))) s16x4* __restrict__ p) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16(p);
+}
+
+// Stages kt0 .. kt0 + per - 1 of the depth (as many as there are), kt0 = per * blockIdx.y.
+template <typename M, typename T, typename S, int LL, int RL, int OUT>
+__global__ __launch_bounds__(64 * S::WAVES, S::PER_CU) void product_tile_kernel(
+    int rows, int cols, int depth, int per, const typename M::elem* __restrict__ left, long left_ld,
+    const typename M::elem* __restrict__ right, long right_ld, Epilogue e, typename M::acc* __restrict__ partial,
+    int tiles_m, int tiles_n) {
+  typedef typename M::acc Acc;
+  constexpr int E = sizeof(typename M::elem);
+  constexpr int kDepth = 128 / E;  // elements of depth per stage
+  constexpr int MB = S::MB, NB = S::NB, FR = MB + NB, LC = S::LCOPIES, COPIES = S::LCOPIES + S::RCOPIES;
+  __shared__ __attribute__((aligned(1024))) char smem[2 * S::STAGE];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  // (256 x 256) waves w and w + 4 share a SIMD: the same rows, so the left fragments repeat there
+  const int wm = wave % S::WM, wn = wave / S::WM;
+  int ti, tj;
+  tile_of(blockIdx.x, tiles_m, tiles_n, ti, tj);
+  const long m0 = static_cast<long>(ti) * S::BM;
+  const int n0 = tj * S::BN;
+
+  const int all = (depth + kDepth - 1) / kDepth, kt0 = per * blockIdx.y;
+  const int nk = min(per, all - kt0);
+  // elements of depth in this workgroup's last stage
+  const int last_depth = kt0 + nk == all ? depth - (all - 1) * kDepth : kDepth;
+  const long lstep = LL == kAlongDepth ? 128 : kDepth * left_ld * E;
+  const long rstep = RL == kAlongDepth ? 128 : kDepth * right_ld * E;
+  const char* const lbase = reinterpret_cast<const char*>(left) + (LL == kAlongDepth ? m0 * left_ld : m0) * E + kt0 * lstep;
+  const char* const rbase = reinterpret_cast<const char*>(right) + (RL == kAlongDepth ? n0 * right_ld : n0) * E + kt0 * rstep;
+  const int last_m = static_cast<int>(min(static_cast<long>(rows) - 1 - m0, static_cast<long>(S::BM - 1)));
+  const int last_n = min(cols - 1 - n0, S::BN - 1);
+  unsigned off[COPIES];
+  auto set_offsets = [&](int valid) {
+#pragma unroll
+    for (int j = 0; j < COPIES; ++j) {
+      if (j < LC)
+        off[j] = copy_offset<S::BM, E, LL, false>(wave + S::WAVES * j, lane, static_cast<unsigned>(left_ld), last_m, valid);
+      else
+        off[j] = copy_offset<S::BN, E, RL, true>(wave + S::WAVES * (j - LC), lane, static_cast<unsigned>(right_ld), last_n, valid);
+    }
+  };
+  set_offsets(nk == 1 ? last_depth : kDepth);
+  // copy j (the left operand's first) of stage kt into its buffer
+  auto copy1 = [&](int kt, int j) {
+    char* const dst = smem + (kt & 1) * S::STAGE + (j < LC ? 0 : S::LEFT) + (wave + S::WAVES * (j < LC ? j : j - LC)) * 1024;
+    const char* const src = j < LC ? lbase + kt * lstep : rbase + kt * rstep;
+    // opaque, so that the address stays a scalar base and a 32-bit offset per lane (the compiler
+    // otherwise keeps 64-bit lane pointers through the loop, and spills)
+    unsigned o = off[j];
+    asm volatile("" : "+v"(o));
+    __builtin_amdgcn_global_load_lds(static_cast<const void*>(src + o), (lds_ptr_t)dst, 16, 0, 0);
+  };
+  // zeroes what lies beyond the depth in the last stage's buffer
+  auto clear_tail = [&]() {
+    char* const buf = smem + ((nk - 1) & 1) * S::STAGE;
+    for (int n = tid; n < S::STAGE / 16; n += 64 * S::WAVES) {
+      const bool r = n >= S::LEFT / 16;
+      const int c = r ? n - S::LEFT / 16 : n;
+      bool beyond;
+      if ((r ? RL : LL) == kAlongDepth)
+        beyond = ((c & 7) ^ (r ? chunk_swizzle<true>(c >> 3) : chunk_swizzle<false>(c >> 3))) * (16 / E) >= last_depth;
+      else
+        beyond = c / ((r ? S::BN : S::BM) * E / 16) >= last_depth;
+      if (beyond) *reinterpret_cast<i32x4*>(buf + 16 * n) = i32x4{0, 0, 0, 0};
+    }
+  };
+
+  // fragment reads
+  const int li = lane & 15, lg = lane >> 4;
+  // byte addresses of a lane's first block; the others are 2048 (left) or 512 and 4096 (right)
+  // further along the depth, and along the index, where the block number only meets bits 5 to 8,
+  // differ from it by exclusive or with 32 times theirs
+  int la, ra;
+  if constexpr (LL == kAlongDepth) {
+    const int i = wm * (16 * MB) + li;
+    la = 128 * i + 16 * (lg ^ chunk_swizzle<false>(i));
+  } else {
+    const int k = 8 * lg + (li >> 2);
+    la = S::BM * E * k + 32 * ((wm * MB) ^ block_swizzle<S::BM>(k)) + 8 * (li & 3);
+  }
+  if constexpr (RL == kAlongDepth) {
+    const int i = wn * (16 * NB) + 8 * (li >> 2) + (li & 3);
+    ra = S::LEFT + 128 * i + 16 * (lg ^ chunk_swizzle<true>(i));
+  } else {
+    const int k = 8 * lg + (li >> 2);
+    ra = S::LEFT + S::BN * E * k + 32 * ((wn * NB) ^ block_swizzle<S::BN>(k)) + 8 * (li & 3);
+  }
+  static_assert(S::LEFT % 512 == 0 && S::STAGE % 512 == 0 && (MB & (MB - 1)) == 0 && (NB & (NB - 1)) == 0, "block addresses");
+  auto transposed = [&](int at, int row) {
+    // rows 4 apart have the same swizzle (f leaves bit 2 of k out)
+    const s16x4 x = read_transposed((__attribute__((address_space(3))) s16x4*)(smem + at));
+    const s16x4 y = read_transposed((__attribute__((address_space(3))) s16x4*)(smem + at + 4 * row));
+    i32x4 v;
+    __builtin_memcpy(&v, &x, 8);
+    __builtin_memcpy(reinterpret_cast<char*>(&v) + 8, &y, 8);
+    return v;
+  };
+  auto read1 = [&](int kt, int half, i32x4 (&x)[FR], int g) {
+    const int buf = (kt & 1) * S::STAGE;
+    if (g < MB) {
+      if constexpr (LL == kAlongDepth)
+        x[g] = *reinterpret_cast<const i32x4*>(smem + buf + (la ^ (64 * half)) + 2048 * g);
+      else
+        x[g] = transposed(((buf + la) ^ (32 * g)) + 32 * S::BM * E * half, S::BM * E);
+    } else {
+      if constexpr (RL == kAlongDepth)
+        x[g] = *reinterpret_cast<const i32x4*>(smem + buf + (ra ^ (64 * half)) + 4096 * ((g - MB) >> 1) + 512 * ((g - MB) & 1));
+      else
+        x[g] = transposed(((buf + ra) ^ (32 * (g - MB))) + 32 * S::BN * E * half, S::BN * E);
+    }
+  };
+
+  Acc acc[MB][NB];
+#pragma unroll
+  for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) acc[mb][nb] = Acc{0, 0, 0, 0};
+  i32x4 x0[FR], x1[FR];
+
+  auto mma1 = [&](const i32x4 (&x)[FR], int u) {
+    // block rows in order, the columns of every other one reversed: each step changes one operand
+    const int mb = u / NB, nb = (mb & 1) ? NB - 1 - u % NB : u % NB;
+    acc[mb][nb] = M::mma(x[MB + nb], x[mb], acc[mb][nb]);
+  };
+  constexpr int kMma = MB * NB;
+  // fragment reads after every second MFMA where there are enough of them, else spread evenly
+  auto reads = [&](int kt, int half, i32x4 (&x)[FR], int u) {
+    if constexpr (kMma >= 2 * FR) {
+      if (u % 2 == 0 && u / 2 < FR) read1(kt, half, x, u / 2);
+    } else {
+#pragma unroll
+      for (int g = u * FR / kMma; g < (u + 1) * FR / kMma; ++g) read1(kt, half, x, g);
+    }
+  };
+  // first half of stage kt
+  auto first_half = [&](int kt) {
+    OZ2_WAIT_LGKMCNT(0);
+    OZ2_SCHED_FENCE();
+#pragma unroll
+    for (int u = 0; u < kMma; ++u) {
+      mma1(x0, u);
+      reads(kt, 1, x1, u);
+      OZ2_SCHED_FENCE();
+    }
+  };
+  // second half: copies of stage kt + 2 (if there is one), reads of stage kt + 1 (past the last
+  // stage, of a buffer whose contents are not used)
+  auto second_half = [&](int kt) {
+    const bool more = kt + 2 < nk;
+#pragma unroll
+    for (int u = 0; u < kMma; ++u) {
+      mma1(x1, u);
+      if (u < COPIES) {
+        if (more) copy1(kt + 2, u);
+      }
+      reads(kt + 1, 0, x0, u);
+      OZ2_SCHED_FENCE();
+    }
+  };
+  static_assert(kMma >= COPIES, "a copy per MFMA of the second half");
+  // every wave's copies of the next stage have landed, and every wave is done with this one
+  auto middle = [&]() {
+    OZ2_WAIT_LGKMCNT(0);
+    OZ2_WAIT_VMCNT(0);
+    OZ2_SCHED_FENCE();
+    __builtin_amdgcn_s_barrier();
+    OZ2_SCHED_FENCE();
+  };
+
+  if (nk > 0) {
+    const bool partial = last_depth < kDepth;
+#pragma unroll
+    for (int j = 0; j < COPIES; ++j) copy1(0, j);
+    if (nk > 1) {
+      if (nk == 2) set_offsets(last_depth);
+#pragma unroll
+      for (int j = 0; j < COPIES; ++j) copy1(1, j);
+      OZ2_WAIT_VMCNT(COPIES);
+    } else {
+      OZ2_WAIT_VMCNT(0);
+    }
+    OZ2_SCHED_FENCE();
+    __builtin_amdgcn_s_barrier();
+    if (nk == 1 && partial) {
+      clear_tail();
+      __syncthreads();
+    }
+    OZ2_SCHED_FENCE();
+#pragma unroll
+    for (int g = 0; g < FR; ++g) read1(0, 0, x0, g);
+    OZ2_SCHED_FENCE();
+    // one loop body for every stage: peeled ends cost the compiler a second set of registers
+    for (int kt = 0; kt < nk; ++kt) {
+      first_half(kt);
+      if (kt == nk - 3) set_offsets(last_depth);
+      middle();
+      if (kt == nk - 2 && partial) {
+        clear_tail();
+        __syncthreads();
+      }
+      second_half(kt);
+    }
+    OZ2_WAIT_LGKMCNT(0);
+  }
+
+  // acc[mb][nb][v]: output row m0 + 16 MB wm + 16 mb + lane % 16; column n0 + 16 NB wn +
+  // 32 (nb / 2) + 8 (lane / 16) + 4 (nb % 2) + v, or, right operand along the index,
+  // 16 nb + 4 (lane / 16) + v.
+  // The lane's place is worked out again here rather than kept in registers through the loop.
+  int end_lane = threadIdx.x & 63;
+  asm volatile("" : "+v"(end_lane));
+  const int eg = end_lane >> 4;
+  const long mrow = m0 + wm * (16 * MB) + (end_lane & 15);
+  if constexpr (OUT == kOutPartial) {
+    // the sums as they are, rows of cols rounded up to a multiple of 8
+    const long ld4 = (cols + 7) / 8 * 2;
+    Acc* const dst = partial + blockIdx.y * (rows * ld4);
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb) {
+      const long m = mrow + 16 * mb;
+      if (m >= rows) continue;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        const int n = n0 + wn * (16 * NB) + (RL == kAlongDepth ? 32 * (nb >> 1) + 8 * eg + 4 * (nb & 1) : 16 * nb + 4 * eg);
+        if (n < cols) dst[m * ld4 + n / 4] = acc[mb][nb];
+      }
+    }
+    return;
+  }
+  if constexpr (OUT == kOutPlain && RL == kAlongIndex) {
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb) {
+      const long m = mrow + 16 * mb;
+      if (m >= rows) continue;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        const int n = n0 + wn * (16 * NB) + 16 * nb + 4 * eg;
+        if (n >= cols) continue;
+        T t[4];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) t[v] = static_cast<T>(static_cast<float>(acc[mb][nb][v]));
+        T* const y = static_cast<T*>(e.y) + m * e.ldy + n;
+        if (n + 4 <= cols) {
+          __builtin_memcpy(y, t, sizeof(t));
+        } else {
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            if (n + v < cols) y[v] = t[v];
+        }
+      }
+    }
+  } else {
+    auto finish = [&](auto act, auto full) {
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb) {
+        const long m = mrow + 16 * mb;
+        if (m >= rows) continue;
+#pragma unroll
+        for (int nb = 0; nb < NB; nb += 2) {
+          const int n = n0 + wn * (16 * NB) + 16 * nb + 8 * eg;
+          if (n >= cols) continue;
+          float v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = static_cast<float>(acc[mb][nb + (i >> 2)][i & 3]);
+          finish8<T, decltype(act)::value, decltype(full)::value>(v, e, m, n, cols);
+        }
+      }
+    };
+    if (cols % 8 == 0)
+      with_activation(e.act, [&](auto act) { finish(act, std::true_type{}); });
+    else
+      with_activation(e.act, [&](auto act) { finish(act, std::false_type{}); });
+  }
+}
+
+// Adds up the sums over parts of the depth, in their order, and finishes the outputs: eight
+// columns of one row per thread.
+template <typename M, typename T, int ACT, bool FULL>
+__global__ __launch_bounds__(256) void join_kernel(int rows, int cols, int splits, const typename M::acc* __restrict__ partial,
+                                                   Epilogue e) {
+  const int groups = (cols + 7) / 8;
+  const long plane = static_cast<long>(rows) * groups * 2;
+  const long n = static_cast<long>(blockIdx.x) * 256 + threadIdx.x;
+  if (n >= static_cast<long>(rows) * groups) return;
+  const long m = n / groups;
+  const int g = static_cast<int>(n - m * groups);
+  typename M::acc a = partial[2 * n], b = partial[2 * n + 1];
+#pragma unroll 4
+  for (int s = 1; s < splits; ++s) {
+    a += partial[s * plane + 2 * n];
+    b += partial[s * plane + 2 * n + 1];
+  }
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[i] = static_cast<float>(a[i]);
+    v[4 + i] = static_cast<float>(b[i]);
+  }
+  finish8<T, ACT, FULL>(v, e, m, 8 * g, cols);
+}
+
+template <typename M, typename T, typename S, int LL, int RL, int OUT>
+static hipError_t launch_tile(const Product& pr, hipStream_t st) {
+  typedef typename M::elem E;
+  const int tiles_m = (pr.rows + S::BM - 1) / S::BM, tiles_n = (pr.cols + S::BN - 1) / S::BN;
+  const int stages = (pr.depth * static_cast<int>(sizeof(E)) + 127) / 128;
+  const int per = OUT == kOutPartial ? (stages + pr.plan.splits - 1) / pr.plan.splits : stages;
+  const dim3 grid(static_cast<unsigned>(tiles_m) * static_cast<unsigned>(tiles_n), OUT == kOutPartial ? pr.plan.splits : 1);
+  hipLaunchKernelGGL((product_tile_kernel<M, T, S, LL, RL, OUT>), grid, dim3(64 * S::WAVES), 0, st, pr.rows, pr.cols,
+                     pr.depth, per, static_cast<const E*>(pr.left), pr.left_ld, static_cast<const E*>(pr.right),
+                     pr.right_ld, pr.epi, static_cast<typename M::acc*>(pr.partial), tiles_m, tiles_n);
+  return hipGetLastError();
+}
+
+template <typename M, typename T>
+static hipError_t launch_join(const Product& pr, hipStream_t st) {
+  const long n = static_cast<long>(pr.rows) * ((pr.cols + 7) / 8);
+  const dim3 grid(static_cast<unsigned>((n + 255) / 256));
+  with_activation(pr.epi.act, [&](auto act) {
+    constexpr int ACT = decltype(act)::value;
+    const auto kernel = pr.cols % 8 == 0 ? join_kernel<M, T, ACT, true> : join_kernel<M, T, ACT, false>;
+    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, pr.rows, pr.cols, pr.plan.splits,
+                       static_cast<const typename M::acc*>(pr.partial), pr.epi);
+  });
+  return hipGetLastError();
+}
+
+// One layout of the operands on the planned tile; OUT: kOutEpilogue or kOutPlain.
+template <typename M, typename T, int LL, int RL, int OUT>
+static hipError_t launch_layout(const Product& pr, hipStream_t st) {
+  if (pr.plan.tile == kTile256) return launch_tile<M, T, Tile256, LL, RL, OUT>(pr, st);
+  if (pr.plan.splits > 1) {
+    hipError_t err;
+    if (pr.plan.tile == kTile64 && LL == kAlongDepth)
+      err = launch_tile<M, T, Tile64, kAlongDepth, RL, kOutPartial>(pr, st);
+    else
+      err = launch_tile<M, T, Tile128, LL, RL, kOutPartial>(pr, st);
+    return err != hipSuccess ? err : launch_join<M, T>(pr, st);
+  }
+  if (pr.plan.tile == kTile64 && LL == kAlongDepth) return launch_tile<M, T, Tile64, kAlongDepth, RL, OUT>(pr, st);
+  return launch_tile<M, T, Tile128, LL, RL, OUT>(pr, st);
+}
+
+// ---- few rows ----------------------------------------------------------------------------
+// rows <= 16 MT, both operands along the depth, rows at any alignment.  Reading the right
+// operand (the weights) once is the whole work, so it goes straight from memory to registers:
+// a workgroup takes 16 of its rows and its waves share the depth, each with a contiguous part
+// in steps of 64 bytes per row (one matrix instruction deep), kDeep steps' loads in flight.
+// The waves' sums meet in LDS.  The matrix cores compute 16 MT rows whatever there are: at
+// one instruction per KiB of weights they are far from busy.
+template <typename E>
+__device__ __forceinline__ i32x4 load_chunk(const E* row, int k, int depth) {
+  constexpr int N = 16 / sizeof(E);
+  i32x4 v;
+  if (k + N <= depth) {
+    __builtin_memcpy(&v, row + k, 16);
+  } else {
+    E t[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) t[i] = k + i < depth ? row[k + i] : static_cast<E>(0);
+    __builtin_memcpy(&v, t, 16);
+  }
+  return v;
+}
+
+template <typename M, typename T, int MT, int ACT, bool FULL>
+__global__ __launch_bounds__(1024) void product_few_kernel(int rows, int cols, int depth, int per,
+                                                           const typename M::elem* __restrict__ left, long left_ld,
+                                                           const typename M::elem* __restrict__ right, long right_ld,
+                                                           Epilogue e) {
+  typedef typename M::elem E;
+  typedef typename M::acc Acc;
+  constexpr int kStep = 64 / sizeof(E), kDeep = 8;
+  __shared__ Acc sums[16][MT * 16][4];  // wave, row, four columns each
+  __shared__ float out[MT * 16][16];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int waves = blockDim.x >> 6;
+  const int n0 = blockIdx.x * 16;
+  const int li = lane & 15, k0 = (lane >> 4) * (16 / static_cast<int>(sizeof(E)));
+  const E* const rrow = right + min(n0 + li, cols - 1) * right_ld;
+  const E* lrow[MT];
+#pragma unroll
+  for (int t = 0; t < MT; ++t) lrow[t] = left + static_cast<long>(min(16 * t + li, rows - 1)) * left_ld;
+  Acc acc[MT] = {};
+  // this wave's steps: `per` of them, the last wave's the rest; whole steps in groups of kDeep
+  const int steps = (depth + kStep - 1) / kStep, whole = depth / kStep;
+  const int s1 = min((wave + 1) * per, steps);
+  int s = wave * per;
+  for (; s + kDeep <= min(s1, whole); s += kDeep) {
+    i32x4 w[kDeep], x[MT][kDeep];
+#pragma unroll
+    for (int j = 0; j < kDeep; ++j) __builtin_memcpy(&w[j], rrow + (s + j) * kStep + k0, 16);
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int j = 0; j < kDeep; ++j) __builtin_memcpy(&x[t][j], lrow[t] + (s + j) * kStep + k0, 16);
+#pragma unroll
+    for (int j = 0; j < kDeep; ++j)
+#pragma unroll
+      for (int t = 0; t < MT; ++t) acc[t] = M::mma(w[j], x[t][j], acc[t]);
+  }
+  for (; s < s1; ++s) {
+    const i32x4 w = load_chunk(rrow, s * kStep + k0, depth);
+#pragma unroll
+    for (int t = 0; t < MT; ++t) acc[t] = M::mma(w, load_chunk(lrow[t], s * kStep + k0, depth), acc[t]);
+  }
+#pragma unroll
+  for (int t = 0; t < MT; ++t) sums[wave][16 * t + li][lane >> 4] = acc[t];
+  __syncthreads();
+  for (int i = threadIdx.x; i < MT * 16 * 4; i += blockDim.x) {
+    Acc a = sums[0][i >> 2][i & 3];
+    for (int w = 1; w < waves; ++w) a += sums[w][i >> 2][i & 3];
+#pragma unroll
+    for (int v = 0; v < 4; ++v) out[i >> 2][4 * (i & 3) + v] = static_cast<float>(a[v]);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 2 * rows; i += blockDim.x) {
+    const int n = n0 + 8 * (i & 1);
+    if (n >= cols) continue;
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = out[i >> 1][8 * (i & 1) + j];
+    finish8<T, ACT, FULL>(v, e, i >> 1, n, cols);
+  }
+}
+
+template <typename M, typename T, int MT>
+static hipError_t launch_few(const Product& pr, hipStream_t st) {
+  typedef typename M::elem E;
+  const int steps = (pr.depth * static_cast<int>(sizeof(E)) + 63) / 64;
+  // about eight steps a wave (all its loads in flight at once), 4 to 16 waves
+  const int waves = steps >= 128 ? 16 : steps >= 64 ? 8 : 4;
+  const int per = (steps + waves - 1) / waves;
+  with_activation(pr.epi.act, [&](auto act) {
+    constexpr int ACT = decltype(act)::value;
+    const auto kernel = pr.cols % 8 == 0 ? product_few_kernel<M, T, MT, ACT, true> : product_few_kernel<M, T, MT, ACT, false>;
+    hipLaunchKernelGGL(kernel, dim3((pr.cols + 15) / 16), dim3(64 * waves), 0, st, pr.rows, pr.cols, pr.depth, per,
+                       static_cast<const E*>(pr.left), pr.left_ld, static_cast<const E*>(pr.right), pr.right_ld, pr.epi);
+  });
+  return hipGetLastError();
+}
+
+// Every product of one operand type.
+template <typename M, typename T>
+static hipError_t launch_type(const Product& pr, hipStream_t st) {
+  if (!pr.left_along_index && !pr.right_along_index) {
+    if (pr.plan.tile == kFew) return pr.rows <= 16 ? launch_few<M, T, 1>(pr, st) : launch_few<M, T, 2>(pr, st);
+    return launch_layout<M, T, kAlongDepth, kAlongDepth, kOutEpilogue>(pr, st);
+  }
+  if constexpr (sizeof(typename M::elem) == 2) {
+    if (!pr.left_along_index) return launch_layout<M, T, kAlongDepth, kAlongIndex, kOutPlain>(pr, st);
+    if (pr.right_along_index) return launch_layout<M, T, kAlongIndex, kAlongIndex, kOutPlain>(pr, st);
+  }
+  return hipErrorInvalidValue;
+}
+
+}  // namespace oz2

@@ -66,10 +66,10 @@ def test_unsupported_sizes():
 
 
 def test_small_workspace_is_refused():
-    need = oz.ozaki2_linear_workspace_size(oz.OZ2_LINEAR_BWD, oz.OZ2_F16, 8, 16, 24)
+    need = oz.ozaki2_linear_workspace_size(oz.OZ2_LINEAR_BWD | oz.OZ2_LINEAR_ALIGNED, oz.OZ2_F16, 8, 16, 24)
     assert need > 0
     assert call(oz.ozaki2_linear_bwd, BWD, work=0x70000000, work_bytes=need - 1) == oz.OZ2_ERR_WORKSPACE
-    need = oz.ozaki2_linear_workspace_size(oz.OZ2_LINEAR_I8, oz.OZ2_F16, 8, 16, 24)
+    need = oz.ozaki2_linear_workspace_size(oz.OZ2_LINEAR_I8 | oz.OZ2_LINEAR_ALIGNED, oz.OZ2_F16, 8, 16, 24)
     assert need > 0
     assert call(oz.ozaki2_linear_i8, I8, work=0x70000000, work_bytes=need - 1) == oz.OZ2_ERR_WORKSPACE
     assert oz.ozaki2_linear_workspace_size(oz.OZ2_LINEAR_BWD, oz.OZ2_F32, 8, 16, 24) == 0
@@ -80,6 +80,13 @@ def test_small_workspace_is_refused():
         assert call(oz.ozaki2_linear_i8, I8) == oz.OZ2_ERR_WORKSPACE
     finally:
         assert oz.ozaki2_set_workspace(None, 0) == oz.OZ2_OK
+
+
+def test_workspace_sizes_of_empty_products():
+    for call in (oz.OZ2_LINEAR_FWD, oz.OZ2_LINEAR_BWD, oz.OZ2_LINEAR_I8):
+        for sizes in ((0, 16, 24), (40, 0, 24), (40, 16, 0), (0, 0, 0)):
+            for flag in (0, oz.OZ2_LINEAR_ALIGNED):
+                assert oz.ozaki2_linear_workspace_size(call | flag, oz.OZ2_BF16, *sizes) >= 0
 
 
 def test_empty_calls_launch_nothing():
@@ -115,9 +122,7 @@ def test_tensor_wrappers_refuse():
         oz.linear_backward(torch.zeros(4, 5, dtype=torch.float16), x, w, activation="relu")
     with pytest.raises(ValueError, match="needs names"):
         oz.linear_backward(torch.zeros(4, 5, dtype=torch.float16), x, w, needs=("residual",))
-    with pytest.raises(ValueError, match="shape"):
-        oz._rows(x, "x", (4, 7), x)
-    with pytest.raises(ValueError, match="row-major|CUDA"):
-        oz._rows(x.t(), "x", (6, 4), x)
+    with pytest.raises(ValueError):
+        oz.linear(x, torch.zeros(5, 7, dtype=torch.bfloat16))
     with pytest.raises(ValueError, match="float32"):
         oz.quantize_rows(x.double())
