@@ -40,19 +40,25 @@ struct Epilogue {
 };
 
 // Which kernel computes a product, and over how many parts of the depth.
-enum { kTile256 = 0, kTile128 = 1, kTile64 = 2, kFew = 3 };
+enum { kTile256 = 0, kTile128 = 1, kTile64 = 2, kFew8 = 3, kFew16 = 4 };
 struct Plan {
   int tile = kTile128;
   int splits = 1;
 };
 Plan plan_product(bool i8, long rows, long cols, long depth, bool left_along_index, bool right_along_index);
+inline bool few_rows(const Plan& plan) { return plan.tile == kFew8 || plan.tile == kFew16; }
+// Rows few enough for every workgroup to quantise them itself (32 KB of bf16, 16 KB of LDS).
+inline bool quantize_in_product(const Plan& plan, long rows, long depth) {
+  return few_rows(plan) && rows * ((depth + 15) / 16 * 16) <= 16384;
+}
 inline size_t partial_bytes(const Plan& plan, long rows, long cols) {
   return plan.splits > 1 ? 4 * static_cast<size_t>(plan.splits) * rows * ((cols + 7) / 8 * 8) : 0;
 }
 
 // out[m][n] = epilogue(sum_k left(m, k) right(n, k)), m < rows, n < cols, k < depth.  An operand
 // lies along the depth (element (i, k) at i * ld + k) or along its index (at k * ld + i; products
-// without an epilogue only).  Rows must be as rows_aligned says, except for kFew.
+// without an epilogue only).  Rows must be as rows_aligned says, except for
+// kFew8 and kFew16.
 struct Product {
   int type;   // element type of operands (unless int8) and outputs
   bool i8;    // int8 operands
@@ -66,6 +72,7 @@ struct Product {
   Epilogue epi;
   Plan plan;
   void* partial;  // partial_bytes of it
+  bool quantize;  // int8 on kFew8 and kFew16: left is in the outputs' type, and is quantised by the kernel
 };
 
 // Whether the product kernels can take an operand as it lies: every row starts on a 16-byte
@@ -86,8 +93,8 @@ hipError_t launch_dropout_add(int type, int p, int r, const void* x, long ldx, c
                               const Drop& drop, void* y, long ldy, hipStream_t st);
 // dz = drop(dy) act'(z) in the operands' type, its rows padded with zeros to a multiple of 8
 // (skipped when dz is null), and, when db is not
-// null, db = its column sums, by way of part: grad_row_blocks(p) x r floats.
-int grad_row_blocks(int p);
+// null, db = its column sums, by way of part: grad_row_blocks(p, r) x r floats.
+int grad_row_blocks(int p, int r);
 hipError_t launch_grad_rows(int type, int p, int r, const void* dy, long lddy, const void* z, long ldz, int act,
                             const Drop& drop, void* dz, long lddz, void* db, float* part, hipStream_t st);
 // columns q .. fill - 1 of out are set to zero
@@ -228,23 +235,87 @@ __device__ __forceinline__ void drop8(float (&v)[8], const Drop& d, long row, in
   }
 }
 
-// ---- epilogue ------------------------------------------------------------------------------
-// Eight accumulators of row m, columns n .. n + 7 (n a multiple of 8, n < cols).  FULL: the
-// columns are a multiple of 8, so no group is cut (a quarter of the code).
-template <typename T, int ACT, bool FULL>
-__device__ __forceinline__ void finish8(float (&v)[8], const Epilogue& e, long m, int n, int cols) {
-  const int valid = FULL ? 8 : cols - n;
-  float t[8];
-  if (e.xs != nullptr) {
-    const float s = e.xs[m];
-    load8(e.ws + n, valid, t);
+// ---- quantisation ----------------------------------------------------------------------------
+constexpr float kTinyRow = 1e-36f;
+
+// Largest magnitude of eight values; +Inf if one is NaN.
+__device__ __forceinline__ float magnitude8(const float (&v)[8]) {
+  float top = 0.0f;
+  OZ2_UNROLL
+  for (int i = 0; i < 8; ++i) top = v[i] != v[i] ? __builtin_inff() : fmaxf(top, fabsf(v[i]));
+  return top;
+}
+
+__device__ __forceinline__ float wave_max_magnitude(float top) {
+  OZ2_UNROLL
+  for (int off = 32; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
+  return top;
+}
+
+// The factor 127 / top that a row's elements are multiplied with, and its scale `step`.
+__device__ __forceinline__ float quantization(float top, float& step) {
+  const bool finite = top <= 3.4028234e38f, live = finite && top >= kTinyRow;
+  step = live ? top / 127.0f : finite ? 0.0f : __builtin_nanf("");
+  return live ? 127.0f / top : 0.0f;
+}
+
+// The level of one element (0 in a row without a finite scale).
+__device__ __forceinline__ int level(float v, float inv) { return inv != 0.0f ? static_cast<int>(rintf(v * inv)) : 0; }
+
+// Levels of v[0 .. valid) to p, zeros behind them up to `count` (at most 8).
+__device__ __forceinline__ void store_levels(int8_t* p, int count, int valid, const float (&v)[8], float inv) {
+  int8_t t[8];
+  OZ2_UNROLL
+  for (int i = 0; i < 8; ++i) t[i] = static_cast<int8_t>(i < valid ? level(v[i], inv) : 0);
+  if (count >= 8) {
+    __builtin_memcpy(p, t, 8);
+  } else {
     OZ2_UNROLL
-    for (int i = 0; i < 8; ++i) v[i] = v[i] * s * t[i];
+    for (int i = 0; i < 8; ++i)
+      if (i < count) p[i] = t[i];
+  }
+}
+
+// ---- epilogue ------------------------------------------------------------------------------
+// What an epilogue reads for eight columns, as it lies in memory: eight 16-bit elements.
+typedef int raw8 __attribute__((ext_vector_type(4)));
+
+template <typename T, bool FULL>
+__device__ __forceinline__ raw8 load_raw8(const void* base, long at, int valid) {
+  T t[8];
+  const T* const p = static_cast<const T*>(base) + at;
+  if (FULL || valid >= 8) {
+    __builtin_memcpy(t, p, sizeof(t));
+  } else {
+    OZ2_UNROLL
+    for (int i = 0; i < 8; ++i) t[i] = i < valid ? p[i] : static_cast<T>(0.0f);
+  }
+  raw8 r;
+  __builtin_memcpy(&r, t, sizeof(r));
+  return r;
+}
+
+template <typename T>
+__device__ __forceinline__ float raw_element(const raw8& r, int i) {
+  T t[8];
+  __builtin_memcpy(t, &r, sizeof(r));
+  return static_cast<float>(t[i]);
+}
+
+// Eight accumulators of row m, columns n .. n + 7 (n a multiple of 8, n < cols), with the
+// operands of the epilogue already read (those that the Epilogue names).  FULL: the columns
+// are a multiple of 8, so no group is cut (a quarter of the code).
+template <typename T, int ACT, bool FULL>
+__device__ __forceinline__ void finish8(float (&v)[8], const Epilogue& e, long m, int n, int cols, float xs,
+                                        const float (&ws)[8], const raw8& bias, const raw8& res) {
+  const int valid = FULL ? 8 : cols - n;
+  if (e.xs != nullptr) {
+    OZ2_UNROLL
+    for (int i = 0; i < 8; ++i) v[i] = v[i] * xs * ws[i];
   }
   if (e.bias != nullptr) {
-    load8(static_cast<const T*>(e.bias) + n, valid, t);
     OZ2_UNROLL
-    for (int i = 0; i < 8; ++i) v[i] += t[i];
+    for (int i = 0; i < 8; ++i) v[i] += raw_element<T>(bias, i);
   }
   if (e.z != nullptr) store8(static_cast<T*>(e.z) + m * e.ldz + n, valid, v);
   if constexpr (ACT != kActNone) {
@@ -253,11 +324,25 @@ __device__ __forceinline__ void finish8(float (&v)[8], const Epilogue& e, long m
   }
   if (e.drop.t != 0) drop8(v, e.drop, m, cols, n >> 3);
   if (e.res != nullptr) {
-    load8(static_cast<const T*>(e.res) + m * e.ldr + n, valid, t);
     OZ2_UNROLL
-    for (int i = 0; i < 8; ++i) v[i] += t[i];
+    for (int i = 0; i < 8; ++i) v[i] += raw_element<T>(res, i);
   }
   store8(static_cast<T*>(e.y) + m * e.ldy + n, valid, v);
+}
+
+// The same for one group by itself.
+template <typename T, int ACT, bool FULL>
+__device__ __forceinline__ void finish8(float (&v)[8], const Epilogue& e, long m, int n, int cols) {
+  const int valid = FULL ? 8 : cols - n;
+  float xs = 0.0f, ws[8] = {};
+  raw8 bias = {}, res = {};
+  if (e.res != nullptr) res = load_raw8<T, FULL>(e.res, m * e.ldr + n, valid);
+  if (e.bias != nullptr) bias = load_raw8<T, FULL>(e.bias, n, valid);
+  if (e.xs != nullptr) {
+    xs = e.xs[m];
+    load8(e.ws + n, valid, ws);
+  }
+  finish8<T, ACT, FULL>(v, e, m, n, cols, xs, ws, bias, res);
 }
 
 }  // namespace oz2

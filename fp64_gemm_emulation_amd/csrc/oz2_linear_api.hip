@@ -92,7 +92,7 @@ struct FwdWork {
 FwdWork carve_fwd(Carver& c, long p, long q, long r, bool pack_x, bool pack_w) {
   FwdWork w{};
   w.plan = oz2::plan_product(false, p, r, q, false, false);
-  if (w.plan.tile == oz2::kFew) return w;  // takes any rows
+  if (oz2::few_rows(w.plan)) return w;  // takes any rows
   if (pack_x) w.x = c.take(2 * p * oz2::packed_ld(q, 2));
   if (pack_w) w.w = c.take(2 * r * oz2::packed_ld(q, 2));
   w.partial = c.take(oz2::partial_bytes(w.plan, p, r));
@@ -113,7 +113,7 @@ BwdWork carve_bwd(Carver& c, long p, long q, long r, bool make_dz, bool pack_x, 
   if (pack_x) w.x = c.take(2 * p * oz2::packed_ld(q, 2));
   if (pack_w) w.w = c.take(2 * r * oz2::packed_ld(q, 2));
   w.partial = c.take(std::max(oz2::partial_bytes(w.dx, p, q), oz2::partial_bytes(w.dw, r, q)));
-  w.sums = static_cast<float*>(c.take(sizeof(float) * oz2::grad_row_blocks(static_cast<int>(p)) * r));
+  w.sums = static_cast<float*>(c.take(sizeof(float) * oz2::grad_row_blocks(static_cast<int>(p), static_cast<int>(r)) * r));
   return w;
 }
 
@@ -127,9 +127,10 @@ struct I8Work {
 I8Work carve_i8(Carver& c, long p, long q, long r, bool pack_v) {
   I8Work w{};
   w.plan = oz2::plan_product(true, p, r, q, false, false);
+  if (oz2::quantize_in_product(w.plan, p, q)) return w;
   w.q = static_cast<int8_t*>(c.take(p * oz2::packed_ld(q, 1)));
   w.scale = static_cast<float*>(c.take(sizeof(float) * p));
-  if (w.plan.tile == oz2::kFew) return w;  // takes any rows
+  if (oz2::few_rows(w.plan)) return w;  // takes any rows
   if (pack_v) w.v = static_cast<int8_t*>(c.take(r * oz2::packed_ld(q, 1)));
   w.partial = c.take(oz2::partial_bytes(w.plan, p, r));
   return w;
@@ -138,9 +139,9 @@ I8Work carve_i8(Carver& c, long p, long q, long r, bool pack_v) {
 // The call's workspace: the caller's if given, else the library's.
 int workspace(void* work, size_t work_bytes, size_t need, char** base) {
   *base = static_cast<char*>(work);
+  if (reinterpret_cast<uintptr_t>(work) % kAlign != 0) return OZ2_ERR_ARG;
   if (need == 0) return OZ2_OK;
   if (work == nullptr) return oz2::acquire_linear_workspace(need, base);
-  if (reinterpret_cast<uintptr_t>(work) % kAlign != 0) return OZ2_ERR_ARG;
   return work_bytes < need ? OZ2_ERR_WORKSPACE : OZ2_OK;
 }
 
@@ -176,7 +177,7 @@ int ozaki2_linear(int type, int p, int q, int r, const void* X, int ldx, const v
   if (ws.w != nullptr && (rc = status(oz2::launch_pack_rows(2, r, q, W, ldw, ws.w, lp, st))) != OZ2_OK) return rc;
   const bool packed = ws.x != nullptr || ws.w != nullptr;  // then the depth may count its zeros
   oz2::Product pr{type,  false, p, r, packed ? static_cast<int>(lp) : q, ws.x != nullptr ? ws.x : X, ws.x != nullptr ? lp : ldx,
-                  false, ws.w != nullptr ? ws.w : W, ws.w != nullptr ? lp : ldw, false, {}, ws.plan, ws.partial};
+                  false, ws.w != nullptr ? ws.w : W, ws.w != nullptr ? lp : ldw, false, {}, ws.plan, ws.partial, false};
   pr.epi.bias = bias;
   pr.epi.act = act;
   pr.epi.drop = make_drop(dropout);
@@ -238,14 +239,14 @@ int ozaki2_linear_bwd(int type, int p, int q, int r, const void* dY, int lddy, c
   // and X likewise beyond q
   if (want_dx) {
     if (pack_w && (rc = status(oz2::launch_pack_rows(2, r, q, W, ldw, ws.w, lq, st))) != OZ2_OK) return rc;
-    oz2::Product pr{type, false, p, q, r, dz, lddz, false, pack_w ? ws.w : W, pack_w ? lq : ldw, true, {}, ws.dx, ws.partial};
+    oz2::Product pr{type, false, p, q, r, dz, lddz, false, pack_w ? ws.w : W, pack_w ? lq : ldw, true, {}, ws.dx, ws.partial, false};
     pr.epi.y = dX;
     pr.epi.ldy = lddx;
     if ((rc = status(oz2::launch_product(pr, st))) != OZ2_OK) return rc;
   }
   if (want_dw) {
     if (pack_x && (rc = status(oz2::launch_pack_rows(2, p, q, X, ldx, ws.x, lq, st))) != OZ2_OK) return rc;
-    oz2::Product pr{type, false, r, q, p, dz, lddz, true, pack_x ? ws.x : X, pack_x ? lq : ldx, true, {}, ws.dw, ws.partial};
+    oz2::Product pr{type, false, r, q, p, dz, lddz, true, pack_x ? ws.x : X, pack_x ? lq : ldx, true, {}, ws.dw, ws.partial, false};
     pr.epi.y = dW;
     pr.epi.ldy = lddw;
     if ((rc = status(oz2::launch_product(pr, st))) != OZ2_OK) return rc;
@@ -297,11 +298,15 @@ int ozaki2_linear_i8(int type, int p, int q, int r, const void* X, int ldx, cons
   const I8Work ws = carve_i8(c, p, q, r, pack_v);
   const hipStream_t st = static_cast<hipStream_t>(stream);
   const long lq = oz2::packed_ld(q, 1);
-  if ((rc = status(oz2::launch_quantize_rows(type, p, q, X, ldx, ws.q, lq, static_cast<int>(lq), ws.scale, st))) != OZ2_OK) return rc;
+  const bool quantize = ws.q == nullptr;  // in the product
+  if (!quantize) {
+    rc = status(oz2::launch_quantize_rows(type, p, q, X, ldx, ws.q, lq, static_cast<int>(lq), ws.scale, st));
+    if (rc != OZ2_OK) return rc;
+  }
   if (ws.v != nullptr && (rc = status(oz2::launch_pack_rows(1, r, q, V, ldv, ws.v, lq, st))) != OZ2_OK) return rc;
   // where V is read as it lies at any length, so is Q; else both rows end in zeros
-  oz2::Product pr{type,  true, p, r, ws.plan.tile == oz2::kFew ? q : static_cast<int>(lq), ws.q, lq,
-                  false, ws.v != nullptr ? ws.v : V, ws.v != nullptr ? lq : ldv, false, {}, ws.plan, ws.partial};
+  oz2::Product pr{type,  true, p, r, oz2::few_rows(ws.plan) ? q : static_cast<int>(lq), quantize ? X : ws.q, quantize ? ldx : lq,
+                  false, ws.v != nullptr ? ws.v : V, ws.v != nullptr ? lq : ldv, false, {}, ws.plan, ws.partial, quantize};
   pr.epi.bias = bias;
   pr.epi.act = act;
   pr.epi.res = R;

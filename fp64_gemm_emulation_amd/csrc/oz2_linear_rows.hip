@@ -50,26 +50,37 @@ hipError_t launch_dropout_add(int type, int p, int r, const void* x, long ldx, c
   return dropout_add<float>(p, r, x, ldx, res, ldr, drop, y, ldy, st);
 }
 
-// dz = drop(dy) act'(z): a workgroup takes kGradRows rows of 256 columns, a thread eight
+// dz = drop(dy) act'(z): a workgroup takes a block of rows of 256 columns, a thread eight
 // consecutive columns of every eighth row.  Column sums are of the unrounded f32 values, in
 // a fixed order: over the thread's rows, over the eight threads of a column group, and (in
 // column_sums_kernel) over the row blocks.
-constexpr int kGradRows = 64;
 constexpr int kGradCols = 256;
 
-int grad_row_blocks(int p) { return (p + kGradRows - 1) / kGradRows; }
+// Rows per block: as many, up to 256, as leave 1024 workgroups (four per CU), for fewer
+// partial sums; at least 16.
+static int grad_block_rows(int p, int r) {
+  const long col_blocks = (static_cast<long>(r) + kGradCols - 1) / kGradCols;
+  int rows = 256;
+  while (rows > 16 && (p + rows - 1) / rows * col_blocks < 1024) rows /= 2;
+  return rows;
+}
+
+int grad_row_blocks(int p, int r) {
+  const int rows = grad_block_rows(p, r);
+  return (p + rows - 1) / rows;
+}
 
 template <typename T, int ACT>
 __global__ __launch_bounds__(256) void grad_rows_kernel(int p, int r, const T* dy, long lddy, const T* z, long ldz,
-                                                        Drop d, T* dz, long lddz, float* part) {
+                                                        Drop d, T* dz, long lddz, int block_rows, float* part) {
   __shared__ float sums[8][kGradCols];
   const int g = threadIdx.x & 31, rr = threadIdx.x >> 5;
   const int col = blockIdx.y * kGradCols + 8 * g;
   const int valid = r - col;
-  const long row0 = static_cast<long>(blockIdx.x) * kGradRows;
+  const long row0 = static_cast<long>(blockIdx.x) * block_rows;
   float sum[8] = {};
   if (valid > 0) {
-    for (long row = row0 + rr; row < min(row0 + kGradRows, static_cast<long>(p)); row += 8) {
+    for (long row = row0 + rr; row < min(row0 + block_rows, static_cast<long>(p)); row += 8) {
       float v[8], t[8];
       load8(dy + row * lddy + col, valid, v);
       if (d.t != 0) drop8(v, d, row, r, col >> 3);
@@ -95,23 +106,35 @@ __global__ __launch_bounds__(256) void grad_rows_kernel(int p, int r, const T* d
   if (c < r) part[static_cast<long>(blockIdx.x) * r + c] = s;
 }
 
+// 32 columns per workgroup, every eighth row block per thread.
 template <typename T>
 __global__ __launch_bounds__(256) void column_sums_kernel(int blocks, int r, const float* part, T* db) {
-  const int c = blockIdx.x * 256 + threadIdx.x;
-  if (c >= r) return;
+  __shared__ float sums[8][32];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
   float s = 0.0f;
-  for (int b = 0; b < blocks; ++b) s += part[static_cast<long>(b) * r + c];
+  if (c < r) {
+#pragma unroll 4
+    for (int b = w; b < blocks; b += 8) s += part[static_cast<long>(b) * r + c];
+  }
+  sums[w][lane] = s;
+  __syncthreads();
+  if (w != 0 || c >= r) return;
+  s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s += sums[i][lane];
   db[c] = static_cast<T>(s);
 }
 
 template <typename T>
 static hipError_t grad_rows(int p, int r, const void* dy, long lddy, const void* z, long ldz, int act, const Drop& d,
                             void* dz, long lddz, void* db, float* part, hipStream_t st) {
-  const dim3 grid(grad_row_blocks(p), (r + kGradCols - 1) / kGradCols);
+  const dim3 grid(grad_row_blocks(p, r), (r + kGradCols - 1) / kGradCols);
   if (p > 0 && r > 0) {  // without rows the column sums are zeros
     auto launch = [&](auto kernel) {
       hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, p, r, static_cast<const T*>(dy), lddy,
-                         static_cast<const T*>(z), ldz, d, static_cast<T*>(dz), lddz, db != nullptr ? part : nullptr);
+                         static_cast<const T*>(z), ldz, d, static_cast<T*>(dz), lddz,
+                         grad_block_rows(p, r), db != nullptr ? part : nullptr);
     };
     switch (act) {
       case kActRelu: launch(grad_rows_kernel<T, kActRelu>); break;
@@ -124,7 +147,7 @@ static hipError_t grad_rows(int p, int r, const void* dy, long lddy, const void*
     if (err != hipSuccess) return err;
   }
   if (db == nullptr) return hipSuccess;
-  hipLaunchKernelGGL(column_sums_kernel<T>, dim3((r + 255) / 256), dim3(256), 0, st, grad_row_blocks(p), r, part,
+  hipLaunchKernelGGL(column_sums_kernel<T>, dim3((r + 31) / 32), dim3(256), 0, st, grad_row_blocks(p, r), r, part,
                      static_cast<T*>(db));
   return hipGetLastError();
 }
@@ -138,35 +161,47 @@ hipError_t launch_grad_rows(int type, int p, int r, const void* dy, long lddy, c
 // Row quantisation: scale = max|x| / 127, q = rint(x (127 / max|x|)); a row whose
 // largest magnitude is below kTinyRow (127 / it would overflow) is taken for zeros, with scale
 // 0, and one that holds Inf or NaN gets the scale NaN, so its products are NaN.  One
-// workgroup per row.
-constexpr float kTinyRow = 1e-36f;
+// workgroup per row, eight elements per thread at a time; the first kHeld of them stay in
+// registers between the two passes, so rows up to 8192 are read once.
+constexpr int kHeld = 4;
 
 template <typename T>
-__global__ __launch_bounds__(256) void quantize_rows_kernel(int q, const T* x, long ldx, int8_t* out, long ldo, int fill, float* scale) {
+__global__ __launch_bounds__(256) void quantize_rows_kernel(int q, const T* x, long ldx, int8_t* out, long ldo, int fill,
+                                                            float* scale) {
   __shared__ float tops[4];
   const long row = blockIdx.x;
   const T* const src = x + row * ldx;
+  int8_t* const dst = out + row * ldo;
+  float held[kHeld][8], v[8];
   float top = 0.0f;
-  bool bad = false;
-  for (int k = threadIdx.x; k < q; k += 256) {
-    const float a = fabsf(static_cast<float>(src[k]));
-    bad = bad || a != a;
-    top = fmaxf(top, a);
-  }
 #pragma unroll
-  for (int off = 32; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, kWave));
-  if (__any(bad)) top = __builtin_inff();
+  for (int h = 0; h < kHeld; ++h) {
+    const int k = 8 * (threadIdx.x + 256 * h);
+    if (k < q) {
+      load8(src + k, q - k, held[h]);
+      top = fmaxf(top, magnitude8(held[h]));
+    }
+  }
+  for (int k = 8 * (threadIdx.x + 256 * kHeld); k < q; k += 8 * 256) {
+    load8(src + k, q - k, v);
+    top = fmaxf(top, magnitude8(v));
+  }
+  top = wave_max_magnitude(top);
   if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
   __syncthreads();
   top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-  const bool finite = top <= 3.4028234e38f;
-  const float inv = top >= kTinyRow && finite ? 127.0f / top : 0.0f;
-  for (int k = threadIdx.x; k < q; k += 256) {
-    const float v = rintf(static_cast<float>(src[k]) * inv);
-    out[row * ldo + k] = static_cast<int8_t>(finite ? static_cast<int>(v) : 0);
+  float step;
+  const float inv = quantization(top, step);
+#pragma unroll
+  for (int h = 0; h < kHeld; ++h) {
+    const int k = 8 * (threadIdx.x + 256 * h);
+    if (k < fill) store_levels(dst + k, min(fill - k, 8), q - k, held[h], inv);
   }
-  for (int k = q + threadIdx.x; k < fill; k += 256) out[row * ldo + k] = 0;
-  if (threadIdx.x == 0) scale[row] = inv == 0.0f && finite ? 0.0f : finite ? top / 127.0f : __builtin_nanf("");
+  for (int k = 8 * (threadIdx.x + 256 * kHeld); k < fill; k += 8 * 256) {
+    if (k < q) load8(src + k, q - k, v);
+    store_levels(dst + k, min(fill - k, 8), q - k, v, inv);
+  }
+  if (threadIdx.x == 0) scale[row] = step;
 }
 
 hipError_t launch_quantize_rows(int type, int p, int q, const void* x, long ldx, int8_t* out, long ldo, int fill,

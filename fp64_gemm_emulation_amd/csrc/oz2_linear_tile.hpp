@@ -411,19 +411,47 @@ __global__ __launch_bounds__(64 * S::WAVES, S::PER_CU) void product_tile_kernel(
       }
     }
   } else {
+    // Everything the epilogue reads is read first, for all of the wave's groups of eight columns:
+    // the stores may alias it as far as the compiler knows (Y may be R), so it would wait for
+    // each group's loads in turn.
     auto finish = [&](auto act, auto full) {
+      constexpr bool FULL = decltype(full)::value;
+      constexpr int NG = NB / 2;
+      const int nfirst = n0 + wn * (16 * NB) + 8 * eg;
+      raw8 bias[NG] = {}, res[MB][NG] = {};
+      float xs[MB] = {}, ws[NG][8] = {};
+      if (e.res != nullptr) {
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+          for (int g = 0; g < NG; ++g)
+            if (mrow + 16 * mb < rows && nfirst + 32 * g < cols)
+              res[mb][g] = load_raw8<T, FULL>(e.res, (mrow + 16 * mb) * e.ldr + nfirst + 32 * g, cols - nfirst - 32 * g);
+      }
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        const int n = nfirst + 32 * g;
+        if (n >= cols) continue;
+        if (e.bias != nullptr) bias[g] = load_raw8<T, FULL>(e.bias, n, cols - n);
+        if constexpr (E == 1) load8(e.ws + n, FULL ? 8 : cols - n, ws[g]);
+      }
+      if constexpr (E == 1) {
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb)
+          if (mrow + 16 * mb < rows) xs[mb] = e.xs[mrow + 16 * mb];
+      }
 #pragma unroll
       for (int mb = 0; mb < MB; ++mb) {
         const long m = mrow + 16 * mb;
         if (m >= rows) continue;
 #pragma unroll
-        for (int nb = 0; nb < NB; nb += 2) {
-          const int n = n0 + wn * (16 * NB) + 16 * nb + 8 * eg;
+        for (int g = 0; g < NG; ++g) {
+          const int n = nfirst + 32 * g;
           if (n >= cols) continue;
           float v[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = static_cast<float>(acc[mb][nb + (i >> 2)][i & 3]);
-          finish8<T, decltype(act)::value, decltype(full)::value>(v, e, m, n, cols);
+          for (int i = 0; i < 8; ++i) v[i] = static_cast<float>(acc[mb][2 * g + (i >> 2)][i & 3]);
+          finish8<T, decltype(act)::value, FULL>(v, e, m, n, cols, xs[mb], ws[g], bias[g], res[mb][g]);
         }
       }
     };
@@ -446,7 +474,7 @@ __global__ __launch_bounds__(256) void join_kernel(int rows, int cols, int split
   const long m = n / groups;
   const int g = static_cast<int>(n - m * groups);
   typename M::acc a = partial[2 * n], b = partial[2 * n + 1];
-#pragma unroll 4
+#pragma unroll 8
   for (int s = 1; s < splits; ++s) {
     a += partial[s * plane + 2 * n];
     b += partial[s * plane + 2 * n + 1];
@@ -503,12 +531,18 @@ static hipError_t launch_layout(const Product& pr, hipStream_t st) {
 }
 
 // ---- few rows ----------------------------------------------------------------------------
-// rows <= 16 MT, both operands along the depth, rows at any alignment.  Reading the right
+// rows <= R, both operands along the depth, rows at any alignment.  Reading the right
 // operand (the weights) once is the whole work, so it goes straight from memory to registers:
-// a workgroup takes 16 of its rows and its waves share the depth, each with a contiguous part
-// in steps of 64 bytes per row (one matrix instruction deep), kDeep steps' loads in flight.
-// The waves' sums meet in LDS.  The matrix cores compute 16 MT rows whatever there are: at
-// one instruction per KiB of weights they are far from busy.
+// a workgroup takes R of its rows and its waves share the depth, each with a contiguous part
+// in steps, kDeep steps' loads in flight.  The waves' sums meet in LDS.
+// R = 16: a step is 64 bytes per row, one matrix instruction deep.  R = 8: the instruction's
+// 16 rows and columns hold 8 rows twice, 64 bytes further along the second time, on both
+// sides; the two diagonal quarters of its result are then sums over two parts of the depth
+// (the others are not used).  That gives twice the workgroups, and whole cache lines per row.
+// The matrix cores compute R rows whatever there are: at one instruction per KiB of weights
+// they are far from busy.
+// QUANT (int8): the left operand is still in the outputs' type; every workgroup quantises the
+// few rows itself, into LDS, which saves a launch and hides behind the first loads of weights.
 template <typename E>
 __device__ __forceinline__ i32x4 load_chunk(const E* row, int k, int depth) {
   constexpr int N = 16 / sizeof(E);
@@ -524,79 +558,142 @@ __device__ __forceinline__ i32x4 load_chunk(const E* row, int k, int depth) {
   return v;
 }
 
-template <typename M, typename T, int MT, int ACT, bool FULL>
-__global__ __launch_bounds__(1024) void product_few_kernel(int rows, int cols, int depth, int per,
-                                                           const typename M::elem* __restrict__ left, long left_ld,
-                                                           const typename M::elem* __restrict__ right, long right_ld,
-                                                           Epilogue e) {
+constexpr int kFewWaves = 8;
+
+template <typename M, typename T, int R, bool QUANT, int ACT, bool FULL>
+__global__ __launch_bounds__(64 * kFewWaves) void product_few_kernel(int rows, int cols, int depth, int per,
+                                                                     const void* __restrict__ left, long left_ld,
+                                                                     const typename M::elem* __restrict__ right,
+                                                                     long right_ld, Epilogue e) {
   typedef typename M::elem E;
   typedef typename M::acc Acc;
-  constexpr int kStep = 64 / sizeof(E), kDeep = 8;
-  __shared__ Acc sums[16][MT * 16][4];  // wave, row, four columns each
-  __shared__ float out[MT * 16][16];
+  constexpr int G = 16 / R, kStep = G * 64 / sizeof(E), kDeep = 8;
+  __shared__ Acc sums[kFewWaves][16][4];  // wave, column, four rows each of the instruction's result
+  __shared__ float out[R][R];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int waves = blockDim.x >> 6;
-  const int n0 = blockIdx.x * 16;
-  const int li = lane & 15, k0 = (lane >> 4) * (16 / static_cast<int>(sizeof(E)));
-  const E* const rrow = right + min(n0 + li, cols - 1) * right_ld;
-  const E* lrow[MT];
-#pragma unroll
-  for (int t = 0; t < MT; ++t) lrow[t] = left + static_cast<long>(min(16 * t + li, rows - 1)) * left_ld;
-  Acc acc[MT] = {};
+  const int n0 = blockIdx.x * R;
+  const int li = lane & 15;
+  const int k0 = (li / R) * (64 / static_cast<int>(sizeof(E))) + (lane >> 4) * (16 / static_cast<int>(sizeof(E)));
+  const E* const rrow = right + min(n0 + li % R, cols - 1) * right_ld;
+  const int lm = min(li % R, rows - 1);
   // this wave's steps: `per` of them, the last wave's the rest; whole steps in groups of kDeep
   const int steps = (depth + kStep - 1) / kStep, whole = depth / kStep;
-  const int s1 = min((wave + 1) * per, steps);
-  int s = wave * per;
-  for (; s + kDeep <= min(s1, whole); s += kDeep) {
-    i32x4 w[kDeep], x[MT][kDeep];
+  const int s0 = wave * per, s1 = min((wave + 1) * per, steps), s1w = min(s1, whole);
+  i32x4 w[kDeep];
+  auto load_weights = [&](int s) {
 #pragma unroll
     for (int j = 0; j < kDeep; ++j) __builtin_memcpy(&w[j], rrow + (s + j) * kStep + k0, 16);
+  };
+  const bool deep = s0 + kDeep <= s1w;
+  if (deep) load_weights(s0);
+
+  extern __shared__ __attribute__((aligned(16))) int8_t levels[];  // QUANT: rows of `pitch` bytes
+  const int pitch = (depth + 15) / 16 * 16;
+  if constexpr (QUANT) {
+    __shared__ float tops[R][kFewWaves], scales[R];
+    for (int m = 0; m < rows; ++m) {
+      const T* const x = static_cast<const T*>(left) + m * left_ld;
+      float top = 0.0f, v[8];
+      for (int k = 8 * threadIdx.x; k < depth; k += 8 * blockDim.x) {
+        load8(x + k, depth - k, v);
+        top = fmaxf(top, magnitude8(v));
+      }
+      top = wave_max_magnitude(top);
+      if (lane == 0) tops[m][wave] = top;
+    }
+    __syncthreads();
+    for (int m = 0; m < rows; ++m) {
+      const T* const x = static_cast<const T*>(left) + m * left_ld;
+      float top = 0.0f, step, v[8];
+      for (int i = 0; i < waves; ++i) top = fmaxf(top, tops[m][i]);
+      const float inv = quantization(top, step);
+      for (int k = 8 * threadIdx.x; k < pitch; k += 8 * blockDim.x) {
+        if (k < depth) load8(x + k, depth - k, v);
+        store_levels(levels + m * pitch + k, 8, depth - k, v, inv);
+      }
+      if (threadIdx.x == 0) scales[m] = step;
+    }
+    __syncthreads();
+    e.xs = scales;
+  }
+  const E* const lrow = QUANT ? nullptr : static_cast<const E*>(left) + lm * left_ld;
+  auto load_left = [&](int k) {
+    i32x4 v;
+    if constexpr (QUANT)
+      __builtin_memcpy(&v, __builtin_assume_aligned(levels + lm * pitch + k, 16), 16);
+    else
+      __builtin_memcpy(&v, lrow + k, 16);
+    return v;
+  };
+
+  Acc acc = {};
+  int s = s0;
+  if (deep) {
+    // each register of weights is refilled as soon as it is used
+    i32x4 x[kDeep];
+    for (; s + 2 * kDeep <= s1w; s += kDeep) {
 #pragma unroll
-    for (int t = 0; t < MT; ++t)
+      for (int j = 0; j < kDeep; ++j) x[j] = load_left((s + j) * kStep + k0);
 #pragma unroll
-      for (int j = 0; j < kDeep; ++j) __builtin_memcpy(&x[t][j], lrow[t] + (s + j) * kStep + k0, 16);
+      for (int j = 0; j < kDeep; ++j) {
+        acc = M::mma(w[j], x[j], acc);
+        __builtin_memcpy(&w[j], rrow + (s + kDeep + j) * kStep + k0, 16);
+      }
+    }
 #pragma unroll
-    for (int j = 0; j < kDeep; ++j)
+    for (int j = 0; j < kDeep; ++j) x[j] = load_left((s + j) * kStep + k0);
 #pragma unroll
-      for (int t = 0; t < MT; ++t) acc[t] = M::mma(w[j], x[t][j], acc[t]);
+    for (int j = 0; j < kDeep; ++j) acc = M::mma(w[j], x[j], acc);
+    s += kDeep;
   }
   for (; s < s1; ++s) {
-    const i32x4 w = load_chunk(rrow, s * kStep + k0, depth);
-#pragma unroll
-    for (int t = 0; t < MT; ++t) acc[t] = M::mma(w, load_chunk(lrow[t], s * kStep + k0, depth), acc[t]);
+    const int k = s * kStep + k0;
+    i32x4 x = {0, 0, 0, 0};
+    if constexpr (QUANT) {
+      if (k < pitch) x = load_left(k);
+    } else {
+      x = load_chunk(lrow, k, depth);
+    }
+    acc = M::mma(load_chunk(rrow, k, depth), x, acc);
   }
-#pragma unroll
-  for (int t = 0; t < MT; ++t) sums[wave][16 * t + li][lane >> 4] = acc[t];
+  sums[wave][li][lane >> 4] = acc;
   __syncthreads();
-  for (int i = threadIdx.x; i < MT * 16 * 4; i += blockDim.x) {
-    Acc a = sums[0][i >> 2][i & 3];
-    for (int w = 1; w < waves; ++w) a += sums[w][i >> 2][i & 3];
+  for (int i = threadIdx.x; i < R * R; i += blockDim.x) {
+    const int m = i / R, n = i % R;
+    auto a = sums[0][m][n >> 2][n & 3];
+    a = 0;
+    for (int v = 0; v < waves; ++v)
 #pragma unroll
-    for (int v = 0; v < 4; ++v) out[i >> 2][4 * (i & 3) + v] = static_cast<float>(a[v]);
+      for (int g = 0; g < G; ++g) a += sums[v][g * R + m][(g * R + n) >> 2][n & 3];
+    out[m][n] = static_cast<float>(a);
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < 2 * rows; i += blockDim.x) {
-    const int n = n0 + 8 * (i & 1);
-    if (n >= cols) continue;
+  for (int i = threadIdx.x; i < rows * (R / 8); i += blockDim.x) {
+    const int m = i / (R / 8), c = 8 * (i % (R / 8));
+    if (n0 + c >= cols) continue;
     float v[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = out[i >> 1][8 * (i & 1) + j];
-    finish8<T, ACT, FULL>(v, e, i >> 1, n, cols);
+    for (int j = 0; j < 8; ++j) v[j] = out[m][c + j];
+    finish8<T, ACT, FULL>(v, e, m, n0 + c, cols);
   }
 }
 
-template <typename M, typename T, int MT>
+template <typename M, typename T, int R, bool QUANT>
 static hipError_t launch_few(const Product& pr, hipStream_t st) {
   typedef typename M::elem E;
-  const int steps = (pr.depth * static_cast<int>(sizeof(E)) + 63) / 64;
-  // about eight steps a wave (all its loads in flight at once), 4 to 16 waves
-  const int waves = steps >= 128 ? 16 : steps >= 64 ? 8 : 4;
+  const int step = 16 / R * 64;
+  const int steps = (pr.depth * static_cast<int>(sizeof(E)) + step - 1) / step;
+  // eight steps a wave are all in flight at once; eight waves, so that several workgroups share
+  // a CU and one's sums and epilogue overlap another's loads
+  const int waves = steps >= 64 ? 8 : 4;
   const int per = (steps + waves - 1) / waves;
+  const size_t lds = QUANT ? static_cast<size_t>(pr.rows) * ((pr.depth + 15) / 16 * 16) : 0;
   with_activation(pr.epi.act, [&](auto act) {
     constexpr int ACT = decltype(act)::value;
-    const auto kernel = pr.cols % 8 == 0 ? product_few_kernel<M, T, MT, ACT, true> : product_few_kernel<M, T, MT, ACT, false>;
-    hipLaunchKernelGGL(kernel, dim3((pr.cols + 15) / 16), dim3(64 * waves), 0, st, pr.rows, pr.cols, pr.depth, per,
-                       static_cast<const E*>(pr.left), pr.left_ld, static_cast<const E*>(pr.right), pr.right_ld, pr.epi);
+    const auto kernel = pr.cols % 8 == 0 ? product_few_kernel<M, T, R, QUANT, ACT, true> : product_few_kernel<M, T, R, QUANT, ACT, false>;
+    hipLaunchKernelGGL(kernel, dim3((pr.cols + R - 1) / R), dim3(64 * waves), lds, st, pr.rows, pr.cols, pr.depth, per,
+                       pr.left, pr.left_ld, static_cast<const E*>(pr.right), pr.right_ld, pr.epi);
   });
   return hipGetLastError();
 }
@@ -605,7 +702,13 @@ static hipError_t launch_few(const Product& pr, hipStream_t st) {
 template <typename M, typename T>
 static hipError_t launch_type(const Product& pr, hipStream_t st) {
   if (!pr.left_along_index && !pr.right_along_index) {
-    if (pr.plan.tile == kFew) return pr.rows <= 16 ? launch_few<M, T, 1>(pr, st) : launch_few<M, T, 2>(pr, st);
+    if (pr.plan.tile == kFew8 || pr.plan.tile == kFew16) {
+      const bool eight = pr.plan.tile == kFew8;
+      if constexpr (sizeof(typename M::elem) == 1) {
+        if (pr.quantize) return eight ? launch_few<M, T, 8, true>(pr, st) : launch_few<M, T, 16, true>(pr, st);
+      }
+      return eight ? launch_few<M, T, 8, false>(pr, st) : launch_few<M, T, 16, false>(pr, st);
+    }
     return launch_layout<M, T, kAlongDepth, kAlongDepth, kOutEpilogue>(pr, st);
   }
   if constexpr (sizeof(typename M::elem) == 2) {

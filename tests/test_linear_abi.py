@@ -69,15 +69,15 @@ def test_small_workspace_is_refused():
     need = oz.ozaki2_linear_workspace_size(oz.OZ2_LINEAR_BWD | oz.OZ2_LINEAR_ALIGNED, oz.OZ2_F16, 8, 16, 24)
     assert need > 0
     assert call(oz.ozaki2_linear_bwd, BWD, work=0x70000000, work_bytes=need - 1) == oz.OZ2_ERR_WORKSPACE
-    need = oz.ozaki2_linear_workspace_size(oz.OZ2_LINEAR_I8 | oz.OZ2_LINEAR_ALIGNED, oz.OZ2_F16, 8, 16, 24)
+    need = oz.ozaki2_linear_workspace_size(oz.OZ2_LINEAR_I8 | oz.OZ2_LINEAR_ALIGNED, oz.OZ2_F16, 40, 16, 24)
     assert need > 0
-    assert call(oz.ozaki2_linear_i8, I8, work=0x70000000, work_bytes=need - 1) == oz.OZ2_ERR_WORKSPACE
+    assert call(oz.ozaki2_linear_i8, I8, p=40, work=0x70000000, work_bytes=need - 1) == oz.OZ2_ERR_WORKSPACE
     assert oz.ozaki2_linear_workspace_size(oz.OZ2_LINEAR_BWD, oz.OZ2_F32, 8, 16, 24) == 0
     assert oz.ozaki2_linear_workspace_size(oz.OZ2_LINEAR_I8, oz.OZ2_F16, -8, 16, 24) == 0
     # a set workspace serves the call beyond its first 256 bytes
     assert oz.ozaki2_set_workspace(0x70000000, need) == oz.OZ2_OK
     try:
-        assert call(oz.ozaki2_linear_i8, I8) == oz.OZ2_ERR_WORKSPACE
+        assert call(oz.ozaki2_linear_i8, I8, p=40) == oz.OZ2_ERR_WORKSPACE
     finally:
         assert oz.ozaki2_set_workspace(None, 0) == oz.OZ2_OK
 
