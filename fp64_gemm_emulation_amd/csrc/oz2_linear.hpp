@@ -40,7 +40,7 @@ struct Epilogue {
 };
 
 // Which kernel computes a product, and over how many parts of the depth.
-enum { kTile256 = 0, kTile128 = 1, kTile64 = 2, kFew8 = 3, kFew16 = 4 };
+enum { kTile256 = 0, kTile128 = 1, kTile64 = 2, kFew8 = 3, kFew16 = 4, kTile128Deep = 5 };
 struct Plan {
   int tile = kTile128;
   int splits = 1;
@@ -81,8 +81,8 @@ inline bool rows_aligned(const void* ptr, long ld, long len, int elem) {
   return reinterpret_cast<uintptr_t>(ptr) % 16 == 0 && ld * elem % 16 == 0 && len * elem % 16 == 0 &&
          ld * elem < (1L << 24);
 }
-// Row stride of a packed copy: a multiple of 16 bytes.
-inline long packed_ld(long len, int elem) { return (len * elem + 15) / 16 * 16 / elem; }
+// Row stride of a packed copy: a multiple of the cache line.
+inline long packed_ld(long len, int elem) { return (len * elem + 127) / 128 * 128 / elem; }
 hipError_t launch_pack_rows(int elem, long rows, int cols, const void* src, long ld, void* dst, long ld_out, hipStream_t st);
 
 hipError_t launch_product(const Product& pr, hipStream_t st);

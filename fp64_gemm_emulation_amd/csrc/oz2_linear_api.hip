@@ -175,8 +175,8 @@ int ozaki2_linear(int type, int p, int q, int r, const void* X, int ldx, const v
   const long lp = oz2::packed_ld(q, 2);
   if (ws.x != nullptr && (rc = status(oz2::launch_pack_rows(2, p, q, X, ldx, ws.x, lp, st))) != OZ2_OK) return rc;
   if (ws.w != nullptr && (rc = status(oz2::launch_pack_rows(2, r, q, W, ldw, ws.w, lp, st))) != OZ2_OK) return rc;
-  const bool packed = ws.x != nullptr || ws.w != nullptr;  // then the depth may count its zeros
-  oz2::Product pr{type,  false, p, r, packed ? static_cast<int>(lp) : q, ws.x != nullptr ? ws.x : X, ws.x != nullptr ? lp : ldx,
+  // (where q is cut inside 16 bytes, both are packed, with zeros behind)
+  oz2::Product pr{type,  false, p, r, q, ws.x != nullptr ? ws.x : X, ws.x != nullptr ? lp : ldx,
                   false, ws.w != nullptr ? ws.w : W, ws.w != nullptr ? lp : ldw, false, {}, ws.plan, ws.partial, false};
   pr.epi.bias = bias;
   pr.epi.act = act;
@@ -235,8 +235,6 @@ int ozaki2_linear_bwd(int type, int p, int q, int r, const void* dY, int lddy, c
   }
   const void* const dz = make_dz ? ws.dz : dY;
   const long lddz = make_dz ? lr : lddy;
-  // columns beyond r of a packed dZ are zeros, so they may count as depth or as outputs; of W
-  // and X likewise beyond q
   if (want_dx) {
     if (pack_w && (rc = status(oz2::launch_pack_rows(2, r, q, W, ldw, ws.w, lq, st))) != OZ2_OK) return rc;
     oz2::Product pr{type, false, p, q, r, dz, lddz, false, pack_w ? ws.w : W, pack_w ? lq : ldw, true, {}, ws.dx, ws.partial, false};
@@ -304,8 +302,8 @@ int ozaki2_linear_i8(int type, int p, int q, int r, const void* X, int ldx, cons
     if (rc != OZ2_OK) return rc;
   }
   if (ws.v != nullptr && (rc = status(oz2::launch_pack_rows(1, r, q, V, ldv, ws.v, lq, st))) != OZ2_OK) return rc;
-  // where V is read as it lies at any length, so is Q; else both rows end in zeros
-  oz2::Product pr{type,  true, p, r, oz2::few_rows(ws.plan) ? q : static_cast<int>(lq), quantize ? X : ws.q, quantize ? ldx : lq,
+  // (where q is cut inside 16 bytes, V is packed too, or read element by element)
+  oz2::Product pr{type,  true, p, r, q, quantize ? X : ws.q, quantize ? ldx : lq,
                   false, ws.v != nullptr ? ws.v : V, ws.v != nullptr ? lq : ldv, false, {}, ws.plan, ws.partial, quantize};
   pr.epi.bias = bias;
   pr.epi.act = act;

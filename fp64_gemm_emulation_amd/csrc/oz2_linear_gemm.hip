@@ -9,13 +9,14 @@ namespace oz2 {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
-// The plan with the least estimated time, in microseconds.  Measured on bf16 products of 8 to
+// The plan with the least estimated time, in microseconds.  Measured on bf16 products of 17 to
 // 8192 rows, 1024 to 8192 columns and depths 512 to 8192 (the estimates are within 15% there):
-//   a stage (128 bytes of depth) takes 1.5 on a 256 x 256 tile, one to a CU; 0.7 on a
-//   128 x 128 tile alone on a CU and 0.5 each on two or more; 0.4 and 0.3 on a 64 x 128 tile;
-//   a launch with its first loads and its epilogue 5, a join 3, and the partial sums' bytes
+//   a stage (128 bytes of depth) takes 1.55 on a 256 x 256 tile, one to a CU; 0.45 on a
+//   128 x 128 tile alone on a CU and 0.5 each on two or more; 0.27 on a 64 x 128 tile;
+//   a launch with its first loads and its epilogue 5.5, a join 3, and the partial sums' bytes
 //   5 per 25 MB written and read.
-// So few tiles on a long depth are split until the CUs are full, and no further.
+// So few tiles on a long depth are split until the CUs are full, and no further: 1024 x 2048
+// outputs at depth 8192 take 60 in one part, 43.5 in two and 52.5 in four.
 Plan plan_product(bool i8, long rows, long cols, long depth, bool left_along_index, bool right_along_index) {
   constexpr long kCus = 256;
   Plan best{kTile128, 1};
@@ -25,21 +26,26 @@ Plan plan_product(bool i8, long rows, long cols, long depth, bool left_along_ind
   const long stages = (depth * (i8 ? 1 : 2) + 127) / 128;
   auto tiles = [&](long m, long n) { return (rows + m - 1) / m * ((cols + n - 1) / n); };
   auto per_cu = [&](long n) { return (n + kCus - 1) / kCus; };
-  double least = per_cu(tiles(256, 256)) * stages * 1.5 + 5.0;
+  const long n128 = tiles(128, 128), n64 = tiles(64, 128);
+  double least = per_cu(tiles(256, 256)) * stages * 1.55 + 5.5;
   best.tile = kTile256;
   const bool low = rows <= 64 && !left_along_index;
-  const long n = low ? tiles(64, 128) : tiles(128, 128);
-  const double alone = low ? 0.4 : 0.7, shared = low ? 0.3 : 0.5;
   for (const int splits : {1, 2, 3, 4, 6, 8, 11, 16, 22, 32}) {
     if (splits > 1 && 2 * splits > stages) break;
     const long per = (stages + splits - 1) / splits;
     const long used = per > 0 ? (stages + per - 1) / per : 1;  // parts that are not empty
-    const long load = per_cu(n * used);
-    double t = per * (load == 1 ? alone : shared * load) + 5.0;
-    if (used > 1) t += 3.0 + 8e-6 / 5.0 * used * rows * cols;
-    if (t < least) {
+    const double join = used > 1 ? 3.0 + 8e-6 / 5.0 * used * rows * cols : 0.0;
+    auto consider = [&](int tile, double stage_time, long load) {
+      const double t = per * stage_time * load + 5.5 + join;
+      if (t >= least) return;
       least = t;
-      best = Plan{low ? kTile64 : kTile128, static_cast<int>(used)};
+      best = Plan{tile, static_cast<int>(used)};
+    };
+    if (low) {
+      consider(kTile64, 0.27, per_cu(n64 * used));
+    } else {
+      const long load = per_cu(n128 * used);
+      consider(load == 1 ? kTile128Deep : kTile128, load == 1 ? 0.45 : 0.5, load);
     }
   }
   return best;

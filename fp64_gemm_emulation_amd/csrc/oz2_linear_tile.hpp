@@ -72,15 +72,15 @@ __host__ __device__ __forceinline__ void with_activation(int act, F f) {
 // ---- tile kernel ---------------------------------------------------------------------
 // BM x BN outputs per workgroup, its waves in a grid of WM x WN.  Depth advances in
 // stages of 128 bytes, so that every row of an operand along the depth brings whole cache
-// lines; two stages are held in LDS, filled with 1 KiB copies straight from memory.
+// lines; a ring of two or four stages is held in LDS, filled with 1 KiB copies straight from memory.
 //
 // Per stage and wave, two halves of 64 bytes of depth (one matrix instruction deep):
 //   first half:  MFMAs on the first fragments, the second half's fragments read between them;
-//   middle:      every wave has read the stage: wait for the copies of the next stage (issued
-//                one stage ago), barrier;
-//   second half: MFMAs on the second fragments, between them the copies of the stage after
-//                next into the buffer just released, and the next stage's first fragments.
-// So there is one barrier per stage, and a copy has a whole stage of MFMAs to arrive.
+//   middle:      every wave has read the stage: wait for the copies of the next stage, barrier;
+//   second half: MFMAs on the second fragments, between them the copies of the stage one ring
+//                ahead into the buffer just released, and the next stage's first fragments.
+// So there is one barrier per stage, and a copy has the MFMAs of all but one stage of the ring
+// to arrive.
 //
 // LDS layouts and bank conflicts.  Along the depth: rows of 128 bytes, 16-byte chunk c of row
 // i at chunk c ^ s(i).  The 16 lanes that read one chunk of 16 rows then hit 16 different
@@ -93,22 +93,33 @@ __host__ __device__ __forceinline__ void with_activation(int act, F f) {
 // indices, each lane 8 bytes, and each receives one index's 4 depths.  f takes 16 (256
 // elements) or, within either half of the wave, as many as there are blocks (8 or 4) values
 // over the rows one read touches.
-template <int BM_, int BN_, int WM_, int WN_, int PER_CU_>
+// With two groups of waves (GROUPS = 2), each takes one half of every stage for all of the tile
+// and their sums meet in LDS at the end: one wave to a SIMD issues matrix instructions of this
+// size at half rate only, two reach the full rate, and dividing the tile among eight waves
+// instead would read LDS half as much again.
+template <int BM_, int BN_, int WM_, int WN_, int GROUPS_, int RING_, int PER_CU_>
 struct Tile {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, GROUPS = GROUPS_;
+  static constexpr int RING = RING_;            // stages in LDS
   static constexpr int PER_CU = PER_CU_;        // workgroups that fit a CU's LDS
-  static constexpr int WAVES = WM * WN;
+  static constexpr int WAVES = WM * WN * GROUPS;
   static constexpr int MB = BM / (16 * WM);     // 16-row blocks per wave
   static constexpr int NB = BN / (16 * WN);     // 16-column blocks per wave
   static constexpr int LEFT = BM * 128;         // bytes of the left operand's stage, the right one's behind it
   static constexpr int STAGE = (BM + BN) * 128;
   static constexpr int LCOPIES = BM / 8 / WAVES, RCOPIES = BN / 8 / WAVES;  // 1 KiB copies per wave
   static_assert(BM % (8 * WAVES) == 0 && BN % (8 * WAVES) == 0 && NB % 2 == 0, "tile shape");
+  static_assert(RING == 2 || RING == 4, "the waits assume these");
+  static_assert(GROUPS == 1 || (MB % 2 == 0 && 8192 * (MB / 2) * NB <= RING * STAGE), "the groups' exchange");
 };
-// 128 x 64 outputs per wave, two waves to a SIMD
-typedef Tile<256, 256, 2, 4, 1> Tile256;
-typedef Tile<128, 128, 2, 2, 2> Tile128;
-typedef Tile<64, 128, 1, 4, 3> Tile64;
+// 128 x 64 outputs per wave, two waves to a SIMD: a stage is 2048 cycles of MFMAs, enough for the
+// copies of the next to arrive.
+typedef Tile<256, 256, 2, 4, 1, 2, 1> Tile256;
+// Two workgroups to a CU, which have its matrix cores in turn: again 1024 cycles a stage each.
+typedef Tile<128, 128, 2, 2, 1, 2, 2> Tile128;
+// Alone on a CU: a stage is 512 cycles of MFMAs, so three more are under way.
+typedef Tile<128, 128, 2, 2, 2, 4, 1> Tile128Deep;
+typedef Tile<64, 128, 1, 4, 2, 4, 1> Tile64;
 
 // s(i) of an operand along the depth.
 template <bool RIGHT>
@@ -170,11 +181,13 @@ __global__ __launch_bounds__(64 * S::WAVES, S::PER_CU) void product_tile_kernel(
   constexpr int E = sizeof(typename M::elem);
   constexpr int kDepth = 128 / E;  // elements of depth per stage
   constexpr int MB = S::MB, NB = S::NB, FR = MB + NB, LC = S::LCOPIES, COPIES = S::LCOPIES + S::RCOPIES;
-  __shared__ __attribute__((aligned(1024))) char smem[2 * S::STAGE];
+  constexpr int kMask = S::RING - 1;  // stage kt lies in buffer kt & kMask
+  __shared__ __attribute__((aligned(1024))) char smem[S::RING * S::STAGE];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   // (256 x 256) waves w and w + 4 share a SIMD: the same rows, so the left fragments repeat there
-  const int wm = wave % S::WM, wn = wave / S::WM;
+  const int wm = wave % S::WM, wn = wave / S::WM % S::WN;
+  const int group = S::GROUPS == 1 ? 0 : wave / (S::WM * S::WN);
   int ti, tj;
   tile_of(blockIdx.x, tiles_m, tiles_n, ti, tj);
   const long m0 = static_cast<long>(ti) * S::BM;
@@ -200,10 +213,9 @@ __global__ __launch_bounds__(64 * S::WAVES, S::PER_CU) void product_tile_kernel(
         off[j] = copy_offset<S::BN, E, RL, true>(wave + S::WAVES * (j - LC), lane, static_cast<unsigned>(right_ld), last_n, valid);
     }
   };
-  set_offsets(nk == 1 ? last_depth : kDepth);
   // copy j (the left operand's first) of stage kt into its buffer
   auto copy1 = [&](int kt, int j) {
-    char* const dst = smem + (kt & 1) * S::STAGE + (j < LC ? 0 : S::LEFT) + (wave + S::WAVES * (j < LC ? j : j - LC)) * 1024;
+    char* const dst = smem + (kt & kMask) * S::STAGE + (j < LC ? 0 : S::LEFT) + (wave + S::WAVES * (j < LC ? j : j - LC)) * 1024;
     const char* const src = j < LC ? lbase + kt * lstep : rbase + kt * rstep;
     // opaque, so that the address stays a scalar base and a 32-bit offset per lane (the compiler
     // otherwise keeps 64-bit lane pointers through the loop, and spills)
@@ -213,7 +225,7 @@ __global__ __launch_bounds__(64 * S::WAVES, S::PER_CU) void product_tile_kernel(
   };
   // zeroes what lies beyond the depth in the last stage's buffer
   auto clear_tail = [&]() {
-    char* const buf = smem + ((nk - 1) & 1) * S::STAGE;
+    char* const buf = smem + ((nk - 1) & kMask) * S::STAGE;
     for (int n = tid; n < S::STAGE / 16; n += 64 * S::WAVES) {
       const bool r = n >= S::LEFT / 16;
       const int c = r ? n - S::LEFT / 16 : n;
@@ -257,7 +269,7 @@ __global__ __launch_bounds__(64 * S::WAVES, S::PER_CU) void product_tile_kernel(
     return v;
   };
   auto read1 = [&](int kt, int half, i32x4 (&x)[FR], int g) {
-    const int buf = (kt & 1) * S::STAGE;
+    const int buf = (kt & kMask) * S::STAGE;
     if (g < MB) {
       if constexpr (LL == kAlongDepth)
         x[g] = *reinterpret_cast<const i32x4*>(smem + buf + (la ^ (64 * half)) + 2048 * g);
@@ -304,25 +316,41 @@ __global__ __launch_bounds__(64 * S::WAVES, S::PER_CU) void product_tile_kernel(
       OZ2_SCHED_FENCE();
     }
   };
-  // second half: copies of stage kt + 2 (if there is one), reads of stage kt + 1 (past the last
+  // second half: copies of stage kt + RING (if there is one), reads of stage kt + 1 (past the last
   // stage, of a buffer whose contents are not used)
   auto second_half = [&](int kt) {
-    const bool more = kt + 2 < nk;
+    const bool more = kt + S::RING < nk;
 #pragma unroll
     for (int u = 0; u < kMma; ++u) {
       mma1(x1, u);
       if (u < COPIES) {
-        if (more) copy1(kt + 2, u);
+        if (more) copy1(kt + S::RING, u);
       }
       reads(kt + 1, 0, x0, u);
       OZ2_SCHED_FENCE();
     }
   };
   static_assert(kMma >= COPIES, "a copy per MFMA of the second half");
+  // this wave's copies of stage `ready` have landed: of the later ones, those under way (no
+  // more than RING - 1 stages beyond it, of nk in all) may still be
+  auto wait_copies = [&](int ready, int under_way) {
+    const int later = min(under_way, nk - 1 - ready);
+    if (later <= 0)
+      OZ2_WAIT_VMCNT(0);
+    else if (later == 1)
+      OZ2_WAIT_VMCNT(COPIES);
+    else if (later == 2)
+      OZ2_WAIT_VMCNT(2 * COPIES);
+    else
+      OZ2_WAIT_VMCNT(3 * COPIES);
+  };
   // every wave's copies of the next stage have landed, and every wave is done with this one
-  auto middle = [&]() {
+  auto middle = [&](int kt) {
     OZ2_WAIT_LGKMCNT(0);
-    OZ2_WAIT_VMCNT(0);
+    if constexpr (S::RING == 2)
+      OZ2_WAIT_VMCNT(0);
+    else
+      wait_copies(kt + 1, S::RING - 2);
     OZ2_SCHED_FENCE();
     __builtin_amdgcn_s_barrier();
     OZ2_SCHED_FENCE();
@@ -330,16 +358,15 @@ __global__ __launch_bounds__(64 * S::WAVES, S::PER_CU) void product_tile_kernel(
 
   if (nk > 0) {
     const bool partial = last_depth < kDepth;
+    set_offsets(kDepth);
 #pragma unroll
-    for (int j = 0; j < COPIES; ++j) copy1(0, j);
-    if (nk > 1) {
-      if (nk == 2) set_offsets(last_depth);
+    for (int kt = 0; kt < S::RING; ++kt) {
+      if (kt >= nk) break;
+      if (kt == nk - 1) set_offsets(last_depth);
 #pragma unroll
-      for (int j = 0; j < COPIES; ++j) copy1(1, j);
-      OZ2_WAIT_VMCNT(COPIES);
-    } else {
-      OZ2_WAIT_VMCNT(0);
+      for (int j = 0; j < COPIES; ++j) copy1(kt, j);
     }
+    wait_copies(0, S::RING - 1);
     OZ2_SCHED_FENCE();
     __builtin_amdgcn_s_barrier();
     if (nk == 1 && partial) {
@@ -347,50 +374,102 @@ __global__ __launch_bounds__(64 * S::WAVES, S::PER_CU) void product_tile_kernel(
       __syncthreads();
     }
     OZ2_SCHED_FENCE();
+    if constexpr (S::GROUPS == 1) {
 #pragma unroll
-    for (int g = 0; g < FR; ++g) read1(0, 0, x0, g);
-    OZ2_SCHED_FENCE();
-    // one loop body for every stage: peeled ends cost the compiler a second set of registers
-    for (int kt = 0; kt < nk; ++kt) {
-      first_half(kt);
-      if (kt == nk - 3) set_offsets(last_depth);
-      middle();
-      if (kt == nk - 2 && partial) {
-        clear_tail();
-        __syncthreads();
+      for (int g = 0; g < FR; ++g) read1(0, 0, x0, g);
+      OZ2_SCHED_FENCE();
+      // one loop body for every stage: peeled ends cost the compiler a second set of registers
+      for (int kt = 0; kt < nk; ++kt) {
+        first_half(kt);
+        if (kt == nk - 1 - S::RING) set_offsets(last_depth);
+        middle(kt);
+        if (kt == nk - 2 && partial) {
+          clear_tail();
+          __syncthreads();
+        }
+        second_half(kt);
       }
-      second_half(kt);
+    } else {
+#pragma unroll
+      for (int g = 0; g < FR; ++g) read1(0, group, x0, g);
+      OZ2_SCHED_FENCE();
+      // this group's half of a stage: fragments x, reading the next stage's into y
+      auto stage = [&](int kt, const i32x4 (&x)[FR], i32x4 (&y)[FR]) {
+        if (kt == nk - 1 - S::RING) set_offsets(last_depth);
+        middle(kt);
+        if (kt == nk - 2 && partial) {
+          clear_tail();
+          __syncthreads();
+        }
+        const bool more = kt + S::RING < nk;
+#pragma unroll
+        for (int u = 0; u < kMma; ++u) {
+          mma1(x, u);
+          if (u < COPIES) {
+            if (more) copy1(kt + S::RING, u);
+          }
+          reads(kt + 1, group, y, u);
+          OZ2_SCHED_FENCE();
+        }
+      };
+      for (int kt = 0; kt < nk; kt += 2) {
+        stage(kt, x0, x1);
+        if (kt + 1 < nk) stage(kt + 1, x1, x0);
+      }
     }
     OZ2_WAIT_LGKMCNT(0);
   }
+  // Two groups: each gives the other half of its blocks and finishes the other half.
+  constexpr int EMB = S::GROUPS == 1 ? MB : MB / 2;
+  Acc sum[EMB][NB];
+  if constexpr (S::GROUPS == 1) {
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) sum[mb][nb] = acc[mb][nb];
+  } else {
+    Acc* const slots = reinterpret_cast<Acc*>(smem);
+    __syncthreads();
+#pragma unroll
+    for (int mb = 0; mb < EMB; ++mb)
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+        slots[((wave ^ (S::WAVES / 2)) * EMB * NB + mb * NB + nb) * 64 + lane] = group == 0 ? acc[mb + EMB][nb] : acc[mb][nb];
+    __syncthreads();
+#pragma unroll
+    for (int mb = 0; mb < EMB; ++mb)
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+        sum[mb][nb] = (group == 0 ? acc[mb][nb] : acc[mb + EMB][nb]) + slots[(wave * EMB * NB + mb * NB + nb) * 64 + lane];
+  }
 
-  // acc[mb][nb][v]: output row m0 + 16 MB wm + 16 mb + lane % 16; column n0 + 16 NB wn +
+  // sum[mb][nb][v]: output row m0 + 16 MB wm + 16 EMB group + 16 mb + lane % 16; column n0 + 16 NB wn +
   // 32 (nb / 2) + 8 (lane / 16) + 4 (nb % 2) + v, or, right operand along the index,
   // 16 nb + 4 (lane / 16) + v.
   // The lane's place is worked out again here rather than kept in registers through the loop.
   int end_lane = threadIdx.x & 63;
   asm volatile("" : "+v"(end_lane));
   const int eg = end_lane >> 4;
-  const long mrow = m0 + wm * (16 * MB) + (end_lane & 15);
+  const long mrow = m0 + wm * (16 * MB) + group * (16 * EMB) + (end_lane & 15);
   if constexpr (OUT == kOutPartial) {
     // the sums as they are, rows of cols rounded up to a multiple of 8
     const long ld4 = (cols + 7) / 8 * 2;
     Acc* const dst = partial + blockIdx.y * (rows * ld4);
 #pragma unroll
-    for (int mb = 0; mb < MB; ++mb) {
+    for (int mb = 0; mb < EMB; ++mb) {
       const long m = mrow + 16 * mb;
       if (m >= rows) continue;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
         const int n = n0 + wn * (16 * NB) + (RL == kAlongDepth ? 32 * (nb >> 1) + 8 * eg + 4 * (nb & 1) : 16 * nb + 4 * eg);
-        if (n < cols) dst[m * ld4 + n / 4] = acc[mb][nb];
+        if (n < cols) dst[m * ld4 + n / 4] = sum[mb][nb];
       }
     }
     return;
   }
   if constexpr (OUT == kOutPlain && RL == kAlongIndex) {
 #pragma unroll
-    for (int mb = 0; mb < MB; ++mb) {
+    for (int mb = 0; mb < EMB; ++mb) {
       const long m = mrow + 16 * mb;
       if (m >= rows) continue;
 #pragma unroll
@@ -399,7 +478,7 @@ __global__ __launch_bounds__(64 * S::WAVES, S::PER_CU) void product_tile_kernel(
         if (n >= cols) continue;
         T t[4];
 #pragma unroll
-        for (int v = 0; v < 4; ++v) t[v] = static_cast<T>(static_cast<float>(acc[mb][nb][v]));
+        for (int v = 0; v < 4; ++v) t[v] = static_cast<T>(static_cast<float>(sum[mb][nb][v]));
         T* const y = static_cast<T*>(e.y) + m * e.ldy + n;
         if (n + 4 <= cols) {
           __builtin_memcpy(y, t, sizeof(t));
@@ -418,11 +497,11 @@ __global__ __launch_bounds__(64 * S::WAVES, S::PER_CU) void product_tile_kernel(
       constexpr bool FULL = decltype(full)::value;
       constexpr int NG = NB / 2;
       const int nfirst = n0 + wn * (16 * NB) + 8 * eg;
-      raw8 bias[NG] = {}, res[MB][NG] = {};
-      float xs[MB] = {}, ws[NG][8] = {};
+      raw8 bias[NG] = {}, res[EMB][NG] = {};
+      float xs[EMB] = {}, ws[NG][8] = {};
       if (e.res != nullptr) {
 #pragma unroll
-        for (int mb = 0; mb < MB; ++mb)
+        for (int mb = 0; mb < EMB; ++mb)
 #pragma unroll
           for (int g = 0; g < NG; ++g)
             if (mrow + 16 * mb < rows && nfirst + 32 * g < cols)
@@ -437,11 +516,11 @@ __global__ __launch_bounds__(64 * S::WAVES, S::PER_CU) void product_tile_kernel(
       }
       if constexpr (E == 1) {
 #pragma unroll
-        for (int mb = 0; mb < MB; ++mb)
+        for (int mb = 0; mb < EMB; ++mb)
           if (mrow + 16 * mb < rows) xs[mb] = e.xs[mrow + 16 * mb];
       }
 #pragma unroll
-      for (int mb = 0; mb < MB; ++mb) {
+      for (int mb = 0; mb < EMB; ++mb) {
         const long m = mrow + 16 * mb;
         if (m >= rows) continue;
 #pragma unroll
@@ -450,7 +529,7 @@ __global__ __launch_bounds__(64 * S::WAVES, S::PER_CU) void product_tile_kernel(
           if (n >= cols) continue;
           float v[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = static_cast<float>(acc[mb][2 * g + (i >> 2)][i & 3]);
+          for (int i = 0; i < 8; ++i) v[i] = static_cast<float>(sum[mb][2 * g + (i >> 2)][i & 3]);
           finish8<T, decltype(act)::value, FULL>(v, e, m, n, cols, xs[mb], ws[g], bias[g], res[mb][g]);
         }
       }
@@ -515,19 +594,27 @@ static hipError_t launch_join(const Product& pr, hipStream_t st) {
 }
 
 // One layout of the operands on the planned tile; OUT: kOutEpilogue or kOutPlain.
+template <typename M, typename T, typename S, int LL, int RL, int OUT>
+static hipError_t launch_split(const Product& pr, hipStream_t st) {
+  if (pr.plan.splits <= 1) return launch_tile<M, T, S, LL, RL, OUT>(pr, st);
+  const hipError_t err = launch_tile<M, T, S, LL, RL, kOutPartial>(pr, st);
+  return err != hipSuccess ? err : launch_join<M, T>(pr, st);
+}
+
 template <typename M, typename T, int LL, int RL, int OUT>
 static hipError_t launch_layout(const Product& pr, hipStream_t st) {
-  if (pr.plan.tile == kTile256) return launch_tile<M, T, Tile256, LL, RL, OUT>(pr, st);
-  if (pr.plan.splits > 1) {
-    hipError_t err;
-    if (pr.plan.tile == kTile64 && LL == kAlongDepth)
-      err = launch_tile<M, T, Tile64, kAlongDepth, RL, kOutPartial>(pr, st);
-    else
-      err = launch_tile<M, T, Tile128, LL, RL, kOutPartial>(pr, st);
-    return err != hipSuccess ? err : launch_join<M, T>(pr, st);
+  switch (pr.plan.tile) {
+    case kTile256:
+      return launch_tile<M, T, Tile256, LL, RL, OUT>(pr, st);
+    case kTile128:
+      return launch_split<M, T, Tile128, LL, RL, OUT>(pr, st);
+    case kTile128Deep:
+      return launch_split<M, T, Tile128Deep, LL, RL, OUT>(pr, st);
+    case kTile64:
+      if constexpr (LL == kAlongDepth) return launch_split<M, T, Tile64, LL, RL, OUT>(pr, st);
+      break;
   }
-  if (pr.plan.tile == kTile64 && LL == kAlongDepth) return launch_tile<M, T, Tile64, kAlongDepth, RL, OUT>(pr, st);
-  return launch_tile<M, T, Tile128, LL, RL, OUT>(pr, st);
+  return hipErrorInvalidValue;
 }
 
 // ---- few rows ----------------------------------------------------------------------------
