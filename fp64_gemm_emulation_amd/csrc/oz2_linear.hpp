@@ -110,11 +110,33 @@ hipError_t launch_quantize_rows(int type, int p, int q, const void* x, long ldx,
 // ---- eight consecutive elements ------------------------------------------------------
 // Rows may start at any element, so these are unaligned vector accesses (the hardware's
 // unaligned mode) where all eight lie inside the row, and single elements at its end.
-template <typename T>
+// NT: with the non-temporal hint, for data that is read or written once and too large to be
+// found in a cache later.
+typedef int raw8 __attribute__((ext_vector_type(4)));  // eight 16-bit elements as they lie in memory
+typedef raw8 raw8_unaligned __attribute__((aligned(2)));
+
+template <bool NT>
+__device__ __forceinline__ raw8 load16(const void* p) {
+  if constexpr (NT) return __builtin_nontemporal_load(static_cast<const raw8_unaligned*>(p));
+  raw8 r;
+  __builtin_memcpy(&r, p, 16);
+  return r;
+}
+template <bool NT>
+__device__ __forceinline__ void store16(void* p, raw8 r) {
+  if constexpr (NT) __builtin_nontemporal_store(r, static_cast<raw8_unaligned*>(p));
+  else __builtin_memcpy(p, &r, 16);
+}
+
+template <typename T, bool NT = false>
 __device__ __forceinline__ void load8(const T* p, int valid, float (&v)[8]) {
   T t[8];
   if (valid >= 8) {
-    __builtin_memcpy(t, p, sizeof(t));
+    OZ2_UNROLL
+    for (unsigned i = 0; i < sizeof(t) / 16; ++i) {
+      const raw8 r = load16<NT>(reinterpret_cast<const char*>(p) + 16 * i);
+      __builtin_memcpy(reinterpret_cast<char*>(t) + 16 * i, &r, 16);
+    }
   } else {
     OZ2_UNROLL
     for (int i = 0; i < 8; ++i) t[i] = i < valid ? p[i] : static_cast<T>(0.0f);
@@ -123,13 +145,18 @@ __device__ __forceinline__ void load8(const T* p, int valid, float (&v)[8]) {
   for (int i = 0; i < 8; ++i) v[i] = static_cast<float>(t[i]);
 }
 
-template <typename T>
+template <typename T, bool NT = false>
 __device__ __forceinline__ void store8(T* p, int valid, const float (&v)[8]) {
   T t[8];
   OZ2_UNROLL
   for (int i = 0; i < 8; ++i) t[i] = static_cast<T>(v[i]);
   if (valid >= 8) {
-    __builtin_memcpy(p, t, sizeof(t));
+    OZ2_UNROLL
+    for (unsigned i = 0; i < sizeof(t) / 16; ++i) {
+      raw8 r;
+      __builtin_memcpy(&r, reinterpret_cast<const char*>(t) + 16 * i, 16);
+      store16<NT>(reinterpret_cast<char*>(p) + 16 * i, r);
+    }
   } else {
     OZ2_UNROLL
     for (int i = 0; i < 8; ++i)
@@ -277,19 +304,14 @@ __device__ __forceinline__ void store_levels(int8_t* p, int count, int valid, co
 }
 
 // ---- epilogue ------------------------------------------------------------------------------
-// What an epilogue reads for eight columns, as it lies in memory: eight 16-bit elements.
-typedef int raw8 __attribute__((ext_vector_type(4)));
-
-template <typename T, bool FULL>
+// What an epilogue reads for eight columns, as it lies in memory.
+template <typename T, bool FULL, bool NT = false>
 __device__ __forceinline__ raw8 load_raw8(const void* base, long at, int valid) {
-  T t[8];
   const T* const p = static_cast<const T*>(base) + at;
-  if (FULL || valid >= 8) {
-    __builtin_memcpy(t, p, sizeof(t));
-  } else {
-    OZ2_UNROLL
-    for (int i = 0; i < 8; ++i) t[i] = i < valid ? p[i] : static_cast<T>(0.0f);
-  }
+  if (FULL || valid >= 8) return load16<NT>(p);
+  T t[8];
+  OZ2_UNROLL
+  for (int i = 0; i < 8; ++i) t[i] = i < valid ? p[i] : static_cast<T>(0.0f);
   raw8 r;
   __builtin_memcpy(&r, t, sizeof(r));
   return r;
@@ -305,7 +327,7 @@ __device__ __forceinline__ float raw_element(const raw8& r, int i) {
 // Eight accumulators of row m, columns n .. n + 7 (n a multiple of 8, n < cols), with the
 // operands of the epilogue already read (those that the Epilogue names).  FULL: the columns
 // are a multiple of 8, so no group is cut (a quarter of the code).
-template <typename T, int ACT, bool FULL>
+template <typename T, int ACT, bool FULL, bool NT = false>
 __device__ __forceinline__ void finish8(float (&v)[8], const Epilogue& e, long m, int n, int cols, float xs,
                                         const float (&ws)[8], const raw8& bias, const raw8& res) {
   const int valid = FULL ? 8 : cols - n;
@@ -317,7 +339,7 @@ __device__ __forceinline__ void finish8(float (&v)[8], const Epilogue& e, long m
     OZ2_UNROLL
     for (int i = 0; i < 8; ++i) v[i] += raw_element<T>(bias, i);
   }
-  if (e.z != nullptr) store8(static_cast<T*>(e.z) + m * e.ldz + n, valid, v);
+  if (e.z != nullptr) store8<T, NT>(static_cast<T*>(e.z) + m * e.ldz + n, valid, v);
   if constexpr (ACT != kActNone) {
     OZ2_UNROLL
     for (int i = 0; i < 8; ++i) v[i] = activate<ACT>(v[i]);
@@ -327,7 +349,7 @@ __device__ __forceinline__ void finish8(float (&v)[8], const Epilogue& e, long m
     OZ2_UNROLL
     for (int i = 0; i < 8; ++i) v[i] += raw_element<T>(res, i);
   }
-  store8(static_cast<T*>(e.y) + m * e.ldy + n, valid, v);
+  store8<T, NT>(static_cast<T*>(e.y) + m * e.ldy + n, valid, v);
 }
 
 // The same for one group by itself.

@@ -6,9 +6,13 @@
 
 namespace oz2 {
 
+// Matrices above this are read and written with the non-temporal hint: with their like they
+// exceed the 256 MB memory-side cache.
+constexpr double kStreamBytes = 64.0 * (1 << 20);
+
 // y = res + drop(x): one thread per eight consecutive elements of a row, so one generator
 // block per thread.  A workgroup covers cx column groups (a power of two) of 256 / cx rows.
-template <typename T>
+template <typename T, bool NT>
 __global__ __launch_bounds__(256) void dropout_add_kernel(int p, int r, int cx_log2, const T* x, long ldx, const T* res,
                                                           long ldr, Drop d, T* y, long ldy) {
   const int b = (blockIdx.x << cx_log2) + (threadIdx.x & ((1 << cx_log2) - 1));
@@ -18,14 +22,14 @@ __global__ __launch_bounds__(256) void dropout_add_kernel(int p, int r, int cx_l
   for (long row = static_cast<long>(blockIdx.y) * ry + (threadIdx.x >> cx_log2); row < p;
        row += static_cast<long>(gridDim.y) * ry) {
     float v[8], t[8];
-    load8(x + row * ldx + 8 * b, valid, v);
+    load8<T, NT>(x + row * ldx + 8 * b, valid, v);
     if (d.t != 0) drop8(v, d, row, r, b);
     if (res != nullptr) {
-      load8(res + row * ldr + 8 * b, valid, t);
+      load8<T, NT>(res + row * ldr + 8 * b, valid, t);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] += t[i];
     }
-    store8(y + row * ldy + 8 * b, valid, v);
+    store8<T, NT>(y + row * ldy + 8 * b, valid, v);
   }
 }
 
@@ -38,7 +42,8 @@ static hipError_t dropout_add(int p, int r, const void* x, long ldx, const void*
   const int ry = 256 >> cx_log2;
   const long row_blocks = (static_cast<long>(p) + ry - 1) / ry;
   const dim3 grid((groups + (1 << cx_log2) - 1) >> cx_log2, static_cast<unsigned>(row_blocks < 65535 ? row_blocks : 65535));
-  hipLaunchKernelGGL(dropout_add_kernel<T>, grid, dim3(256), 0, st, p, r, cx_log2, static_cast<const T*>(x), ldx,
+  const auto kernel = static_cast<double>(p) * r * sizeof(T) > kStreamBytes ? dropout_add_kernel<T, true> : dropout_add_kernel<T, false>;
+  hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, p, r, cx_log2, static_cast<const T*>(x), ldx,
                      static_cast<const T*>(res), ldr, d, static_cast<T*>(y), ldy);
   return hipGetLastError();
 }
@@ -82,10 +87,10 @@ __global__ __launch_bounds__(256) void grad_rows_kernel(int p, int r, const T* d
   if (valid > 0) {
     for (long row = row0 + rr; row < min(row0 + block_rows, static_cast<long>(p)); row += 8) {
       float v[8], t[8];
-      load8(dy + row * lddy + col, valid, v);
+      load8<T, true>(dy + row * lddy + col, valid, v);
       if (d.t != 0) drop8(v, d, row, r, col >> 3);
       if constexpr (ACT != kActNone) {
-        load8(z + row * ldz + col, valid, t);
+        load8<T, true>(z + row * ldz + col, valid, t);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] *= activation_slope<ACT>(t[i]);
       }
