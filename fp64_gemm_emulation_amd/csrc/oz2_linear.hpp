@@ -7,6 +7,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 namespace oz2 {
 
@@ -46,6 +47,8 @@ struct Plan {
   int splits = 1;
 };
 Plan plan_product(bool i8, long rows, long cols, long depth, bool left_along_index, bool right_along_index);
+// Plans of dX (p x q, depth r) and dW (r x q, depth p); true: for launch_product_pair.
+bool plan_pair(long p, long q, long r, Plan& dx, Plan& dw);
 inline bool few_rows(const Plan& plan) { return plan.tile == kFew8 || plan.tile == kFew16; }
 // Rows few enough for every workgroup to quantise them itself (32 KB of bf16, 16 KB of LDS).
 inline bool quantize_in_product(const Plan& plan, long rows, long depth) {
@@ -83,20 +86,37 @@ inline bool rows_aligned(const void* ptr, long ld, long len, int elem) {
 }
 // Row stride of a packed copy: a multiple of the cache line.
 inline long packed_ld(long len, int elem) { return (len * elem + 127) / 128 * 128 / elem; }
-hipError_t launch_pack_rows(int elem, long rows, int cols, const void* src, long ld, void* dst, long ld_out, hipStream_t st);
+struct PackJob {
+  long rows;
+  int cols;
+  const void* src;
+  long ld;
+  void* dst;
+  long ld_out;
+};
+// One or two operands (either may be null) in one launch.
+hipError_t launch_pack_rows(int elem, const PackJob* a, const PackJob* b, hipStream_t st);
 
 hipError_t launch_product(const Product& pr, hipStream_t st);
+// Both products of a gradient and, where db is not null, the column sums, in one launch; the
+// plans are plan_pair's.
+hipError_t launch_product_pair(int type, const Product& dx, const Product& dw, int p, int r, const float* part, void* db,
+                               hipStream_t st);
+hipError_t launch_pair_bf16(const Product& dx, const Product& dw, int blocks, int r, const float* part, void* db, hipStream_t st);
+hipError_t launch_pair_f16(const Product& dx, const Product& dw, int blocks, int r, const float* part, void* db, hipStream_t st);
 hipError_t launch_product_bf16(const Product& pr, hipStream_t st);
 hipError_t launch_product_f16(const Product& pr, hipStream_t st);
 hipError_t launch_product_i8(const Product& pr, hipStream_t st);
 hipError_t launch_dropout_add(int type, int p, int r, const void* x, long ldx, const void* res, long ldr,
                               const Drop& drop, void* y, long ldy, hipStream_t st);
 // dz = drop(dy) act'(z) in the operands' type, its rows padded with zeros to a multiple of 8
-// (skipped when dz is null), and, when db is not
-// null, db = its column sums, by way of part: grad_row_blocks(p, r) x r floats.
+// (skipped when dz is null), and, when part is not null, its column sums over each of
+// grad_row_blocks(p, r) blocks of rows: part is that many times r floats.  launch_column_sums
+// adds them up into db.
 int grad_row_blocks(int p, int r);
 hipError_t launch_grad_rows(int type, int p, int r, const void* dy, long lddy, const void* z, long ldz, int act,
-                            const Drop& drop, void* dz, long lddz, void* db, float* part, hipStream_t st);
+                            const Drop& drop, void* dz, long lddz, float* part, hipStream_t st);
+hipError_t launch_column_sums(int type, int p, int r, const float* part, void* db, hipStream_t st);
 // columns q .. fill - 1 of out are set to zero
 hipError_t launch_quantize_rows(int type, int p, int q, const void* x, long ldx, int8_t* out, long ldo, int fill,
                                 float* scale, hipStream_t st);
@@ -106,6 +126,18 @@ hipError_t launch_quantize_rows(int type, int p, int q, const void* x, long ldx,
 #else
 #define OZ2_UNROLL
 #endif
+
+// f(activation) for the activation as a compile-time constant.
+template <typename F>
+__host__ __device__ __forceinline__ void with_activation(int act, F f) {
+  switch (act) {
+    case kActRelu: f(std::integral_constant<int, kActRelu>{}); break;
+    case kActGelu: f(std::integral_constant<int, kActGelu>{}); break;
+    case kActGeluTanh: f(std::integral_constant<int, kActGeluTanh>{}); break;
+    case kActSilu: f(std::integral_constant<int, kActSilu>{}); break;
+    default: f(std::integral_constant<int, kActNone>{}); break;
+  }
+}
 
 // ---- eight consecutive elements ------------------------------------------------------
 // Rows may start at any element, so these are unaligned vector accesses (the hardware's
@@ -365,6 +397,30 @@ __device__ __forceinline__ void finish8(float (&v)[8], const Epilogue& e, long m
     load8(e.ws + n, valid, ws);
   }
   finish8<T, ACT, FULL>(v, e, m, n, cols, xs, ws, bias, res);
+}
+
+// ---- column sums ---------------------------------------------------------------------------
+// db = sums over `blocks` partial rows of r columns, kSumColumns columns per workgroup of
+// THREADS threads, in a fixed order; lds: THREADS floats.
+constexpr int kSumColumns = 32;
+
+template <typename T, int THREADS>
+__device__ __forceinline__ void column_sums(float* lds, unsigned wg, int blocks, int r, const float* part, T* db) {
+  constexpr int W = THREADS / kSumColumns;
+  const int lane = threadIdx.x % kSumColumns, w = threadIdx.x / kSumColumns;
+  const int c = static_cast<int>(wg) * kSumColumns + lane;
+  float s = 0.0f;
+  if (c < r) {
+#pragma unroll 4
+    for (int b = w; b < blocks; b += W) s += part[static_cast<long>(b) * r + c];
+  }
+  lds[threadIdx.x] = s;
+  __syncthreads();
+  if (w != 0 || c >= r) return;
+  s = 0.0f;
+  OZ2_UNROLL
+  for (int i = 0; i < W; ++i) s += lds[i * kSumColumns + lane];
+  db[c] = static_cast<T>(s);
 }
 
 }  // namespace oz2

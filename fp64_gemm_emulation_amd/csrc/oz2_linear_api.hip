@@ -100,19 +100,24 @@ FwdWork carve_fwd(Carver& c, long p, long q, long r, bool pack_x, bool pack_w) {
 }
 
 struct BwdWork {
+  bool paired;  // both products in one launch
   oz2::Plan dx, dw;
-  void *dz, *x, *w, *partial;
+  void *dz, *x, *w, *partial_x, *partial_w;
   float* sums;
 };
 
-BwdWork carve_bwd(Carver& c, long p, long q, long r, bool make_dz, bool pack_x, bool pack_w) {
+BwdWork carve_bwd(Carver& c, long p, long q, long r, bool both, bool make_dz, bool pack_x, bool pack_w) {
   BwdWork w{};
-  w.dx = oz2::plan_product(false, p, q, r, false, true);
-  w.dw = oz2::plan_product(false, r, q, p, true, true);
+  w.paired = both && oz2::plan_pair(p, q, r, w.dx, w.dw);
+  if (!w.paired) {
+    w.dx = oz2::plan_product(false, p, q, r, false, true);
+    w.dw = oz2::plan_product(false, r, q, p, true, true);
+  }
   if (make_dz) w.dz = c.take(2 * p * oz2::packed_ld(r, 2));
   if (pack_x) w.x = c.take(2 * p * oz2::packed_ld(q, 2));
   if (pack_w) w.w = c.take(2 * r * oz2::packed_ld(q, 2));
-  w.partial = c.take(std::max(oz2::partial_bytes(w.dx, p, q), oz2::partial_bytes(w.dw, r, q)));
+  w.partial_x = c.take(oz2::partial_bytes(w.dx, p, q));
+  w.partial_w = c.take(oz2::partial_bytes(w.dw, r, q));
   w.sums = static_cast<float*>(c.take(sizeof(float) * oz2::grad_row_blocks(static_cast<int>(p), static_cast<int>(r)) * r));
   return w;
 }
@@ -173,8 +178,9 @@ int ozaki2_linear(int type, int p, int q, int r, const void* X, int ldx, const v
   const FwdWork ws = carve_fwd(c, p, q, r, pack_x, pack_w);
   const hipStream_t st = static_cast<hipStream_t>(stream);
   const long lp = oz2::packed_ld(q, 2);
-  if (ws.x != nullptr && (rc = status(oz2::launch_pack_rows(2, p, q, X, ldx, ws.x, lp, st))) != OZ2_OK) return rc;
-  if (ws.w != nullptr && (rc = status(oz2::launch_pack_rows(2, r, q, W, ldw, ws.w, lp, st))) != OZ2_OK) return rc;
+  const oz2::PackJob jx{p, q, X, ldx, ws.x, lp}, jw{r, q, W, ldw, ws.w, lp};
+  rc = status(oz2::launch_pack_rows(2, ws.x != nullptr ? &jx : nullptr, ws.w != nullptr ? &jw : nullptr, st));
+  if (rc != OZ2_OK) return rc;
   // (where q is cut inside 16 bytes, both are packed, with zeros behind)
   oz2::Product pr{type,  false, p, r, q, ws.x != nullptr ? ws.x : X, ws.x != nullptr ? lp : ldx,
                   false, ws.w != nullptr ? ws.w : W, ws.w != nullptr ? lp : ldw, false, {}, ws.plan, ws.partial, false};
@@ -222,34 +228,32 @@ int ozaki2_linear_bwd(int type, int p, int q, int r, const void* dY, int lddy, c
   const bool pack_x = want_dw && p > 0 && !oz2::rows_aligned(X, ldx, q, 2);
   const bool pack_w = want_dx && r > 0 && !oz2::rows_aligned(W, ldw, q, 2);
   Carver need, c;
-  carve_bwd(need, p, q, r, make_dz, pack_x, pack_w);
+  carve_bwd(need, p, q, r, want_dx && want_dw, make_dz, pack_x, pack_w);
   int rc = workspace(work, work_bytes, need.used, &c.base);
   if (rc != OZ2_OK) return rc;
-  const BwdWork ws = carve_bwd(c, p, q, r, make_dz, pack_x, pack_w);
+  const BwdWork ws = carve_bwd(c, p, q, r, want_dx && want_dw, make_dz, pack_x, pack_w);
   const hipStream_t st = static_cast<hipStream_t>(stream);
   const long lq = oz2::packed_ld(q, 2), lr = oz2::packed_ld(r, 2);
   if (make_dz || want_db) {
     rc = status(oz2::launch_grad_rows(type, p, r, dY, lddy, Z, ldz, act, drop, make_dz ? ws.dz : nullptr, lr,
-                                      want_db ? dbias : nullptr, ws.sums, st));
+                                      want_db ? ws.sums : nullptr, st));
     if (rc != OZ2_OK) return rc;
   }
+  const oz2::PackJob jx{p, q, X, ldx, ws.x, lq}, jw{r, q, W, ldw, ws.w, lq};
+  rc = status(oz2::launch_pack_rows(2, pack_x ? &jx : nullptr, pack_w ? &jw : nullptr, st));
+  if (rc != OZ2_OK) return rc;
   const void* const dz = make_dz ? ws.dz : dY;
   const long lddz = make_dz ? lr : lddy;
-  if (want_dx) {
-    if (pack_w && (rc = status(oz2::launch_pack_rows(2, r, q, W, ldw, ws.w, lq, st))) != OZ2_OK) return rc;
-    oz2::Product pr{type, false, p, q, r, dz, lddz, false, pack_w ? ws.w : W, pack_w ? lq : ldw, true, {}, ws.dx, ws.partial, false};
-    pr.epi.y = dX;
-    pr.epi.ldy = lddx;
-    if ((rc = status(oz2::launch_product(pr, st))) != OZ2_OK) return rc;
-  }
-  if (want_dw) {
-    if (pack_x && (rc = status(oz2::launch_pack_rows(2, p, q, X, ldx, ws.x, lq, st))) != OZ2_OK) return rc;
-    oz2::Product pr{type, false, r, q, p, dz, lddz, true, pack_x ? ws.x : X, pack_x ? lq : ldx, true, {}, ws.dw, ws.partial, false};
-    pr.epi.y = dW;
-    pr.epi.ldy = lddw;
-    if ((rc = status(oz2::launch_product(pr, st))) != OZ2_OK) return rc;
-  }
-  return OZ2_OK;
+  oz2::Product px{type, false, p, q, r, dz, lddz, false, pack_w ? ws.w : W, pack_w ? lq : ldw, true, {}, ws.dx, ws.partial_x, false};
+  px.epi.y = dX;
+  px.epi.ldy = lddx;
+  oz2::Product pw{type, false, r, q, p, dz, lddz, true, pack_x ? ws.x : X, pack_x ? lq : ldx, true, {}, ws.dw, ws.partial_w, false};
+  pw.epi.y = dW;
+  pw.epi.ldy = lddw;
+  if (ws.paired) return status(oz2::launch_product_pair(type, px, pw, p, r, ws.sums, want_db ? dbias : nullptr, st));
+  if (want_db && (rc = status(oz2::launch_column_sums(type, p, r, ws.sums, dbias, st))) != OZ2_OK) return rc;
+  if (want_dx && (rc = status(oz2::launch_product(px, st))) != OZ2_OK) return rc;
+  return want_dw ? status(oz2::launch_product(pw, st)) : OZ2_OK;
 }
 
 int ozaki2_dropout_add(int type, int p, int r, const void* X, int ldx, const void* R, int ldr,
@@ -301,7 +305,8 @@ int ozaki2_linear_i8(int type, int p, int q, int r, const void* X, int ldx, cons
     rc = status(oz2::launch_quantize_rows(type, p, q, X, ldx, ws.q, lq, static_cast<int>(lq), ws.scale, st));
     if (rc != OZ2_OK) return rc;
   }
-  if (ws.v != nullptr && (rc = status(oz2::launch_pack_rows(1, r, q, V, ldv, ws.v, lq, st))) != OZ2_OK) return rc;
+  const oz2::PackJob jv{r, q, V, ldv, ws.v, lq};
+  if ((rc = status(oz2::launch_pack_rows(1, ws.v != nullptr ? &jv : nullptr, nullptr, st))) != OZ2_OK) return rc;
   // (where q is cut inside 16 bytes, V is packed too, or read element by element)
   oz2::Product pr{type,  true, p, r, q, quantize ? X : ws.q, quantize ? ldx : lq,
                   false, ws.v != nullptr ? ws.v : V, ws.v != nullptr ? lq : ldv, false, {}, ws.plan, ws.partial, quantize};
@@ -325,7 +330,13 @@ size_t ozaki2_linear_workspace_size(int call, int type, int p, int q, int r) {
       carve_fwd(c, p, q, r, !aligned, !aligned);
       break;
     case OZ2_LINEAR_BWD:
-      carve_bwd(c, p, q, r, true, !aligned, !aligned);
+      {
+        // with or without both products in one launch, the larger
+        Carver both;
+        carve_bwd(both, p, q, r, true, true, !aligned, !aligned);
+        carve_bwd(c, p, q, r, false, true, !aligned, !aligned);
+        c.used = std::max(c.used, both.used);
+      }
       break;
     case OZ2_LINEAR_I8:
       carve_i8(c, p, q, r, !aligned);

@@ -111,56 +111,40 @@ __global__ __launch_bounds__(256) void grad_rows_kernel(int p, int r, const T* d
   if (c < r) part[static_cast<long>(blockIdx.x) * r + c] = s;
 }
 
-// 32 columns per workgroup, every eighth row block per thread.
 template <typename T>
 __global__ __launch_bounds__(256) void column_sums_kernel(int blocks, int r, const float* part, T* db) {
-  __shared__ float sums[8][32];
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + lane;
-  float s = 0.0f;
-  if (c < r) {
-#pragma unroll 4
-    for (int b = w; b < blocks; b += 8) s += part[static_cast<long>(b) * r + c];
-  }
-  sums[w][lane] = s;
-  __syncthreads();
-  if (w != 0 || c >= r) return;
-  s = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) s += sums[i][lane];
-  db[c] = static_cast<T>(s);
+  __shared__ float lds[256];
+  column_sums<T, 256>(lds, blockIdx.x, blocks, r, part, db);
 }
 
 template <typename T>
-static hipError_t grad_rows(int p, int r, const void* dy, long lddy, const void* z, long ldz, int act, const Drop& d,
-                            void* dz, long lddz, void* db, float* part, hipStream_t st) {
-  const dim3 grid(grad_row_blocks(p, r), (r + kGradCols - 1) / kGradCols);
-  if (p > 0 && r > 0) {  // without rows the column sums are zeros
-    auto launch = [&](auto kernel) {
-      hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, p, r, static_cast<const T*>(dy), lddy,
-                         static_cast<const T*>(z), ldz, d, static_cast<T*>(dz), lddz,
-                         grad_block_rows(p, r), db != nullptr ? part : nullptr);
-    };
-    switch (act) {
-      case kActRelu: launch(grad_rows_kernel<T, kActRelu>); break;
-      case kActGelu: launch(grad_rows_kernel<T, kActGelu>); break;
-      case kActGeluTanh: launch(grad_rows_kernel<T, kActGeluTanh>); break;
-      case kActSilu: launch(grad_rows_kernel<T, kActSilu>); break;
-      default: launch(grad_rows_kernel<T, kActNone>); break;
-    }
-    const hipError_t err = hipGetLastError();
-    if (err != hipSuccess) return err;
-  }
-  if (db == nullptr) return hipSuccess;
-  hipLaunchKernelGGL(column_sums_kernel<T>, dim3((r + 31) / 32), dim3(256), 0, st, grad_row_blocks(p, r), r, part,
+static hipError_t sum_columns(int blocks, int r, const float* part, void* db, hipStream_t st) {
+  hipLaunchKernelGGL(column_sums_kernel<T>, dim3((r + kSumColumns - 1) / kSumColumns), dim3(256), 0, st, blocks, r, part,
                      static_cast<T*>(db));
   return hipGetLastError();
 }
 
+hipError_t launch_column_sums(int type, int p, int r, const float* part, void* db, hipStream_t st) {
+  const int blocks = p > 0 ? grad_row_blocks(p, r) : 0;  // without rows the sums are zeros
+  return type == kTypeBf16 ? sum_columns<bf16>(blocks, r, part, db, st) : sum_columns<f16>(blocks, r, part, db, st);
+}
+
+template <typename T>
+static hipError_t grad_rows(int p, int r, const void* dy, long lddy, const void* z, long ldz, int act, const Drop& d,
+                            void* dz, long lddz, float* part, hipStream_t st) {
+  if (p == 0 || r == 0) return hipSuccess;
+  const dim3 grid(grad_row_blocks(p, r), (r + kGradCols - 1) / kGradCols);
+  with_activation(act, [&](auto a) {
+    hipLaunchKernelGGL((grad_rows_kernel<T, decltype(a)::value>), grid, dim3(256), 0, st, p, r, static_cast<const T*>(dy),
+                       lddy, static_cast<const T*>(z), ldz, d, static_cast<T*>(dz), lddz, grad_block_rows(p, r), part);
+  });
+  return hipGetLastError();
+}
+
 hipError_t launch_grad_rows(int type, int p, int r, const void* dy, long lddy, const void* z, long ldz, int act,
-                            const Drop& drop, void* dz, long lddz, void* db, float* part, hipStream_t st) {
-  if (type == kTypeBf16) return grad_rows<bf16>(p, r, dy, lddy, z, ldz, act, drop, dz, lddz, db, part, st);
-  return grad_rows<f16>(p, r, dy, lddy, z, ldz, act, drop, dz, lddz, db, part, st);
+                            const Drop& drop, void* dz, long lddz, float* part, hipStream_t st) {
+  if (type == kTypeBf16) return grad_rows<bf16>(p, r, dy, lddy, z, ldz, act, drop, dz, lddz, part, st);
+  return grad_rows<f16>(p, r, dy, lddy, z, ldz, act, drop, dz, lddz, part, st);
 }
 
 // Row quantisation: scale = max|x| / 127, q = rint(x (127 / max|x|)); a row whose

@@ -50,24 +50,13 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 // What the tile kernel does with its accumulators: the whole epilogue; rounding and storing
 // only; or storing them as they are, one of several sums over parts of the depth, which
-// join_kernel adds up and finishes.
-enum { kOutEpilogue = 0, kOutPlain = 1, kOutPartial = 2 };
+// join_kernel adds up and finishes; or the third if there is a place for partial sums, else
+// the second.
+enum { kOutEpilogue = 0, kOutPlain = 1, kOutPartial = 2, kOutEither = 3 };
 
 // How an operand lies in memory: along the depth (element (i, k) at i * ld + k), or along its
 // own index (at k * ld + i), as W does in dX = dZ W and both operands do in dW = dZ^T X.
 enum { kAlongDepth = 0, kAlongIndex = 1 };
-
-// f(activation) for the activation as a compile-time constant.
-template <typename F>
-__host__ __device__ __forceinline__ void with_activation(int act, F f) {
-  switch (act) {
-    case kActRelu: f(std::integral_constant<int, kActRelu>{}); break;
-    case kActGelu: f(std::integral_constant<int, kActGelu>{}); break;
-    case kActGeluTanh: f(std::integral_constant<int, kActGeluTanh>{}); break;
-    case kActSilu: f(std::integral_constant<int, kActSilu>{}); break;
-    default: f(std::integral_constant<int, kActNone>{}); break;
-  }
-}
 
 // ---- tile kernel ---------------------------------------------------------------------
 // BM x BN outputs per workgroup, its waves in a grid of WM x WN.  Depth advances in
@@ -178,29 +167,30 @@ __device__ __forceinline__ s16x4 read_transposed(__attribute__((address_space(3)
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16(p);
 }
 
-// Stages kt0 .. kt0 + per - 1 of the depth (as many as there are), kt0 = per * blockIdx.y.
+// One workgroup: tile number wg, stages kt0 .. kt0 + per - 1 of the depth (as many as there
+// are), kt0 = per * part.  smem: RING stages.
 template <typename M, typename T, typename S, int LL, int RL, int OUT>
-__global__ __launch_bounds__(64 * S::WAVES, S::PER_CU) void product_tile_kernel(
-    int rows, int cols, int depth, int per, const typename M::elem* __restrict__ left, long left_ld,
-    const typename M::elem* __restrict__ right, long right_ld, Epilogue e, typename M::acc* __restrict__ partial,
-    int tiles_m, int tiles_n) {
+__device__ __forceinline__ void product_tile(char* smem, unsigned wg, int part, int rows, int cols, int depth, int per,
+                                             const typename M::elem* __restrict__ left, long left_ld,
+                                             const typename M::elem* __restrict__ right, long right_ld,
+                                             const Epilogue& e, typename M::acc* __restrict__ partial, int tiles_m,
+                                             int tiles_n) {
   typedef typename M::acc Acc;
   constexpr int E = sizeof(typename M::elem);
   constexpr int kDepth = S::SB / E;  // elements of depth per stage
   constexpr int MB = S::MB, NB = S::NB, FR = MB + NB, LC = S::LCOPIES, COPIES = S::LCOPIES + S::RCOPIES;
   constexpr int kMask = S::RING - 1;  // stage kt lies in buffer kt & kMask
-  __shared__ __attribute__((aligned(1024))) char smem[S::RING * S::STAGE];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   // (256 x 256) waves w and w + 4 share a SIMD: the same rows, so the left fragments repeat there
   const int wm = wave % S::WM, wn = wave / S::WM % S::WN;
   const int group = S::GROUPS == 1 ? 0 : wave / (S::WM * S::WN);
   int ti, tj;
-  tile_of(blockIdx.x, tiles_m, tiles_n, ti, tj);
+  tile_of(wg, tiles_m, tiles_n, ti, tj);
   const long m0 = static_cast<long>(ti) * S::BM;
   const int n0 = tj * S::BN;
 
-  const int all = (depth + kDepth - 1) / kDepth, kt0 = per * blockIdx.y;
+  const int all = (depth + kDepth - 1) / kDepth, kt0 = per * part;
   const int nk = min(per, all - kt0);
   // elements of depth in this workgroup's last stage
   const int last_depth = kt0 + nk == all ? depth - (all - 1) * kDepth : kDepth;
@@ -460,10 +450,10 @@ __global__ __launch_bounds__(64 * S::WAVES, S::PER_CU) void product_tile_kernel(
   asm volatile("" : "+v"(end_lane));
   const int eg = end_lane >> 4;
   const long mrow = m0 + wm * (16 * MB) + group * (16 * EMB) + (end_lane & 15);
-  if constexpr (OUT == kOutPartial) {
+  if (OUT == kOutPartial || (OUT == kOutEither && partial != nullptr)) {
     // the sums as they are, rows of cols rounded up to a multiple of 8
     const long ld4 = (cols + 7) / 8 * 2;
-    Acc* const dst = partial + blockIdx.y * (rows * ld4);
+    Acc* const dst = partial + part * (rows * ld4);
 #pragma unroll
     for (int mb = 0; mb < EMB; ++mb) {
       const long m = mrow + 16 * mb;
@@ -476,7 +466,8 @@ __global__ __launch_bounds__(64 * S::WAVES, S::PER_CU) void product_tile_kernel(
     }
     return;
   }
-  if constexpr (OUT == kOutPlain && RL == kAlongIndex) {
+  if constexpr (OUT == kOutPlain || OUT == kOutEither) {
+    static_assert(RL == kAlongIndex, "the column order below");
 #pragma unroll
     for (int mb = 0; mb < EMB; ++mb) {
       const long m = mrow + 16 * mb;
@@ -498,7 +489,7 @@ __global__ __launch_bounds__(64 * S::WAVES, S::PER_CU) void product_tile_kernel(
         }
       }
     }
-  } else {
+  } else if constexpr (OUT == kOutEpilogue) {
     // Everything the epilogue reads is read first, for all of the wave's groups of eight columns:
     // the stores may alias it as far as the compiler knows (Y may be R), so it would wait for
     // each group's loads in turn.
@@ -517,7 +508,7 @@ __global__ __launch_bounds__(64 * S::WAVES, S::PER_CU) void product_tile_kernel(
 #pragma unroll
           for (int g = 0; g < NG; ++g)
             if (mrow + 16 * mb < rows && nfirst + 32 * g < cols)
-              res[mb][g] = load_raw8<T, FULL, NT>(e.res, (mrow + 16 * mb) * e.ldr + nfirst + 32 * g, cols - nfirst - 32 * g);
+              res[mb][g] = load_raw8<T, FULL>(e.res, (mrow + 16 * mb) * e.ldr + nfirst + 32 * g, cols - nfirst - 32 * g);
       }
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
@@ -551,6 +542,54 @@ __global__ __launch_bounds__(64 * S::WAVES, S::PER_CU) void product_tile_kernel(
     else
       with_activation(e.act, [&](auto act) { finish(act, std::false_type{}); });
   }
+}
+
+template <typename M, typename T, typename S, int LL, int RL, int OUT>
+__global__ __launch_bounds__(64 * S::WAVES, S::PER_CU) void product_tile_kernel(
+    int rows, int cols, int depth, int per, const typename M::elem* __restrict__ left, long left_ld,
+    const typename M::elem* __restrict__ right, long right_ld, Epilogue e, typename M::acc* __restrict__ partial,
+    int tiles_m, int tiles_n) {
+  __shared__ __attribute__((aligned(1024))) char smem[S::RING * S::STAGE];
+  product_tile<M, T, S, LL, RL, OUT>(smem, blockIdx.x, blockIdx.y, rows, cols, depth, per, left, left_ld, right,
+                                     right_ld, e, partial, tiles_m, tiles_n);
+}
+
+// Two gradient products and the column sums in one launch: dX = dZ W on the first workgroups,
+// dW = dZ^T X on the next, the sums on the last, so that products of too few tiles to fill the
+// CUs fill them together.
+template <typename M>
+struct PairSide {
+  int rows, cols, depth, per, tiles_m, tiles_n, parts;
+  const typename M::elem* left;
+  long left_ld;
+  const typename M::elem* right;
+  long right_ld;
+  Epilogue epi;
+  typename M::acc* partial;  // null: outputs are stored directly
+  unsigned workgroups() const { return static_cast<unsigned>(tiles_m) * tiles_n * parts; }
+};
+
+template <typename M, typename T, typename S>
+__global__ __launch_bounds__(64 * S::WAVES, S::PER_CU) void product_pair_kernel(PairSide<M> dx, PairSide<M> dw, int blocks,
+                                                                                int r, const float* sums, T* db) {
+  __shared__ __attribute__((aligned(1024))) char smem[S::RING * S::STAGE];
+  unsigned wg = blockIdx.x;
+  const unsigned nx = static_cast<unsigned>(dx.tiles_m) * dx.tiles_n, nw = static_cast<unsigned>(dw.tiles_m) * dw.tiles_n;
+  if (wg < nx * dx.parts) {
+    product_tile<M, T, S, kAlongDepth, kAlongIndex, kOutEither>(smem, wg % nx, wg / nx, dx.rows, dx.cols, dx.depth, dx.per,
+                                                                dx.left, dx.left_ld, dx.right, dx.right_ld, dx.epi,
+                                                                dx.partial, dx.tiles_m, dx.tiles_n);
+    return;
+  }
+  wg -= nx * dx.parts;
+  if (wg < nw * dw.parts) {
+    product_tile<M, T, S, kAlongIndex, kAlongIndex, kOutEither>(smem, wg % nw, wg / nw, dw.rows, dw.cols, dw.depth, dw.per,
+                                                                dw.left, dw.left_ld, dw.right, dw.right_ld, dw.epi,
+                                                                dw.partial, dw.tiles_m, dw.tiles_n);
+    return;
+  }
+  wg -= nw * dw.parts;
+  column_sums<T, 64 * S::WAVES>(reinterpret_cast<float*>(smem), wg, blocks, r, sums, db);
 }
 
 // Adds up the sums over parts of the depth, in their order, and finishes the outputs: eight
@@ -603,6 +642,41 @@ static hipError_t launch_join(const Product& pr, hipStream_t st) {
                        static_cast<const typename M::acc*>(pr.partial), pr.epi);
   });
   return hipGetLastError();
+}
+
+template <typename M>
+static PairSide<M> pair_side(const Product& pr) {
+  typedef Tile128Deep S;
+  const int stages = (pr.depth * static_cast<int>(sizeof(typename M::elem)) + S::SB - 1) / S::SB;
+  PairSide<M> side;
+  side.rows = pr.rows;
+  side.cols = pr.cols;
+  side.depth = pr.depth;
+  side.parts = pr.plan.splits;
+  side.per = (stages + side.parts - 1) / side.parts;
+  side.tiles_m = (pr.rows + S::BM - 1) / S::BM;
+  side.tiles_n = (pr.cols + S::BN - 1) / S::BN;
+  side.left = static_cast<const typename M::elem*>(pr.left);
+  side.left_ld = pr.left_ld;
+  side.right = static_cast<const typename M::elem*>(pr.right);
+  side.right_ld = pr.right_ld;
+  side.epi = pr.epi;
+  side.partial = pr.plan.splits > 1 ? static_cast<typename M::acc*>(pr.partial) : nullptr;
+  return side;
+}
+
+template <typename M, typename T>
+static hipError_t launch_pair(const Product& dx, const Product& dw, int blocks, int r, const float* sums, void* db,
+                              hipStream_t st) {
+  typedef Tile128Deep S;
+  const PairSide<M> px = pair_side<M>(dx), pw = pair_side<M>(dw);
+  const unsigned n = px.workgroups() + pw.workgroups() + (db != nullptr ? (r + kSumColumns - 1) / kSumColumns : 0);
+  hipLaunchKernelGGL((product_pair_kernel<M, T, S>), dim3(n), dim3(64 * S::WAVES), 0, st, px, pw, blocks, r, sums,
+                     static_cast<T*>(db));
+  hipError_t err = hipGetLastError();
+  if (err == hipSuccess && dx.plan.splits > 1) err = launch_join<M, T>(dx, st);
+  if (err == hipSuccess && dw.plan.splits > 1) err = launch_join<M, T>(dw, st);
+  return err;
 }
 
 // One layout of the operands on the planned tile; OUT: kOutEpilogue or kOutPlain.
