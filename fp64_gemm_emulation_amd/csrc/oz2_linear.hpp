@@ -50,9 +50,12 @@ Plan plan_product(bool i8, long rows, long cols, long depth, bool left_along_ind
 // Plans of dX (p x q, depth r) and dW (r x q, depth p); true: for launch_product_pair.
 bool plan_pair(long p, long q, long r, Plan& dx, Plan& dw);
 inline bool few_rows(const Plan& plan) { return plan.tile == kFew8 || plan.tile == kFew16; }
-// Rows few enough for every workgroup to quantise them itself (32 KB of bf16, 16 KB of LDS).
+// Whether the workgroups of a product of few rows quantise them themselves: one or two rows,
+// and at most 16 KB of levels.  Against a launch of its own before the product: 14.5 us and
+// 18.5 for one row, 8192 x 8192 weights; 18.1 and 18.7 for two; four rows on 4096 x 4096
+// weights are better quantised once, 10.1 us against 11.5.
 inline bool quantize_in_product(const Plan& plan, long rows, long depth) {
-  return few_rows(plan) && rows * ((depth + 15) / 16 * 16) <= 16384;
+  return few_rows(plan) && rows <= 2 && rows * ((depth + 15) / 16 * 16) <= 16384;
 }
 inline size_t partial_bytes(const Plan& plan, long rows, long cols) {
   return plan.splits > 1 ? 4 * static_cast<size_t>(plan.splits) * rows * ((cols + 7) / 8 * 8) : 0;

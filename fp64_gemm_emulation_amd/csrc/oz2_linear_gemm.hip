@@ -1,6 +1,7 @@
 // oz2_linear_gemm.hip -- which kernel a linear-layer product runs on, and the packing of
 // operands whose rows are not aligned.  The kernels are in oz2_linear_tile.hpp.
 #include <algorithm>
+#include <cmath>
 
 #include "oz2_common.hpp"
 #include "oz2_linear.hpp"
@@ -62,10 +63,24 @@ static Plan plan_tiles(bool i8, long rows, long cols, long depth, bool left_alon
 
 Plan plan_product(bool i8, long rows, long cols, long depth, bool left_along_index, bool right_along_index) {
   if (rows <= 0 || cols <= 0) return Plan{kTile128, 1};  // nothing to compute
-  if (!left_along_index && !right_along_index && rows <= 16)
-    return Plan{rows <= 8 ? kFew8 : kFew16, 1};
   double time;
-  return plan_tiles(i8, rows, cols, depth, left_along_index, right_along_index, &time);
+  const Plan tiles = plan_tiles(i8, rows, cols, depth, left_along_index, right_along_index, &time);
+  if (left_along_index || right_along_index || rows > 16) return tiles;
+  // Few rows.  Eight rows of weights a workgroup give twice the workgroups, sixteen fetch the
+  // left operand half as often: one row, 2048 x 8192 weights 8.6 us against 11.5; eight rows,
+  // 4096 x 4096 weights 10.6 against 8.8.
+  const double bytes = static_cast<double>(cols) * depth * (i8 ? 1 : 2);
+  if (rows <= 8) {
+    // workgroups that quantise: no more than are resident at once (18.0 us with 1024 of them,
+    // 14.5 with 512)
+    if (i8 && quantize_in_product(Plan{kFew8, 1}, rows, depth)) return Plan{cols > 16 * kCus ? kFew16 : kFew8, 1};
+    const bool eight = rows <= 4 || cols < 16 * kCus || bytes / cols <= 4096;
+    return Plan{eight ? kFew8 : kFew16, 1};
+  }
+  // 9 to 16 rows: the weights at 7.5 MB/us, slowed by the left operand's reads beside them and
+  // by too few workgroups, against a tile's time or its weights at 5.2 MB/us
+  const double few = 4.5 + bytes / 7.5e6 * (1.0 + rows / 24.0) * std::sqrt(std::max(1.0, 16.0 * kCus / cols));
+  return few < std::max(time, 4.0 + bytes / 5.2e6) ? Plan{kFew16, 1} : tiles;
 }
 
 // Together the two products take the longer one's parts, or their whole work over all CUs if

@@ -765,11 +765,22 @@ __global__ __launch_bounds__(64 * kFewWaves) void product_few_kernel(int rows, i
   extern __shared__ __attribute__((aligned(16))) int8_t levels[];  // QUANT: rows of `pitch` bytes
   const int pitch = (depth + 15) / 16 * 16;
   if constexpr (QUANT) {
+    // the thread's first kHeld groups of eight of each row stay in registers where there is one row
+    constexpr int kHeld = 2;
     __shared__ float tops[R][kFewWaves], scales[R];
+    float held[kHeld][8], v[8];
     for (int m = 0; m < rows; ++m) {
       const T* const x = static_cast<const T*>(left) + m * left_ld;
-      float top = 0.0f, v[8];
-      for (int k = 8 * threadIdx.x; k < depth; k += 8 * blockDim.x) {
+      float top = 0.0f;
+#pragma unroll
+      for (int h = 0; h < kHeld; ++h) {
+        const int k = 8 * (threadIdx.x + h * blockDim.x);
+        if (k < depth) {
+          load8(x + k, depth - k, held[h]);
+          top = fmaxf(top, magnitude8(held[h]));
+        }
+      }
+      for (int k = 8 * (threadIdx.x + kHeld * blockDim.x); k < depth; k += 8 * blockDim.x) {
         load8(x + k, depth - k, v);
         top = fmaxf(top, magnitude8(v));
       }
@@ -779,10 +790,18 @@ __global__ __launch_bounds__(64 * kFewWaves) void product_few_kernel(int rows, i
     __syncthreads();
     for (int m = 0; m < rows; ++m) {
       const T* const x = static_cast<const T*>(left) + m * left_ld;
-      float top = 0.0f, step, v[8];
+      float top = 0.0f, step;
       for (int i = 0; i < waves; ++i) top = fmaxf(top, tops[m][i]);
       const float inv = quantization(top, step);
-      for (int k = 8 * threadIdx.x; k < pitch; k += 8 * blockDim.x) {
+#pragma unroll
+      for (int h = 0; h < kHeld; ++h) {
+        const int k = 8 * (threadIdx.x + h * blockDim.x);
+        if (k < pitch) {
+          if (rows > 1 && k < depth) load8(x + k, depth - k, held[h]);
+          store_levels(levels + m * pitch + k, 8, depth - k, held[h], inv);
+        }
+      }
+      for (int k = 8 * (threadIdx.x + kHeld * blockDim.x); k < pitch; k += 8 * blockDim.x) {
         if (k < depth) load8(x + k, depth - k, v);
         store_levels(levels + m * pitch + k, 8, depth - k, v, inv);
       }
