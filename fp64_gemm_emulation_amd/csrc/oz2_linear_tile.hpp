@@ -86,40 +86,35 @@ enum { kAlongDepth = 0, kAlongIndex = 1 };
 // and their sums meet in LDS at the end: one wave to a SIMD issues matrix instructions of this
 // size at half rate only, two reach the full rate, and dividing the tile among eight waves
 // instead would read LDS half as much again.
-template <int BM_, int BN_, int WM_, int WN_, int GROUPS_, int SB_, int RING_, int PER_CU_>
+constexpr int kStageBytes = 128;
+
+template <int BM_, int BN_, int WM_, int WN_, int GROUPS_, int RING_, int PER_CU_>
 struct Tile {
-  static constexpr int SB = SB_;                // bytes of depth per stage
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, GROUPS = GROUPS_;
   static constexpr int RING = RING_;            // stages in LDS
   static constexpr int PER_CU = PER_CU_;        // workgroups that fit a CU's LDS
   static constexpr int WAVES = WM * WN * GROUPS;
   static constexpr int MB = BM / (16 * WM);     // 16-row blocks per wave
   static constexpr int NB = BN / (16 * WN);     // 16-column blocks per wave
-  static constexpr int LEFT = BM * SB;          // bytes of the left operand's stage, the right one's behind it
-  static constexpr int STAGE = (BM + BN) * SB;
-  static constexpr int LCOPIES = BM * SB / 1024 / WAVES, RCOPIES = BN * SB / 1024 / WAVES;  // 1 KiB copies per wave
-  static_assert(BM * SB % (1024 * WAVES) == 0 && BN * SB % (1024 * WAVES) == 0 && NB % 2 == 0, "tile shape");
+  static constexpr int LEFT = BM * kStageBytes;          // bytes of the left operand's stage, the right one's behind it
+  static constexpr int STAGE = (BM + BN) * kStageBytes;
+  static constexpr int LCOPIES = BM * kStageBytes / 1024 / WAVES, RCOPIES = BN * kStageBytes / 1024 / WAVES;  // 1 KiB copies per wave
+  static_assert(BM * kStageBytes % (1024 * WAVES) == 0 && BN * kStageBytes % (1024 * WAVES) == 0 && NB % 2 == 0, "tile shape");
   static_assert(RING == 2 || RING == 4, "the waits assume these");
-  static_assert(SB == 128 || (SB == 64 && GROUPS == 1), "a stage is one or two matrix instructions deep");
   static_assert(GROUPS == 1 || (MB % 2 == 0 && 8192 * (MB / 2) * NB <= RING * STAGE), "the groups' exchange");
 };
 // 128 x 64 outputs per wave, two waves to a SIMD: a stage is 2048 cycles of MFMAs, enough for the
 // copies of the next to arrive.
-typedef Tile<256, 256, 2, 4, 1, 128, 2, 1> Tile256;
-// The same with stages of 64 bytes, three of them under way, for two operands along the index,
-// whose stages are whole cache lines at any depth: 213 us against 221 for 8192 x 2048 outputs
-// at depth 8192.  Along the depth it would fetch half lines: 226 us against 203.
-typedef Tile<256, 256, 2, 4, 1, 64, 4, 1> Tile256Index;
+typedef Tile<256, 256, 2, 4, 1, 2, 1> Tile256;
 // Two workgroups to a CU, which have its matrix cores in turn: again 1024 cycles a stage each.
-typedef Tile<128, 128, 2, 2, 1, 128, 2, 2> Tile128;
+typedef Tile<128, 128, 2, 2, 1, 2, 2> Tile128;
 // Alone on a CU: a stage is 512 cycles of MFMAs, so three more are under way.
-typedef Tile<128, 128, 2, 2, 2, 128, 4, 1> Tile128Deep;
-typedef Tile<64, 128, 1, 4, 2, 128, 4, 1> Tile64;
+typedef Tile<128, 128, 2, 2, 2, 4, 1> Tile128Deep;
+typedef Tile<64, 128, 1, 4, 2, 4, 1> Tile64;
 
 // s(i) of an operand along the depth.
-template <int SB, bool RIGHT>
+template <bool RIGHT>
 __device__ __forceinline__ int chunk_swizzle(int i) {
-  if constexpr (SB == 64) return RIGHT ? (i >> 3) & 3 : (i >> 2) & 3;
   return RIGHT ? (((i >> 3) & 3) << 1) | ((i >> 1) & 1) : (i >> 1) & 7;
 }
 // f(k) of an operand along the index, depth rows of B elements.
@@ -132,11 +127,11 @@ __device__ __forceinline__ int block_swizzle(int k) {
 // copies with the 1 KiB unit u.  Of a stage with `valid` elements of depth, chunks beyond them
 // read something inside the operand (and are zeroed in LDS afterwards); so do rows beyond the
 // last, and columns beyond the last chunk, which only reach outputs that are not stored.
-template <int B, int SB, int E, int LAYOUT, bool RIGHT>
+template <int B, int E, int LAYOUT, bool RIGHT>
 __device__ __forceinline__ unsigned copy_offset(int u, int lane, unsigned ld, int last_index, int valid) {
   if constexpr (LAYOUT == kAlongDepth) {
-    const int i = 1024 / SB * u + lane / (SB / 16);
-    const int c = lane % (SB / 16) ^ chunk_swizzle<SB, RIGHT>(i);
+    const int i = 8 * u + (lane >> 3);
+    const int c = (lane & 7) ^ chunk_swizzle<RIGHT>(i);
     return static_cast<unsigned>(min(i, last_index)) * ld * E + (c * (16 / E) < valid ? 16 * c : 0);
   } else {
     constexpr int kRow = B * E, kPerRow = kRow / 16;  // bytes and 16-byte chunks of a depth row
@@ -177,7 +172,7 @@ __device__ __forceinline__ void product_tile(char* smem, unsigned wg, int part, 
                                              int tiles_n) {
   typedef typename M::acc Acc;
   constexpr int E = sizeof(typename M::elem);
-  constexpr int kDepth = S::SB / E;  // elements of depth per stage
+  constexpr int kDepth = kStageBytes / E;  // elements of depth per stage
   constexpr int MB = S::MB, NB = S::NB, FR = MB + NB, LC = S::LCOPIES, COPIES = S::LCOPIES + S::RCOPIES;
   constexpr int kMask = S::RING - 1;  // stage kt lies in buffer kt & kMask
   const int tid = threadIdx.x, lane = tid & 63;
@@ -194,8 +189,8 @@ __device__ __forceinline__ void product_tile(char* smem, unsigned wg, int part, 
   const int nk = min(per, all - kt0);
   // elements of depth in this workgroup's last stage
   const int last_depth = kt0 + nk == all ? depth - (all - 1) * kDepth : kDepth;
-  const long lstep = LL == kAlongDepth ? S::SB : kDepth * left_ld * E;
-  const long rstep = RL == kAlongDepth ? S::SB : kDepth * right_ld * E;
+  const long lstep = LL == kAlongDepth ? kStageBytes : kDepth * left_ld * E;
+  const long rstep = RL == kAlongDepth ? kStageBytes : kDepth * right_ld * E;
   const char* const lbase = reinterpret_cast<const char*>(left) + (LL == kAlongDepth ? m0 * left_ld : m0) * E + kt0 * lstep;
   const char* const rbase = reinterpret_cast<const char*>(right) + (RL == kAlongDepth ? n0 * right_ld : n0) * E + kt0 * rstep;
   const int last_m = static_cast<int>(min(static_cast<long>(rows) - 1 - m0, static_cast<long>(S::BM - 1)));
@@ -205,9 +200,9 @@ __device__ __forceinline__ void product_tile(char* smem, unsigned wg, int part, 
 #pragma unroll
     for (int j = 0; j < COPIES; ++j) {
       if (j < LC)
-        off[j] = copy_offset<S::BM, S::SB, E, LL, false>(wave + S::WAVES * j, lane, static_cast<unsigned>(left_ld), last_m, valid);
+        off[j] = copy_offset<S::BM, E, LL, false>(wave + S::WAVES * j, lane, static_cast<unsigned>(left_ld), last_m, valid);
       else
-        off[j] = copy_offset<S::BN, S::SB, E, RL, true>(wave + S::WAVES * (j - LC), lane, static_cast<unsigned>(right_ld), last_n, valid);
+        off[j] = copy_offset<S::BN, E, RL, true>(wave + S::WAVES * (j - LC), lane, static_cast<unsigned>(right_ld), last_n, valid);
     }
   };
   // copy j (the left operand's first) of stage kt into its buffer
@@ -222,14 +217,14 @@ __device__ __forceinline__ void product_tile(char* smem, unsigned wg, int part, 
   };
   // zeroes what lies beyond the depth in the last stage's buffer
   auto clear_tail = [&]() {
-    constexpr int kChunks = S::SB / 16;
+    constexpr int kChunks = kStageBytes / 16;
     char* const buf = smem + ((nk - 1) & kMask) * S::STAGE;
     for (int n = tid; n < S::STAGE / 16; n += 64 * S::WAVES) {
       const bool r = n >= S::LEFT / 16;
       const int c = r ? n - S::LEFT / 16 : n;
       bool beyond;
       if ((r ? RL : LL) == kAlongDepth)
-        beyond = (c % kChunks ^ (r ? chunk_swizzle<S::SB, true>(c / kChunks) : chunk_swizzle<S::SB, false>(c / kChunks))) *
+        beyond = (c % kChunks ^ (r ? chunk_swizzle<true>(c / kChunks) : chunk_swizzle<false>(c / kChunks))) *
                      (16 / E) >= last_depth;
       else
         beyond = c / ((r ? S::BN : S::BM) * E / 16) >= last_depth;
@@ -245,14 +240,14 @@ __device__ __forceinline__ void product_tile(char* smem, unsigned wg, int part, 
   int la, ra;
   if constexpr (LL == kAlongDepth) {
     const int i = wm * (16 * MB) + li;
-    la = S::SB * i + 16 * (lg ^ chunk_swizzle<S::SB, false>(i));
+    la = kStageBytes * i + 16 * (lg ^ chunk_swizzle<false>(i));
   } else {
     const int k = 8 * lg + (li >> 2);
     la = S::BM * E * k + 32 * ((wm * MB) ^ block_swizzle<S::BM>(k)) + 8 * (li & 3);
   }
   if constexpr (RL == kAlongDepth) {
     const int i = wn * (16 * NB) + 8 * (li >> 2) + (li & 3);
-    ra = S::LEFT + S::SB * i + 16 * (lg ^ chunk_swizzle<S::SB, true>(i));
+    ra = S::LEFT + kStageBytes * i + 16 * (lg ^ chunk_swizzle<true>(i));
   } else {
     const int k = 8 * lg + (li >> 2);
     ra = S::LEFT + S::BN * E * k + 32 * ((wn * NB) ^ block_swizzle<S::BN>(k)) + 8 * (li & 3);
@@ -271,12 +266,12 @@ __device__ __forceinline__ void product_tile(char* smem, unsigned wg, int part, 
     const int buf = (kt & kMask) * S::STAGE;
     if (g < MB) {
       if constexpr (LL == kAlongDepth)
-        x[g] = *reinterpret_cast<const i32x4*>(smem + buf + (la ^ (64 * half)) + 16 * S::SB * g);
+        x[g] = *reinterpret_cast<const i32x4*>(smem + buf + (la ^ (64 * half)) + 16 * kStageBytes * g);
       else
         x[g] = transposed(((buf + la) ^ (32 * g)) + 32 * S::BM * E * half, S::BM * E);
     } else {
       if constexpr (RL == kAlongDepth)
-        x[g] = *reinterpret_cast<const i32x4*>(smem + buf + (ra ^ (64 * half)) + 32 * S::SB * ((g - MB) >> 1) + 4 * S::SB * ((g - MB) & 1));
+        x[g] = *reinterpret_cast<const i32x4*>(smem + buf + (ra ^ (64 * half)) + 32 * kStageBytes * ((g - MB) >> 1) + 4 * kStageBytes * ((g - MB) & 1));
       else
         x[g] = transposed(((buf + ra) ^ (32 * (g - MB))) + 32 * S::BN * E * half, S::BN * E);
     }
@@ -307,10 +302,10 @@ __device__ __forceinline__ void product_tile(char* smem, unsigned wg, int part, 
   // copies of stage kt + RING, spread over a half's MFMAs: issued together at its start they hold
   // up every wave's MFMAs behind 64 KiB of copies (8192 x 8192 outputs at depth 2048: 212 us
   // against 228; 8192 x 2048 at depth 8192, right operand along the index, 202 against 219)
-  constexpr int kEvery = kMma / COPIES, kPhase = S::SB == 64 ? 1 : 0;
+  constexpr int kEvery = kMma / COPIES;
   static_assert(kMma >= COPIES, "a copy per MFMA at most");
   auto copies = [&](int kt, bool more, int u) {
-    if (u % kEvery == kPhase % kEvery && u / kEvery < COPIES) {
+    if (u % kEvery == 0 && u / kEvery < COPIES) {
       if (more) copy1(kt + S::RING, u / kEvery);
     }
   };
@@ -380,7 +375,7 @@ __device__ __forceinline__ void product_tile(char* smem, unsigned wg, int part, 
       __syncthreads();
     }
     OZ2_SCHED_FENCE();
-    if constexpr (S::GROUPS == 1 && S::SB == 128) {
+    if constexpr (S::GROUPS == 1) {
 #pragma unroll
       for (int g = 0; g < FR; ++g) read1(0, 0, x0, g);
       OZ2_SCHED_FENCE();
@@ -399,7 +394,7 @@ __device__ __forceinline__ void product_tile(char* smem, unsigned wg, int part, 
 #pragma unroll
       for (int g = 0; g < FR; ++g) read1(0, group, x0, g);
       OZ2_SCHED_FENCE();
-      // a stage (or this group's half of it): fragments x, reading the next stage's into y
+      // this group's half of a stage: fragments x, reading the next stage's into y
       auto stage = [&](int kt, const i32x4 (&x)[FR], i32x4 (&y)[FR]) {
         if (kt == nk - 1 - S::RING) set_offsets(last_depth);
         middle(kt);
@@ -627,7 +622,7 @@ template <typename M, typename T, typename S, int LL, int RL, int OUT>
 static hipError_t launch_tile(const Product& pr, hipStream_t st) {
   typedef typename M::elem E;
   const int tiles_m = (pr.rows + S::BM - 1) / S::BM, tiles_n = (pr.cols + S::BN - 1) / S::BN;
-  const int stages = (pr.depth * static_cast<int>(sizeof(E)) + S::SB - 1) / S::SB;
+  const int stages = (pr.depth * static_cast<int>(sizeof(E)) + kStageBytes - 1) / kStageBytes;
   const int per = OUT == kOutPartial ? (stages + pr.plan.splits - 1) / pr.plan.splits : stages;
   const dim3 grid(static_cast<unsigned>(tiles_m) * static_cast<unsigned>(tiles_n), OUT == kOutPartial ? pr.plan.splits : 1);
   hipLaunchKernelGGL((product_tile_kernel<M, T, S, LL, RL, OUT>), grid, dim3(64 * S::WAVES), 0, st, pr.rows, pr.cols,
@@ -652,7 +647,7 @@ static hipError_t launch_join(const Product& pr, hipStream_t st) {
 template <typename M>
 static PairSide<M> pair_side(const Product& pr) {
   typedef Tile128Deep S;
-  const int stages = (pr.depth * static_cast<int>(sizeof(typename M::elem)) + S::SB - 1) / S::SB;
+  const int stages = (pr.depth * static_cast<int>(sizeof(typename M::elem)) + kStageBytes - 1) / kStageBytes;
   PairSide<M> side;
   side.rows = pr.rows;
   side.cols = pr.cols;
@@ -696,8 +691,7 @@ template <typename M, typename T, int LL, int RL, int OUT>
 static hipError_t launch_layout(const Product& pr, hipStream_t st) {
   switch (pr.plan.tile) {
     case kTile256:
-      if constexpr (LL == kAlongIndex && RL == kAlongIndex) return launch_tile<M, T, Tile256Index, LL, RL, OUT>(pr, st);
-      else return launch_tile<M, T, Tile256, LL, RL, OUT>(pr, st);
+      return launch_tile<M, T, Tile256, LL, RL, OUT>(pr, st);
     case kTile128:
       return launch_split<M, T, Tile128, LL, RL, OUT>(pr, st);
     case kTile128Deep:
