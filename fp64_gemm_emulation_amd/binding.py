@@ -451,9 +451,9 @@ def linear(x, w, bias=None, activation: str = "none", residual=None, dropout: fl
         pw, ldw = _rows(w, "w", (r, q), dtype, dev)
         pr, ldr = _rows(residual, "residual", (p, r), dtype, dev)
         pb = _vector(bias, "bias", r, dtype, dev)
-        y = out if out is not None else torch.empty((p, r), dtype=dtype, device=device)
+        y = out if out is not None else x.new_empty((p, r))
         py, ldy = _rows(y, "out", (p, r), dtype, dev) if out is not None else (y.data_ptr(), r or 1)
-        z = torch.empty((p, r), dtype=dtype, device=device) if return_z else None
+        z = x.new_empty((p, r)) if return_z else None
         work, pwork, nwork = _scratch(OZ2_LINEAR_FWD | _aligned(2 * q, (px, 2 * ldx), (pw, 2 * ldw)), kind, p, q, r, device)
         rc = _LIB.ozaki2_linear(kind, p, q, r, px, ldx, pw, ldw, pb, act, _dropout_ref(drop), pr, ldr,
                                 z.data_ptr() if return_z else None, r or 1, py, ldy, pwork, nwork, _raw_stream(dev))
@@ -482,9 +482,9 @@ def linear_backward(dy, x, w, z=None, activation: str = "none", dropout: float =
         px, ldx = _rows(x, "x", (p, q), dtype, dev)
         pw, ldw = _rows(w, "w", (r, q), dtype, dev)
         pz, ldz = _rows(z, "z", shape, dtype, dev)
-        dx = torch.empty((p, q), dtype=dtype, device=device) if "x" in needs else None
-        dw = torch.empty((r, q), dtype=dtype, device=device) if "w" in needs else None
-        db = torch.empty((r,), dtype=dtype, device=device) if "bias" in needs else None
+        dx = dy.new_empty((p, q)) if "x" in needs else None
+        dw = dy.new_empty((r, q)) if "w" in needs else None
+        db = dy.new_empty((r,)) if "bias" in needs else None
         work, pwork, nwork = _scratch(OZ2_LINEAR_BWD | _aligned(2 * q, (px, 2 * ldx), (pw, 2 * ldw)), kind, p, q, r, device)
         rc = _LIB.ozaki2_linear_bwd(kind, p, q, r, pdy, lddy, px, ldx, pw, ldw, pz, ldz, act, _dropout_ref(drop),
                                     dx.data_ptr() if dx is not None else None, q or 1,
@@ -506,7 +506,7 @@ def dropout_add(x, residual=None, dropout: float = 0.0, seed: int = 0, offset: i
     with _entered(dev, stream):
         px, ldx = _rows(x, "x", shape, dtype, dev)
         pr, ldr = _rows(residual, "residual", shape, dtype, dev)
-        y = out if out is not None else torch.empty((p, r), dtype=dtype, device=x.device)
+        y = out if out is not None else x.new_empty((p, r))
         py, ldy = _rows(y, "out", shape, dtype, dev) if out is not None else (y.data_ptr(), r or 1)
         rc = _LIB.ozaki2_dropout_add(kind, p, r, px, ldx, pr, ldr, _dropout_ref(drop), py, ldy, _raw_stream(dev))
     if rc != OZ2_OK:
@@ -546,7 +546,7 @@ def linear_i8(x, v, t, bias=None, activation: str = "none", residual=None, out=N
         pt = _vector(t, "t", r, torch.float32, dev)
         pr, ldr = _rows(residual, "residual", (p, r), dtype, dev)
         pb = _vector(bias, "bias", r, dtype, dev)
-        y = out if out is not None else torch.empty((p, r), dtype=dtype, device=device)
+        y = out if out is not None else x.new_empty((p, r))
         py, ldy = _rows(y, "out", (p, r), dtype, dev) if out is not None else (y.data_ptr(), r or 1)
         work, pwork, nwork = _scratch(OZ2_LINEAR_I8 | _aligned(q, (pv, ldv)), kind, p, q, r, device)
         rc = _LIB.ozaki2_linear_i8(kind, p, q, r, px, ldx, pv, ldv, pt, pb, act, pr, ldr, py, ldy, pwork, nwork,

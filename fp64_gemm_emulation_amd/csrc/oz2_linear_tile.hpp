@@ -593,16 +593,28 @@ __global__ __launch_bounds__(64 * S::WAVES, S::PER_CU) void product_pair_kernel(
 }
 
 // Adds up the sums over parts of the depth, in their order, and finishes the outputs: eight
-// columns of one row per thread.
+// columns of one row per thread.  Workgroups of one wave: there are few outputs, and a wave
+// waits mostly for its loads.
+constexpr int kJoinThreads = 64;
+
 template <typename M, typename T, int ACT, bool FULL>
-__global__ __launch_bounds__(256) void join_kernel(int rows, int cols, int splits, const typename M::acc* __restrict__ partial,
-                                                   Epilogue e) {
+__global__ __launch_bounds__(kJoinThreads) void join_kernel(int rows, int cols, int splits,
+                                                            const typename M::acc* __restrict__ partial, Epilogue e) {
   const int groups = (cols + 7) / 8;
   const long plane = static_cast<long>(rows) * groups * 2;
-  const long n = static_cast<long>(blockIdx.x) * 256 + threadIdx.x;
+  const long n = static_cast<long>(blockIdx.x) * kJoinThreads + threadIdx.x;
   if (n >= static_cast<long>(rows) * groups) return;
   const long m = n / groups;
-  const int g = static_cast<int>(n - m * groups);
+  const int col = 8 * static_cast<int>(n - m * groups), valid = cols - col;
+  // what the epilogue reads is under way with the sums
+  float xs = 0.0f, ws[8] = {};
+  raw8 bias = {}, res = {};
+  if (e.res != nullptr) res = load_raw8<T, FULL>(e.res, m * e.ldr + col, valid);
+  if (e.bias != nullptr) bias = load_raw8<T, FULL>(e.bias, col, valid);
+  if constexpr (sizeof(typename M::elem) == 1) {
+    xs = e.xs[m];
+    load8(e.ws + col, FULL ? 8 : valid, ws);
+  }
   typename M::acc a = partial[2 * n], b = partial[2 * n + 1];
 #pragma unroll 8
   for (int s = 1; s < splits; ++s) {
@@ -615,7 +627,7 @@ __global__ __launch_bounds__(256) void join_kernel(int rows, int cols, int split
     v[i] = static_cast<float>(a[i]);
     v[4 + i] = static_cast<float>(b[i]);
   }
-  finish8<T, ACT, FULL>(v, e, m, 8 * g, cols);
+  finish8<T, ACT, FULL>(v, e, m, col, cols, xs, ws, bias, res);
 }
 
 template <typename M, typename T, typename S, int LL, int RL, int OUT>
@@ -634,11 +646,11 @@ static hipError_t launch_tile(const Product& pr, hipStream_t st) {
 template <typename M, typename T>
 static hipError_t launch_join(const Product& pr, hipStream_t st) {
   const long n = static_cast<long>(pr.rows) * ((pr.cols + 7) / 8);
-  const dim3 grid(static_cast<unsigned>((n + 255) / 256));
+  const dim3 grid(static_cast<unsigned>((n + kJoinThreads - 1) / kJoinThreads));
   with_activation(pr.epi.act, [&](auto act) {
     constexpr int ACT = decltype(act)::value;
     const auto kernel = pr.cols % 8 == 0 ? join_kernel<M, T, ACT, true> : join_kernel<M, T, ACT, false>;
-    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, pr.rows, pr.cols, pr.plan.splits,
+    hipLaunchKernelGGL(kernel, grid, dim3(kJoinThreads), 0, st, pr.rows, pr.cols, pr.plan.splits,
                        static_cast<const typename M::acc*>(pr.partial), pr.epi);
   });
   return hipGetLastError();
