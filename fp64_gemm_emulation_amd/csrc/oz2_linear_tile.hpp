@@ -82,10 +82,19 @@ enum { kAlongDepth = 0, kAlongIndex = 1 };
 // indices, each lane 8 bytes, and each receives one index's 4 depths.  f takes 16 (256
 // elements) or, within either half of the wave, as many as there are blocks (8 or 4) values
 // over the rows one read touches.
+//
 // With two groups of waves (GROUPS = 2), each takes one half of every stage for all of the tile
 // and their sums meet in LDS at the end: one wave to a SIMD issues matrix instructions of this
 // size at half rate only, two reach the full rate, and dividing the tile among eight waves
 // instead would read LDS half as much again.
+//
+// What bounds it: on large outputs the matrix cores are 70 to 74% busy at about 1.9 GHz, which
+// random operands and the board's power set; a 256 x 256 stage moves 256 KiB through LDS in the
+// 2048 cycles its MFMAs take, as much as LDS can.  Measured (bf16): 8192^3 in 780 us, 1.41
+// PFLOP/s; 8192 x 2048 outputs at depth 8192 in 195 to 205 us in every layout, 1.34 to 1.41
+// PFLOP/s; int8 8192^3 in 415 us, 2.65 POP/s; 1024 x 4096 at depth 2048 (256 tiles of
+// 128 x 128, one to a CU) in 21.8 us, 0.79 PFLOP/s.  32 x 32 matrix instructions, which read the
+// same bytes, took 905 us for the first: the two waves of a SIMD mix less finely.
 constexpr int kStageBytes = 128;
 
 template <int BM_, int BN_, int WM_, int WN_, int GROUPS_, int RING_, int PER_CU_>
@@ -578,7 +587,8 @@ __global__ __launch_bounds__(64 * S::WAVES, S::PER_CU) void product_tile_kernel(
 
 // Two gradient products and the column sums in one launch: dX = dZ W on the first workgroups,
 // dW = dZ^T X on the next, the sums on the last, so that products of too few tiles to fill the
-// CUs fill them together.
+// CUs fill them together: 23.3 us for 1537 x 1001 and 2049 x 1001 outputs (240 tiles), where
+// one after the other took 21 and 22 and the sums 3.
 template <typename M>
 struct PairSide {
   int rows, cols, depth, per, tiles_m, tiles_n, parts;
@@ -616,7 +626,7 @@ __global__ __launch_bounds__(64 * S::WAVES, S::PER_CU) void product_pair_kernel(
 
 // Adds up the sums over parts of the depth, in their order, and finishes the outputs: eight
 // columns of one row per thread.  Workgroups of one wave: there are few outputs, and a wave
-// waits mostly for its loads.
+// waits mostly for its loads (3.9 us for 37 x 2048 outputs in 16 parts, 4.8 MB).
 constexpr int kJoinThreads = 64;
 
 template <typename M, typename T, int ACT, bool FULL>
