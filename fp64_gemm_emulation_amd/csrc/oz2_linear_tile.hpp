@@ -88,13 +88,13 @@ enum { kAlongDepth = 0, kAlongIndex = 1 };
 // size at half rate only, two reach the full rate, and dividing the tile among eight waves
 // instead would read LDS half as much again.
 //
-// What bounds it: on large outputs the matrix cores are 70 to 74% busy at about 1.9 GHz, which
-// random operands and the board's power set; a 256 x 256 stage moves 256 KiB through LDS in the
-// 2048 cycles its MFMAs take, as much as LDS can.  Measured (bf16): 8192^3 in 780 us, 1.41
-// PFLOP/s; 8192 x 2048 outputs at depth 8192 in 195 to 205 us in every layout, 1.34 to 1.41
-// PFLOP/s; int8 8192^3 in 415 us, 2.65 POP/s; 1024 x 4096 at depth 2048 (256 tiles of
-// 128 x 128, one to a CU) in 21.8 us, 0.79 PFLOP/s.  32 x 32 matrix instructions, which read the
-// same bytes, took 905 us for the first: the two waves of a SIMD mix less finely.
+// What bounds it: the matrix cores, 70 to 74% busy at depth 8192 (LDS is active 27% of the time,
+// without bank conflicts in the loop); at depth 2048 the epilogue's instructions and stores as well
+// (58% busy in bf16, 43% in int8), which no other workgroup's products overlap.  Measured (bf16):
+// 8192^3 in 780 us, 1.41 PFLOP/s; 8192 x 2048 outputs at depth 8192 in 201 to 207 us in the three
+// layouts, 1.33 to 1.37 PFLOP/s; int8 8192^3 in 420 to 438 us, 2.5 to 2.6 POP/s; 1024 x 4096 at
+// depth 2048 (256 tiles of 128 x 128, one to a CU) in 21.8 us, 0.79 PFLOP/s.  32 x 32 matrix
+// instructions took 905 us for the first where these took 814, both before later steps.
 constexpr int kStageBytes = 128;
 
 template <int BM_, int BN_, int WM_, int WN_, int GROUPS_, int RING_, int PER_CU_>
@@ -587,8 +587,8 @@ __global__ __launch_bounds__(64 * S::WAVES, S::PER_CU) void product_tile_kernel(
 
 // Two gradient products and the column sums in one launch: dX = dZ W on the first workgroups,
 // dW = dZ^T X on the next, the sums on the last, so that products of too few tiles to fill the
-// CUs fill them together: 23.3 us for 1537 x 1001 and 2049 x 1001 outputs (240 tiles), where
-// one after the other took 21 and 22 and the sums 3.
+// CUs fill them together: 23.3 us for 1537 x 1001 and 2049 x 1001 outputs (240 tiles) with the
+// sums, where the products alone, one after the other, took 21.4 and 18.5 (1000 columns).
 template <typename M>
 struct PairSide {
   int rows, cols, depth, per, tiles_m, tiles_n, parts;
@@ -751,7 +751,9 @@ static hipError_t launch_layout(const Product& pr, hipStream_t st) {
 // rows <= R, both operands along the depth, rows at any alignment.  Reading the right
 // operand (the weights) once is the whole work, so it goes straight from memory to registers:
 // a workgroup takes R of its rows and its waves share the depth, each with a contiguous part
-// in steps, kDeep steps' loads in flight.  The waves' sums meet in LDS.
+// in steps, kDeep steps' loads in flight.  The waves' sums meet in LDS.  Bound by memory: one
+// row on 8192 x 2048 bf16 weights 8.1 us, 4.1 TB/s with the launch in it; on 8192 x 8192, 24.4 us,
+// 5.5 TB/s (a large copy moves 5.2 TB/s both ways).
 // R = 16: a step is 64 bytes per row, one matrix instruction deep.  R = 8: the instruction's
 // 16 rows and columns hold 8 rows twice, 64 bytes further along the second time, on both
 // sides; the two diagonal quarters of its result are then sums over two parts of the depth
