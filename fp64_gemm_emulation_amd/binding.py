@@ -11,6 +11,7 @@ Loading fails loudly if the library has not been built: there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
@@ -51,9 +52,21 @@ class OZ2Dropout(ctypes.Structure):
     _fields_ = [("probability", ctypes.c_double), ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64)]
 
 
+def _share_hip_runtime():
+    """PyTorch's wheel brings its own HIP runtime.  Where it is not loaded yet (torch imported
+    after this module), load it now, so that the library binds to it: with the system's copy the
+    process would hold two, and the library's launches on torch's memory and streams fail."""
+    spec = importlib.util.find_spec("torch")
+    for folder in (spec.submodule_search_locations or ()) if spec is not None else ():
+        runtime = os.path.join(folder, "lib", "libamdhip64.so")
+        if os.path.exists(runtime):
+            ctypes.CDLL(runtime)
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it first (python -m fp64_gemm_emulation_amd.build)")
+    _share_hip_runtime()
     lib = ctypes.CDLL(LIB_PATH)
     i, vp, sz = ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t
     sig = {
