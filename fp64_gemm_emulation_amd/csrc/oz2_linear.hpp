@@ -38,7 +38,14 @@ struct Epilogue {
   long ldy = 0;
   const float* xs = nullptr;  // int8 products: scale of each row of the left operand
   const float* ws = nullptr;  //               and of each row of the right one
+  float scale = 1.0f;  // of the sums: the gradient's products (which have none of the above)
 };
+
+// The power of two that a gradient's dZ is stored with.  Dropout's scale stays out of dZ (it
+// multiplies the products' sums), so |dZ| is at most |dY| times the slope, and an activation's
+// slope is at most 1.13: only there can f16 overflow, and half of dZ cannot.  It costs the last
+// bit of values below 2^-13, and no rounding of others.
+__host__ __device__ constexpr float dz_factor(bool f16, int act) { return f16 && act >= kActGelu ? 0.5f : 1.0f; }
 
 // Which kernel computes a product, and over how many parts of the depth.
 enum { kTile256 = 0, kTile128 = 1, kTile64 = 2, kFew8 = 3, kFew16 = 4, kTile128Deep = 5 };
@@ -101,25 +108,33 @@ struct PackJob {
 hipError_t launch_pack_rows(int elem, const PackJob* a, const PackJob* b, hipStream_t st);
 
 hipError_t launch_product(const Product& pr, hipStream_t st);
+// Sums of a gradient's dZ over its rows: db = scale times the sum over `blocks` partial rows of
+// r floats (db null: none).
+struct ColumnSums {
+  int blocks, r;
+  const float* part;
+  float scale;
+  void* db;
+};
 // Both products of a gradient and, where db is not null, the column sums, in one launch; the
 // plans are plan_pair's.
-hipError_t launch_product_pair(int type, const Product& dx, const Product& dw, int p, int r, const float* part, void* db,
-                               hipStream_t st);
-hipError_t launch_pair_bf16(const Product& dx, const Product& dw, int blocks, int r, const float* part, void* db, hipStream_t st);
-hipError_t launch_pair_f16(const Product& dx, const Product& dw, int blocks, int r, const float* part, void* db, hipStream_t st);
+hipError_t launch_product_pair(int type, const Product& dx, const Product& dw, const ColumnSums& sums, hipStream_t st);
+hipError_t launch_pair_bf16(const Product& dx, const Product& dw, const ColumnSums& sums, hipStream_t st);
+hipError_t launch_pair_f16(const Product& dx, const Product& dw, const ColumnSums& sums, hipStream_t st);
 hipError_t launch_product_bf16(const Product& pr, hipStream_t st);
 hipError_t launch_product_f16(const Product& pr, hipStream_t st);
 hipError_t launch_product_i8(const Product& pr, hipStream_t st);
 hipError_t launch_dropout_add(int type, int p, int r, const void* x, long ldx, const void* res, long ldr,
                               const Drop& drop, void* y, long ldy, hipStream_t st);
-// dz = drop(dy) act'(z) in the operands' type, its rows padded with zeros to a multiple of 8
-// (skipped when dz is null), and, when part is not null, its column sums over each of
+// dz = mask(dy) act'(z) dz_factor in the operands' type, mask being dropout without its scale
+// (drop.scale is not used), its rows padded with zeros to a multiple of 8 (skipped when dz is
+// null), and, when part is not null, the column sums of mask(dy) act'(z) over each of
 // grad_row_blocks(p, r) blocks of rows: part is that many times r floats.  launch_column_sums
-// adds them up into db.
+// adds them up.
 int grad_row_blocks(int p, int r);
 hipError_t launch_grad_rows(int type, int p, int r, const void* dy, long lddy, const void* z, long ldz, int act,
                             const Drop& drop, void* dz, long lddz, float* part, hipStream_t st);
-hipError_t launch_column_sums(int type, int p, int r, const float* part, void* db, hipStream_t st);
+hipError_t launch_column_sums(int type, const ColumnSums& sums, hipStream_t st);
 // columns q .. fill - 1 of out are set to zero
 hipError_t launch_quantize_rows(int type, int p, int q, const void* x, long ldx, int8_t* out, long ldo, int fill,
                                 float* scale, hipStream_t st);
@@ -284,8 +299,9 @@ __host__ __device__ __forceinline__ void philox_block(uint32_t (&c)[4], uint32_t
   }
 }
 
-// v[i] <- element 8 block8 + i of its row, dropped or scaled.  A dropped element is 0
-// whatever it held (Inf and NaN too).
+// v[i] <- element 8 block8 + i of its row, dropped or scaled (SCALE false: dropped or left).  A
+// dropped element is 0 whatever it held (Inf and NaN too).
+template <bool SCALE = true>
 __device__ __forceinline__ void drop8(float (&v)[8], const Drop& d, long row, int cols, int block8) {
   const uint64_t n = static_cast<uint64_t>(row) * static_cast<uint64_t>((cols + 7) >> 3) + static_cast<uint64_t>(block8);
   uint32_t c[4] = {static_cast<uint32_t>(n), static_cast<uint32_t>(n >> 32), d.c2, d.c3};
@@ -293,7 +309,7 @@ __device__ __forceinline__ void drop8(float (&v)[8], const Drop& d, long row, in
   OZ2_UNROLL
   for (int i = 0; i < 8; ++i) {
     const uint32_t u = (i & 1) ? c[i >> 1] >> 16 : c[i >> 1] & 0xFFFFu;
-    v[i] = u >= d.t ? v[i] * d.scale : 0.0f;
+    v[i] = u >= d.t ? (SCALE ? v[i] * d.scale : v[i]) : 0.0f;
   }
 }
 
@@ -403,27 +419,27 @@ __device__ __forceinline__ void finish8(float (&v)[8], const Epilogue& e, long m
 }
 
 // ---- column sums ---------------------------------------------------------------------------
-// db = sums over `blocks` partial rows of r columns, kSumColumns columns per workgroup of
-// THREADS threads, in a fixed order; lds: THREADS floats.
+// ColumnSums, kSumColumns columns per workgroup of THREADS threads, in a fixed order; lds:
+// THREADS floats.
 constexpr int kSumColumns = 32;
 
 template <typename T, int THREADS>
-__device__ __forceinline__ void column_sums(float* lds, unsigned wg, int blocks, int r, const float* part, T* db) {
+__device__ __forceinline__ void column_sums(float* lds, unsigned wg, const ColumnSums& sums) {
   constexpr int W = THREADS / kSumColumns;
   const int lane = threadIdx.x % kSumColumns, w = threadIdx.x / kSumColumns;
   const int c = static_cast<int>(wg) * kSumColumns + lane;
   float s = 0.0f;
-  if (c < r) {
+  if (c < sums.r) {
 #pragma unroll 4
-    for (int b = w; b < blocks; b += W) s += part[static_cast<long>(b) * r + c];
+    for (int b = w; b < sums.blocks; b += W) s += sums.part[static_cast<long>(b) * sums.r + c];
   }
   lds[threadIdx.x] = s;
   __syncthreads();
-  if (w != 0 || c >= r) return;
+  if (w != 0 || c >= sums.r) return;
   s = 0.0f;
   OZ2_UNROLL
   for (int i = 0; i < W; ++i) s += lds[i * kSumColumns + lane];
-  db[c] = static_cast<T>(s);
+  static_cast<T*>(sums.db)[c] = static_cast<T>(s * sums.scale);
 }
 
 }  // namespace oz2

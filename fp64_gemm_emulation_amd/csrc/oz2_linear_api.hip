@@ -222,7 +222,8 @@ int ozaki2_linear_bwd(int type, int p, int q, int r, const void* dY, int lddy, c
       if (o != o2 && overlap(*o, *o2)) return OZ2_ERR_ARG;
   }
   const oz2::Drop drop = make_drop(dropout);
-  // dZ is dY itself without activation and dropout, if its rows are aligned; making it packs it
+  // dZ is dY itself without activation and dropout, if its rows are aligned; making it packs it.
+  // Dropout's scale multiplies the products' sums, not dZ.
   const bool product = want_dx || want_dw;
   const bool make_dz = product && p > 0 && r > 0 && (act != OZ2_ACT_NONE || drop.t != 0 || !oz2::rows_aligned(dY, lddy, r, 2));
   const bool pack_x = want_dw && p > 0 && !oz2::rows_aligned(X, ldx, q, 2);
@@ -247,11 +248,14 @@ int ozaki2_linear_bwd(int type, int p, int q, int r, const void* dY, int lddy, c
   oz2::Product px{type, false, p, q, r, dz, lddz, false, pack_w ? ws.w : W, pack_w ? lq : ldw, true, {}, ws.dx, ws.partial_x, false};
   px.epi.y = dX;
   px.epi.ldy = lddx;
+  px.epi.scale = make_dz ? drop.scale / oz2::dz_factor(type == OZ2_F16, act) : 1.0f;
   oz2::Product pw{type, false, r, q, p, dz, lddz, true, pack_x ? ws.x : X, pack_x ? lq : ldx, true, {}, ws.dw, ws.partial_w, false};
   pw.epi.y = dW;
   pw.epi.ldy = lddw;
-  if (ws.paired) return status(oz2::launch_product_pair(type, px, pw, p, r, ws.sums, want_db ? dbias : nullptr, st));
-  if (want_db && (rc = status(oz2::launch_column_sums(type, p, r, ws.sums, dbias, st))) != OZ2_OK) return rc;
+  pw.epi.scale = px.epi.scale;
+  const oz2::ColumnSums sums{p > 0 ? oz2::grad_row_blocks(p, r) : 0, r, ws.sums, drop.scale, want_db ? dbias : nullptr};
+  if (ws.paired) return status(oz2::launch_product_pair(type, px, pw, sums, st));
+  if (want_db && (rc = status(oz2::launch_column_sums(type, sums, st))) != OZ2_OK) return rc;
   if (want_dx && (rc = status(oz2::launch_product(px, st))) != OZ2_OK) return rc;
   return want_dw ? status(oz2::launch_product(pw, st)) : OZ2_OK;
 }

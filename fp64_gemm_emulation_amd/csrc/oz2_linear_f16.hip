@@ -7,8 +7,8 @@ hipError_t launch_product_f16(const Product& pr, hipStream_t st) {
   return launch_type<MmaF16, f16>(pr, st);
 }
 
-hipError_t launch_pair_f16(const Product& dx, const Product& dw, int blocks, int r, const float* part, void* db, hipStream_t st) {
-  return launch_pair<MmaF16, f16>(dx, dw, blocks, r, part, db, st);
+hipError_t launch_pair_f16(const Product& dx, const Product& dw, const ColumnSums& sums, hipStream_t st) {
+  return launch_pair<MmaF16, f16>(dx, dw, sums, st);
 }
 
 }  // namespace oz2

@@ -115,11 +115,8 @@ bool plan_pair(long p, long q, long r, Plan& dx, Plan& dw) {
   return paired;
 }
 
-hipError_t launch_product_pair(int type, const Product& dx, const Product& dw, int p, int r, const float* part, void* db,
-                               hipStream_t st) {
-  const int blocks = grad_row_blocks(p, r);
-  return type == kTypeBf16 ? launch_pair_bf16(dx, dw, blocks, r, part, db, st)
-                           : launch_pair_f16(dx, dw, blocks, r, part, db, st);
+hipError_t launch_product_pair(int type, const Product& dx, const Product& dw, const ColumnSums& sums, hipStream_t st) {
+  return type == kTypeBf16 ? launch_pair_bf16(dx, dw, sums, st) : launch_pair_f16(dx, dw, sums, st);
 }
 
 hipError_t launch_product(const Product& pr, hipStream_t st) {

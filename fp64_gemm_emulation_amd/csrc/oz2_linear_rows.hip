@@ -57,7 +57,7 @@ hipError_t launch_dropout_add(int type, int p, int r, const void* x, long ldx, c
   return dropout_add<float>(p, r, x, ldx, res, ldr, drop, y, ldy, st);
 }
 
-// dz = drop(dy) act'(z): a workgroup takes a block of rows of 256 columns, a thread eight
+// dz = mask(dy) act'(z) dz_factor: a workgroup takes a block of rows of 256 columns, a thread eight
 // consecutive columns of every eighth row.  Column sums are of the unrounded f32 values, in
 // a fixed order: over the thread's rows, over the eight threads of a column group, and (in
 // column_sums_kernel) over the row blocks.  Bound by memory: 8192 x 8192 bf16, gelu, in 77 us,
@@ -91,16 +91,21 @@ __global__ __launch_bounds__(256) void grad_rows_kernel(int p, int r, const T* d
     for (long row = row0 + rr; row < min(row0 + block_rows, static_cast<long>(p)); row += 8) {
       float v[8], t[8];
       load8<T, true>(dy + row * lddy + col, valid, v);
-      if (d.t != 0) drop8(v, d, row, r, col >> 3);
+      if (d.t != 0) drop8<false>(v, d, row, r, col >> 3);
       if constexpr (ACT != kActNone) {
         load8<T, true>(z + row * ldz + col, valid, t);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] *= activation_slope<ACT>(t[i]);
       }
-      // dz's rows are padded to multiples of 8 with zeros (load8's)
-      if (dz != nullptr) store8(dz + row * lddz + col, 8, v);
 #pragma unroll
       for (int i = 0; i < 8; ++i) sum[i] += v[i];
+      if (dz != nullptr) {
+        constexpr float kFactor = dz_factor(std::is_same_v<T, f16>, ACT);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= kFactor;
+        // dz's rows are padded to multiples of 8 with zeros (load8's)
+        store8(dz + row * lddz + col, 8, v);
+      }
     }
   }
   if (part == nullptr) return;  // uniform over the launch
@@ -115,21 +120,15 @@ __global__ __launch_bounds__(256) void grad_rows_kernel(int p, int r, const T* d
 }
 
 template <typename T>
-__global__ __launch_bounds__(256) void column_sums_kernel(int blocks, int r, const float* part, T* db) {
+__global__ __launch_bounds__(256) void column_sums_kernel(ColumnSums sums) {
   __shared__ float lds[256];
-  column_sums<T, 256>(lds, blockIdx.x, blocks, r, part, db);
+  column_sums<T, 256>(lds, blockIdx.x, sums);
 }
 
-template <typename T>
-static hipError_t sum_columns(int blocks, int r, const float* part, void* db, hipStream_t st) {
-  hipLaunchKernelGGL(column_sums_kernel<T>, dim3((r + kSumColumns - 1) / kSumColumns), dim3(256), 0, st, blocks, r, part,
-                     static_cast<T*>(db));
+hipError_t launch_column_sums(int type, const ColumnSums& sums, hipStream_t st) {
+  const auto kernel = type == kTypeBf16 ? column_sums_kernel<bf16> : column_sums_kernel<f16>;
+  hipLaunchKernelGGL(kernel, dim3((sums.r + kSumColumns - 1) / kSumColumns), dim3(256), 0, st, sums);
   return hipGetLastError();
-}
-
-hipError_t launch_column_sums(int type, int p, int r, const float* part, void* db, hipStream_t st) {
-  const int blocks = p > 0 ? grad_row_blocks(p, r) : 0;  // without rows the sums are zeros
-  return type == kTypeBf16 ? sum_columns<bf16>(blocks, r, part, db, st) : sum_columns<f16>(blocks, r, part, db, st);
 }
 
 template <typename T>

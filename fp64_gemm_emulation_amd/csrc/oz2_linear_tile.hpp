@@ -497,7 +497,7 @@ __device__ __forceinline__ void product_tile(char* smem, unsigned wg, int part, 
         const int c = wn * (2 * NB) + 2 * nb + (eg >> 1);
         T t[4];
 #pragma unroll
-        for (int v = 0; v < 4; ++v) t[v] = static_cast<T>(static_cast<float>(sum[mb][nb][v]));
+        for (int v = 0; v < 4; ++v) t[v] = static_cast<T>(e.scale * static_cast<float>(sum[mb][nb][v]));
         __builtin_memcpy(smem + i * kPitch + 16 * (c ^ (i & 15)) + 8 * (eg & 1), t, sizeof(t));
       }
     }
@@ -602,8 +602,7 @@ struct PairSide {
 };
 
 template <typename M, typename T, typename S>
-__global__ __launch_bounds__(64 * S::WAVES, S::PER_CU) void product_pair_kernel(PairSide<M> dx, PairSide<M> dw, int blocks,
-                                                                                int r, const float* sums, T* db) {
+__global__ __launch_bounds__(64 * S::WAVES, S::PER_CU) void product_pair_kernel(PairSide<M> dx, PairSide<M> dw, ColumnSums sums) {
   __shared__ __attribute__((aligned(1024))) char smem[S::RING * S::STAGE];
   unsigned wg = blockIdx.x;
   const unsigned nx = static_cast<unsigned>(dx.tiles_m) * dx.tiles_n, nw = static_cast<unsigned>(dw.tiles_m) * dw.tiles_n;
@@ -621,7 +620,7 @@ __global__ __launch_bounds__(64 * S::WAVES, S::PER_CU) void product_pair_kernel(
     return;
   }
   wg -= nw * dw.parts;
-  column_sums<T, 64 * S::WAVES>(reinterpret_cast<float*>(smem), wg, blocks, r, sums, db);
+  column_sums<T, 64 * S::WAVES>(reinterpret_cast<float*>(smem), wg, sums);
 }
 
 // Adds up the sums over parts of the depth, in their order, and finishes the outputs: eight
@@ -656,8 +655,8 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(int rows, int cols, 
   float v[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    v[i] = static_cast<float>(a[i]);
-    v[4 + i] = static_cast<float>(b[i]);
+    v[i] = e.scale * static_cast<float>(a[i]);
+    v[4 + i] = e.scale * static_cast<float>(b[i]);
   }
   finish8<T, ACT, FULL>(v, e, m, col, cols, xs, ws, bias, res);
 }
@@ -710,13 +709,11 @@ static PairSide<M> pair_side(const Product& pr) {
 }
 
 template <typename M, typename T>
-static hipError_t launch_pair(const Product& dx, const Product& dw, int blocks, int r, const float* sums, void* db,
-                              hipStream_t st) {
+static hipError_t launch_pair(const Product& dx, const Product& dw, const ColumnSums& sums, hipStream_t st) {
   typedef Tile128Deep S;
   const PairSide<M> px = pair_side<M>(dx), pw = pair_side<M>(dw);
-  const unsigned n = px.workgroups() + pw.workgroups() + (db != nullptr ? (r + kSumColumns - 1) / kSumColumns : 0);
-  hipLaunchKernelGGL((product_pair_kernel<M, T, S>), dim3(n), dim3(64 * S::WAVES), 0, st, px, pw, blocks, r, sums,
-                     static_cast<T*>(db));
+  const unsigned n = px.workgroups() + pw.workgroups() + (sums.db != nullptr ? (sums.r + kSumColumns - 1) / kSumColumns : 0);
+  hipLaunchKernelGGL((product_pair_kernel<M, T, S>), dim3(n), dim3(64 * S::WAVES), 0, st, px, pw, sums);
   hipError_t err = hipGetLastError();
   if (err == hipSuccess && dx.plan.splits > 1) err = launch_join<M, T>(dx, st);
   if (err == hipSuccess && dw.plan.splits > 1) err = launch_join<M, T>(dw, st);

@@ -295,7 +295,9 @@ int ozaki2_linear(int type, int p, int q, int r, const void* X, int ldx, const v
  * (the residual's gradient is dY itself).  Outputs that are NULL are not computed; X is needed
  * for dW only, W for dX only, Z only when act is not OZ2_ACT_NONE; `dropout` has to be the
  * forward call's.  dZ is rounded to `type` before the two products, which is what feeds the
- * matrix cores; dbias sums the unrounded values.  Empty sizes give zero gradients.
+ * matrix cores, but without dropout's scale, which multiplies the 32-bit sums, and in f16 with
+ * the gelus and silu as half of it: so it is exact for none and relu, and finite for every
+ * finite dY.  dbias sums the unrounded values.  Empty sizes give zero gradients.
  */
 int ozaki2_linear_bwd(int type, int p, int q, int r, const void* dY, int lddy, const void* X, int ldx, const void* W,
                       int ldw, const void* Z, int ldz, int act, const oz2_dropout_t* dropout, void* dX, int lddx,
