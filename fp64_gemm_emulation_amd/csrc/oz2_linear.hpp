@@ -256,8 +256,12 @@ __device__ __forceinline__ float activate(float a) {
   }
 }
 
+// The slopes have reached their limits (0 and 1, in f32) well before |z| = 100; z is held within
+// 1e4, since beyond it the formulas meet 0 times infinity: in z^2 past 1.8e19, and at an infinite z,
+// as a pre-activation past f16's range is kept.
 template <int ACT>
 __device__ __forceinline__ float activation_slope(float z) {
+  z = z > 1e4f ? 1e4f : z < -1e4f ? -1e4f : z;  // NaN stays NaN
   if constexpr (ACT == kActRelu) {
     return z > 0.0f ? 1.0f : 0.0f;
   } else if constexpr (ACT == kActGelu) {
