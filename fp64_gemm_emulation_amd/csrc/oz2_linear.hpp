@@ -20,7 +20,9 @@ enum { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4 
 // Dropout as the kernels see it: keep where the 16-bit draw is at least t, times scale.
 struct Drop {
   uint32_t t = 0;  // rint(2^16 p); 0: everything kept, 2^16: nothing
-  float scale = 1.0f;  // 2^16 / (2^16 - t), the reciprocal of the exact keep probability
+  // 2^16 / (2^16 - t), the reciprocal of the exact keep probability; with t = 0 in a gradient's
+  // products, where nothing is dropped any more, the factor of their sums
+  float scale = 1.0f;
   uint32_t k0 = 0, k1 = 0;  // key: the seed's halves
   uint32_t c2 = 0, c3 = 0;  // upper counter words: the offset's halves
 };
@@ -38,7 +40,6 @@ struct Epilogue {
   long ldy = 0;
   const float* xs = nullptr;  // int8 products: scale of each row of the left operand
   const float* ws = nullptr;  //               and of each row of the right one
-  float scale = 1.0f;  // of the sums: the gradient's products (which have none of the above)
 };
 
 // The power of two that a gradient's dZ is stored with.  Dropout's scale stays out of dZ (it
@@ -225,16 +226,15 @@ __device__ __forceinline__ float sigmoid_gelu_tanh(float a) {
   return sigmoid(a * __builtin_fmaf(1.5957691216057308f * 0.044715f, a * a, 1.5957691216057308f));
 }
 
-// Phi(-|a|) = erfc(|a| / sqrt 2) / 2 and e = exp(-a^2 / 2), by formula 7.1.26 of Abramowitz and
+// Phi(-|a|) = erfc(|a| / sqrt 2) / 2 from a and e = exp(-a^2 / 2), by formula 7.1.26 of Abramowitz and
 // Stegun, "Handbook of Mathematical Functions" (a fifth-degree polynomial in
 // 1 / (1 + 0.3275911 x) times exp(-x^2), within 1.5e-7): a third of the instructions of erff.
-__device__ __forceinline__ float normal_tail(float a, float& e) {
+__device__ __forceinline__ float normal_tail(float a, float e) {
   const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3275911f * 0.70710678118654752f, fabsf(a), 1.0f));
   float p = __builtin_fmaf(t, 0.5f * 1.061405429f, 0.5f * -1.453152027f);
   p = __builtin_fmaf(t, p, 0.5f * 1.421413741f);
   p = __builtin_fmaf(t, p, 0.5f * -0.284496736f);
   p = __builtin_fmaf(t, p, 0.5f * 0.254829592f);
-  e = exp_fast(-0.5f * a * a);
   return t * p * e;
 }
 
@@ -244,8 +244,7 @@ __device__ __forceinline__ float activate(float a) {
     return a <= 0.0f ? 0.0f : a;  // NaN stays NaN
   } else if constexpr (ACT == kActGelu) {
     // max(a, 0) - |a| Phi(-|a|); the minimum keeps +Inf from meeting its factor 0
-    float e;
-    const float h = normal_tail(a, e);
+    const float h = normal_tail(a, exp_fast(-0.5f * a * a));
     return __builtin_fmaf(-fabsf(fminf(a, 65536.0f)), h, fmaxf(a, 0.0f));
   } else if constexpr (ACT == kActGeluTanh) {
     return a * sigmoid_gelu_tanh(a);
@@ -256,24 +255,24 @@ __device__ __forceinline__ float activate(float a) {
   }
 }
 
-// The slopes have reached their limits (0 and 1, in f32) well before |z| = 100; z is held within
-// 1e4, since beyond it the formulas meet 0 times infinity: in z^2 past 1.8e19, and at an infinite z,
-// as a pre-activation past f16's range is kept.
+// The slopes have reached their limits (0 and 1, in f32) well before |z| = 100.  Beyond, the
+// formulas would multiply 0 by infinity (z^2 past 1.8e19, or an infinite z, as a pre-activation
+// past f16's range is kept), so their outer z is held within 1e4; NaN comes through s or h.
 template <int ACT>
 __device__ __forceinline__ float activation_slope(float z) {
-  z = z > 1e4f ? 1e4f : z < -1e4f ? -1e4f : z;  // NaN stays NaN
+  const float zc = __builtin_amdgcn_fmed3f(z, -1e4f, 1e4f);
   if constexpr (ACT == kActRelu) {
     return z > 0.0f ? 1.0f : 0.0f;
   } else if constexpr (ACT == kActGelu) {
-    float e;
+    const float e = __builtin_amdgcn_exp2f(-0.72134752044448170f * z * z);  // a multiply less than exp_fast
     const float h = normal_tail(z, e);
-    return __builtin_fmaf(z * 0.39894228040143268f, e, z > 0.0f ? 1.0f - h : h);
+    return __builtin_fmaf(zc * 0.39894228040143268f, e, z > 0.0f ? 1.0f - h : h);
   } else if constexpr (ACT == kActGeluTanh) {
     const float s = sigmoid_gelu_tanh(z);
-    return s + z * s * (1.0f - s) * 1.5957691216057308f * __builtin_fmaf(3.0f * 0.044715f, z * z, 1.0f);
+    return s + zc * s * (1.0f - s) * 1.5957691216057308f * __builtin_fmaf(3.0f * 0.044715f, zc * zc, 1.0f);
   } else if constexpr (ACT == kActSilu) {
     const float s = sigmoid(z);
-    return s * (1.0f + z * (1.0f - s));
+    return s * (1.0f + zc * (1.0f - s));
   } else {
     return 1.0f;
   }

@@ -248,11 +248,11 @@ int ozaki2_linear_bwd(int type, int p, int q, int r, const void* dY, int lddy, c
   oz2::Product px{type, false, p, q, r, dz, lddz, false, pack_w ? ws.w : W, pack_w ? lq : ldw, true, {}, ws.dx, ws.partial_x, false};
   px.epi.y = dX;
   px.epi.ldy = lddx;
-  px.epi.scale = make_dz ? drop.scale / oz2::dz_factor(type == OZ2_F16, act) : 1.0f;
+  px.epi.drop.scale = make_dz ? drop.scale / oz2::dz_factor(type == OZ2_F16, act) : 1.0f;
   oz2::Product pw{type, false, r, q, p, dz, lddz, true, pack_x ? ws.x : X, pack_x ? lq : ldx, true, {}, ws.dw, ws.partial_w, false};
   pw.epi.y = dW;
   pw.epi.ldy = lddw;
-  pw.epi.scale = px.epi.scale;
+  pw.epi.drop.scale = px.epi.drop.scale;
   const oz2::ColumnSums sums{p > 0 ? oz2::grad_row_blocks(p, r) : 0, r, ws.sums, drop.scale, want_db ? dbias : nullptr};
   if (ws.paired) return status(oz2::launch_product_pair(type, px, pw, sums, st));
   if (want_db && (rc = status(oz2::launch_column_sums(type, sums, st))) != OZ2_OK) return rc;

@@ -97,15 +97,15 @@ __global__ __launch_bounds__(256) void grad_rows_kernel(int p, int r, const T* d
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] *= activation_slope<ACT>(t[i]);
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sum[i] += v[i];
+      // dz's rows are padded to multiples of 8 with zeros (load8's)
       if (dz != nullptr) {
         constexpr float kFactor = dz_factor(std::is_same_v<T, f16>, ACT);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= kFactor;
-        // dz's rows are padded to multiples of 8 with zeros (load8's)
-        store8(dz + row * lddz + col, 8, v);
+        for (int i = 0; i < 8; ++i) t[i] = v[i] * kFactor;
+        store8(dz + row * lddz + col, 8, t);
       }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[i] += v[i];
     }
   }
   if (part == nullptr) return;  // uniform over the launch

@@ -204,6 +204,12 @@ __device__ __forceinline__ void product_tile(char* smem, unsigned wg, int part, 
   const char* const rbase = reinterpret_cast<const char*>(right) + (RL == kAlongDepth ? n0 * right_ld : n0) * E + kt0 * rstep;
   const int last_m = static_cast<int>(min(static_cast<long>(rows) - 1 - m0, static_cast<long>(S::BM - 1)));
   const int last_n = min(cols - 1 - n0, S::BN - 1);
+  // read here: its use comes before that of y, whose load the output's pass through LDS hides
+  float scale = 1.0f;
+  if constexpr (OUT == kOutPlain || OUT == kOutEither) {
+    scale = e.drop.scale;
+    asm volatile("" : "+s"(scale));
+  }
   unsigned off[COPIES];
   auto set_offsets = [&](int valid) {
 #pragma unroll
@@ -497,7 +503,7 @@ __device__ __forceinline__ void product_tile(char* smem, unsigned wg, int part, 
         const int c = wn * (2 * NB) + 2 * nb + (eg >> 1);
         T t[4];
 #pragma unroll
-        for (int v = 0; v < 4; ++v) t[v] = static_cast<T>(e.scale * static_cast<float>(sum[mb][nb][v]));
+        for (int v = 0; v < 4; ++v) t[v] = static_cast<T>(scale * static_cast<float>(sum[mb][nb][v]));
         __builtin_memcpy(smem + i * kPitch + 16 * (c ^ (i & 15)) + 8 * (eg & 1), t, sizeof(t));
       }
     }
@@ -652,11 +658,12 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(int rows, int cols, 
     a += partial[s * plane + 2 * n];
     b += partial[s * plane + 2 * n + 1];
   }
+  const float scale = e.drop.t == 0 ? e.drop.scale : 1.0f;
   float v[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    v[i] = e.scale * static_cast<float>(a[i]);
-    v[4 + i] = e.scale * static_cast<float>(b[i]);
+    v[i] = scale * static_cast<float>(a[i]);
+    v[4 + i] = scale * static_cast<float>(b[i]);
   }
   finish8<T, ACT, FULL>(v, e, m, col, cols, xs, ws, bias, res);
 }
