@@ -179,6 +179,7 @@ int validate(const Call& c, const oz2_dump_t* dump) {
 struct Owned {
   void* ptr = nullptr;
   size_t bytes = 0;
+  std::vector<void*> outgrown;  // kept until ozaki2_release: captured graphs may hold them (linear-layer calls)
 };
 
 struct State {
@@ -225,25 +226,42 @@ int scratch_workspace(char** base) {
 }
 
 // A library-owned buffer of at least `need` bytes on the device current at this call (each
-// device gets its own), allocated or grown on first need.
-int acquire_owned(std::vector<Owned>& owned, size_t need, char** base) {
+// device gets its own), allocated or grown on first need.  keep_outgrown: a buffer that is too
+// small stays until ozaki2_release, as a captured graph may replay into it, and the next is at
+// least twice as large (where that much can be had), so that all outgrown ones together are no
+// larger than the one in use.
+int acquire_owned(std::vector<Owned>& owned, bool keep_outgrown, size_t need, char** base) {
   int dev = 0;
   if (hipGetDevice(&dev) != hipSuccess || dev < 0) return OZ2_ERR_HIP;
-  if (owned.size() <= static_cast<size_t>(dev)) owned.resize(static_cast<size_t>(dev) + 1);
+  try {
+    if (owned.size() <= static_cast<size_t>(dev)) owned.resize(static_cast<size_t>(dev) + 1);
+    if (keep_outgrown) owned[static_cast<size_t>(dev)].outgrown.reserve(owned[static_cast<size_t>(dev)].outgrown.size() + 1);
+  } catch (const std::bad_alloc&) {  // the tables of buffers
+    return OZ2_ERR_WORKSPACE;
+  }
   Owned& o = owned[static_cast<size_t>(dev)];
   if (o.bytes < need) {
-    if (o.ptr != nullptr) {
+    if (!keep_outgrown && o.ptr != nullptr) {
       if (hipDeviceSynchronize() != hipSuccess) return OZ2_ERR_HIP;
       (void)hipFree(o.ptr);
       o.ptr = nullptr;
       o.bytes = 0;
     }
-    if (hipMalloc(&o.ptr, need) != hipSuccess) {
-      o.ptr = nullptr;
+    void* ptr = nullptr;
+    size_t bytes = std::max(need, 2 * o.bytes);
+    hipError_t err = hipMalloc(&ptr, bytes);
+    if (err != hipSuccess && bytes > need) {
+      (void)hipGetLastError();
+      bytes = need;
+      err = hipMalloc(&ptr, bytes);
+    }
+    if (err != hipSuccess) {
       (void)hipGetLastError();
       return OZ2_ERR_WORKSPACE;
     }
-    o.bytes = need;
+    if (o.ptr != nullptr) o.outgrown.push_back(o.ptr);
+    o.ptr = ptr;
+    o.bytes = bytes;
   }
   *base = static_cast<char*>(o.ptr);
   return OZ2_OK;
@@ -255,7 +273,7 @@ int acquire_workspace(size_t need, char** base) {
     *base = static_cast<char*>(g.user);
     return OZ2_OK;
   }
-  return acquire_owned(g.owned, need, base);
+  return acquire_owned(g.owned, false, need, base);
 }
 
 struct Recorder {
@@ -368,11 +386,7 @@ int acquire_linear_workspace(size_t need, char** base) {
     *base = static_cast<char*>(g.user) + kLinearWorkspaceSkip;
     return OZ2_OK;
   }
-  try {
-    return acquire_owned(g.owned_linear, need, base);
-  } catch (const std::bad_alloc&) {  // the table of buffers
-    return OZ2_ERR_WORKSPACE;
-  }
+  return acquire_owned(g.owned_linear, true, need, base);
 }
 
 }  // namespace oz2
@@ -429,8 +443,9 @@ int ozaki2_release(void) {
       if (hipSetDevice(static_cast<int>(dev)) != hipSuccess || hipDeviceSynchronize() != hipSuccess ||
           hipFree(o.ptr) != hipSuccess)
         rc = OZ2_ERR_HIP;
-      o.ptr = nullptr;
-      o.bytes = 0;
+      for (void* p : o.outgrown)
+        if (hipFree(p) != hipSuccess) rc = OZ2_ERR_HIP;
+      o = Owned{};
     }
     if (!owned->empty() && hipSetDevice(cur) != hipSuccess) rc = OZ2_ERR_HIP;
   }

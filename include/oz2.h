@@ -240,10 +240,12 @@ int ozaki2_tau(int s);
  *   - `work` / `work_bytes`: scratch of at least ozaki2_linear_workspace_size bytes, 256-byte
  *     aligned, whose contents do not matter and that nothing else uses until the call's work
  *     is done.  NULL uses the buffer of ozaki2_set_workspace, beyond its first 256 bytes, else
- *     one that the library owns (per device, apart from the dgemm calls', freed by
- *     ozaki2_release); calls on different streams that share one must be ordered by the caller.
+ *     one that the library owns (per device, apart from the dgemm calls'; a call that needs more
+ *     gets another, and all are freed by ozaki2_release); calls on different streams that share one
+ *     must be ordered by the caller.
  *     With a caller's `work`, or once the library's buffer has its size, calls enqueue kernels
- *     only and can be captured in a HIP graph.
+ *     only and can be captured in a HIP graph, which keeps the workspace's address: the caller's
+ *     must stay valid, and the library's does until ozaki2_release.
  */
 
 /* Element types of the linear-layer calls. */
