@@ -323,6 +323,9 @@ def dgemm_debug(A, B, s: int = 14, mode: str = "fast", want=DUMP_FIELDS, stream=
 # Row-major 2-D tensors, one token per row (a 3-D batch is passed as its reshape(-1, q)).
 # Outputs and scratch are allocated on the stream of the call, so calls on different
 # streams share nothing; operands made on another stream have to be ready on this one.
+# With stream= given, the operands are recorded on it, so that their memory is not handed out
+# again while the call reads it, and the outputs on the stream that was current, to which they
+# return (waiting for the call there is the caller's part).
 # A single token's layer takes a few microseconds on the GPU, so these functions look up
 # attributes once, and torch itself on first use only.
 _torch = None
@@ -418,6 +421,31 @@ class _NoContext:
 _NO_CONTEXT = _NoContext()
 
 
+class _OnStream:
+    """The caller's stream made current, and what the call uses recorded on the streams that
+    use it."""
+
+    def __init__(self, stream):
+        self.stream = stream
+
+    def __enter__(self):
+        self.before = _torch.cuda.current_stream(self.stream.device)
+        self.context = _torch.cuda.stream(self.stream)
+        self.context.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        self.context.__exit__(*exc)
+
+    def record(self, operands, outputs):
+        for t in operands:
+            if t is not None:
+                t.record_stream(self.stream)
+        for t in outputs:
+            if t is not None:
+                t.record_stream(self.before)
+
+
 def _entered(dev, stream):
     """Context that makes the call's device and stream current while outputs and scratch are
     allocated and the library is entered (none where they are)."""
@@ -426,7 +454,7 @@ def _entered(dev, stream):
     if stream is not None:
         if stream.device.index != dev:
             raise ValueError("the stream belongs to another device than the operands")
-        return _torch.cuda.stream(stream)
+        return _OnStream(stream)
     return _NO_CONTEXT if dev == _torch.cuda.current_device() else _torch.cuda.device(dev)
 
 
@@ -459,7 +487,7 @@ def linear(x, w, bias=None, activation: str = "none", residual=None, dropout: fl
     r = _shape2(w, "w")[0]
     kind, act, drop = _kind(x, "x"), _activation(activation), _make_dropout(dropout, seed, offset)
     dtype, dev, device = x.dtype, x.get_device(), x.device
-    with _entered(dev, stream):
+    with _entered(dev, stream) as on:
         px, ldx = _rows(x, "x", shape, dtype, dev)
         pw, ldw = _rows(w, "w", (r, q), dtype, dev)
         pr, ldr = _rows(residual, "residual", (p, r), dtype, dev)
@@ -470,6 +498,8 @@ def linear(x, w, bias=None, activation: str = "none", residual=None, dropout: fl
         work, pwork, nwork = _scratch(OZ2_LINEAR_FWD | _aligned(2 * q, (px, 2 * ldx), (pw, 2 * ldw)), kind, p, q, r, device)
         rc = _LIB.ozaki2_linear(kind, p, q, r, px, ldx, pw, ldw, pb, act, _dropout_ref(drop), pr, ldr,
                                 z.data_ptr() if return_z else None, r or 1, py, ldy, pwork, nwork, _raw_stream(dev))
+        if on is not None:
+            on.record((x, w, bias, residual, out), (y if out is None else None, z))
     if rc != OZ2_OK:
         raise Oz2Error(rc, "ozaki2_linear")
     return (y, z) if return_z else y
@@ -490,7 +520,7 @@ def linear_backward(dy, x, w, z=None, activation: str = "none", dropout: float =
     if act != OZ2_ACT_NONE and z is None:
         raise ValueError("the gradient of an activation needs z")
     dtype, dev, device = dy.dtype, dy.get_device(), dy.device
-    with _entered(dev, stream):
+    with _entered(dev, stream) as on:
         pdy, lddy = _rows(dy, "dy", shape, dtype, dev)
         px, ldx = _rows(x, "x", (p, q), dtype, dev)
         pw, ldw = _rows(w, "w", (r, q), dtype, dev)
@@ -503,6 +533,8 @@ def linear_backward(dy, x, w, z=None, activation: str = "none", dropout: float =
                                     dx.data_ptr() if dx is not None else None, q or 1,
                                     dw.data_ptr() if dw is not None else None, q or 1,
                                     db.data_ptr() if db is not None else None, pwork, nwork, _raw_stream(dev))
+        if on is not None:
+            on.record((dy, x, w, z), (dx, dw, db))
     if rc != OZ2_OK:
         raise Oz2Error(rc, "ozaki2_linear_bwd")
     return dx, dw, db
@@ -516,12 +548,14 @@ def dropout_add(x, residual=None, dropout: float = 0.0, seed: int = 0, offset: i
     p, r = shape = _shape2(x, "x")
     kind, drop = _kind(x, "x", f32=True), _make_dropout(dropout, seed, offset)
     dtype, dev = x.dtype, x.get_device()
-    with _entered(dev, stream):
+    with _entered(dev, stream) as on:
         px, ldx = _rows(x, "x", shape, dtype, dev)
         pr, ldr = _rows(residual, "residual", shape, dtype, dev)
         y = out if out is not None else x.new_empty((p, r))
         py, ldy = _rows(y, "out", shape, dtype, dev) if out is not None else (y.data_ptr(), r or 1)
         rc = _LIB.ozaki2_dropout_add(kind, p, r, px, ldx, pr, ldr, _dropout_ref(drop), py, ldy, _raw_stream(dev))
+        if on is not None:
+            on.record((x, residual, out), (y if out is None else None,))
     if rc != OZ2_OK:
         raise Oz2Error(rc, "ozaki2_dropout_add")
     return y
@@ -533,11 +567,13 @@ def quantize_rows(x, stream=None):
     p, q = shape = _shape2(x, "x")
     kind = _kind(x, "x", f32=True)
     dev, device = x.get_device(), x.device
-    with _entered(dev, stream):
+    with _entered(dev, stream) as on:
         px, ldx = _rows(x, "x", shape, x.dtype, dev)
         out = torch.empty((p, q), dtype=torch.int8, device=device)
         scale = torch.empty((p,), dtype=torch.float32, device=device)
         rc = _LIB.ozaki2_quantize_rows(kind, p, q, px, ldx, out.data_ptr(), q or 1, scale.data_ptr(), _raw_stream(dev))
+        if on is not None:
+            on.record((x,), (out, scale))
     if rc != OZ2_OK:
         raise Oz2Error(rc, "ozaki2_quantize_rows")
     return out, scale
@@ -553,7 +589,7 @@ def linear_i8(x, v, t, bias=None, activation: str = "none", residual=None, out=N
     if t is None:
         raise ValueError("t, the scales of v's rows, is needed")
     dtype, dev, device = x.dtype, x.get_device(), x.device
-    with _entered(dev, stream):
+    with _entered(dev, stream) as on:
         px, ldx = _rows(x, "x", shape, dtype, dev)
         pv, ldv = _rows(v, "v", (r, q), torch.int8, dev)
         pt = _vector(t, "t", r, torch.float32, dev)
@@ -564,6 +600,8 @@ def linear_i8(x, v, t, bias=None, activation: str = "none", residual=None, out=N
         work, pwork, nwork = _scratch(OZ2_LINEAR_I8 | _aligned(q, (pv, ldv)), kind, p, q, r, device)
         rc = _LIB.ozaki2_linear_i8(kind, p, q, r, px, ldx, pv, ldv, pt, pb, act, pr, ldr, py, ldy, pwork, nwork,
                                    _raw_stream(dev))
+        if on is not None:
+            on.record((x, v, t, bias, residual, out), (y if out is None else None,))
     if rc != OZ2_OK:
         raise Oz2Error(rc, "ozaki2_linear_i8")
     return y
