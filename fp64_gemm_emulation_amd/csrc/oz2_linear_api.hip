@@ -141,13 +141,19 @@ I8Work carve_i8(Carver& c, long p, long q, long r, bool pack_v) {
   return w;
 }
 
-// The call's workspace: the caller's if given, else the library's.
-int workspace(void* work, size_t work_bytes, size_t need, char** base) {
-  *base = static_cast<char*>(work);
+// Lays out the call's workspace, carve(carver), in the caller's memory if given, else in the
+// library's (where the size has to be known first).
+template <typename Work, typename F>
+int workspace(void* work, size_t work_bytes, Work& ws, F carve) {
   if (reinterpret_cast<uintptr_t>(work) % kAlign != 0) return OZ2_ERR_ARG;
-  if (need == 0) return OZ2_OK;
-  if (work == nullptr) return oz2::acquire_linear_workspace(need, base);
-  return work_bytes < need ? OZ2_ERR_WORKSPACE : OZ2_OK;
+  Carver c{static_cast<char*>(work)};
+  ws = carve(c);
+  if (work != nullptr) return work_bytes < c.used ? OZ2_ERR_WORKSPACE : OZ2_OK;
+  if (c.used == 0) return OZ2_OK;
+  Carver owned;
+  const int rc = oz2::acquire_linear_workspace(c.used, &owned.base);
+  if (rc == OZ2_OK) ws = carve(owned);
+  return rc;
 }
 
 int status(hipError_t e) { return e == hipSuccess ? OZ2_OK : OZ2_ERR_HIP; }
@@ -171,11 +177,9 @@ int ozaki2_linear(int type, int p, int q, int r, const void* X, int ldx, const v
   if (overlap(y, x) || overlap(y, w) || overlap(y, b) || overlap(y, z) || (overlap(y, res) && !same(y, res))) return OZ2_ERR_ARG;
   if (overlap(z, x) || overlap(z, w) || overlap(z, b) || overlap(z, res)) return OZ2_ERR_ARG;
   const bool pack_x = !oz2::rows_aligned(X, ldx, q, 2), pack_w = !oz2::rows_aligned(W, ldw, q, 2);
-  Carver need, c;
-  carve_fwd(need, p, q, r, pack_x, pack_w);
-  int rc = workspace(work, work_bytes, need.used, &c.base);
+  FwdWork ws;
+  int rc = workspace(work, work_bytes, ws, [&](Carver& c) { return carve_fwd(c, p, q, r, pack_x, pack_w); });
   if (rc != OZ2_OK) return rc;
-  const FwdWork ws = carve_fwd(c, p, q, r, pack_x, pack_w);
   const hipStream_t st = static_cast<hipStream_t>(stream);
   const long lp = oz2::packed_ld(q, 2);
   const oz2::PackJob jx{p, q, X, ldx, ws.x, lp}, jw{r, q, W, ldw, ws.w, lp};
@@ -228,11 +232,10 @@ int ozaki2_linear_bwd(int type, int p, int q, int r, const void* dY, int lddy, c
   const bool make_dz = product && p > 0 && r > 0 && (act != OZ2_ACT_NONE || drop.t != 0 || !oz2::rows_aligned(dY, lddy, r, 2));
   const bool pack_x = want_dw && p > 0 && !oz2::rows_aligned(X, ldx, q, 2);
   const bool pack_w = want_dx && r > 0 && !oz2::rows_aligned(W, ldw, q, 2);
-  Carver need, c;
-  carve_bwd(need, p, q, r, want_dx && want_dw, make_dz, pack_x, pack_w);
-  int rc = workspace(work, work_bytes, need.used, &c.base);
+  BwdWork ws;
+  int rc = workspace(work, work_bytes, ws,
+                     [&](Carver& c) { return carve_bwd(c, p, q, r, want_dx && want_dw, make_dz, pack_x, pack_w); });
   if (rc != OZ2_OK) return rc;
-  const BwdWork ws = carve_bwd(c, p, q, r, want_dx && want_dw, make_dz, pack_x, pack_w);
   const hipStream_t st = static_cast<hipStream_t>(stream);
   const long lq = oz2::packed_ld(q, 2), lr = oz2::packed_ld(r, 2);
   if (make_dz || want_db) {
@@ -297,11 +300,9 @@ int ozaki2_linear_i8(int type, int p, int q, int r, const void* X, int ldx, cons
   if (Y == nullptr || t == nullptr || (q > 0 && (X == nullptr || V == nullptr))) return OZ2_ERR_ARG;
   if (overlap(y, x) || overlap(y, v) || overlap(y, sc) || overlap(y, b) || (overlap(y, res) && !same(y, res))) return OZ2_ERR_ARG;
   const bool pack_v = !oz2::rows_aligned(V, ldv, q, 1);
-  Carver need, c;
-  carve_i8(need, p, q, r, pack_v);
-  int rc = workspace(work, work_bytes, need.used, &c.base);
+  I8Work ws;
+  int rc = workspace(work, work_bytes, ws, [&](Carver& c) { return carve_i8(c, p, q, r, pack_v); });
   if (rc != OZ2_OK) return rc;
-  const I8Work ws = carve_i8(c, p, q, r, pack_v);
   const hipStream_t st = static_cast<hipStream_t>(stream);
   const long lq = oz2::packed_ld(q, 1);
   const bool quantize = ws.q == nullptr;  // in the product
