@@ -331,11 +331,15 @@ def dgemm_debug(A, B, s: int = 14, mode: str = "fast", want=DUMP_FIELDS, stream=
 _torch = None
 _KINDS = {}          # torch dtype -> oz2_type_t
 _raw_stream = None   # device index -> hipStream_t of its current stream
+_current_device = None
+_grad_enabled = None
 
 
 def _use_torch():
-    global _torch, _raw_stream
+    global _torch, _raw_stream, _current_device, _grad_enabled
     import torch
+    _grad_enabled = torch.is_grad_enabled
+    _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
     _KINDS.update({torch.bfloat16: OZ2_BF16, torch.float16: OZ2_F16, torch.float32: OZ2_F32})
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
         (lambda index: torch.cuda.current_stream(index).cuda_stream)
@@ -410,6 +414,13 @@ def _make_dropout(dropout, seed, offset):
     return OZ2Dropout(dropout, seed, offset)
 
 
+def _no_autograd(name):
+    """The functions here compute no gradient by themselves: an operand whose gradient autograd
+    would be asked for is refused, rather than answered with a result that has lost it."""
+    raise ValueError(f"{name} is not differentiated by autograd: call it under torch.no_grad() (or on detached tensors) "
+                     "and take its gradients with linear_backward or dropout_add")
+
+
 class _NoContext:
     def __enter__(self):
         pass
@@ -455,7 +466,7 @@ def _entered(dev, stream):
         if stream.device.index != dev:
             raise ValueError("the stream belongs to another device than the operands")
         return _OnStream(stream)
-    return _NO_CONTEXT if dev == _torch.cuda.current_device() else _torch.cuda.device(dev)
+    return _NO_CONTEXT if dev == _current_device() else _torch.cuda.device(dev)
 
 
 def _aligned(row_bytes, *rows):
@@ -481,11 +492,15 @@ def linear(x, w, bias=None, activation: str = "none", residual=None, dropout: fl
            offset: int = 0, return_z: bool = False, out=None, stream=None):
     """residual + D(act(x w^T + bias)) for x [p, q], w [r, q] in bfloat16 or float16, D the
     dropout of the C header; with return_z, (y, z), z the pre-activation for
-    linear_backward.  `out` may be `residual` itself."""
+    linear_backward.  `out` may be `residual` itself.  No autograd: operands that require a
+    gradient are refused unless gradients are off."""
     torch = _torch or _use_torch()
     p, q = shape = _shape2(x, "x")
     r = _shape2(w, "w")[0]
     kind, act, drop = _kind(x, "x"), _activation(activation), _make_dropout(dropout, seed, offset)
+    if _grad_enabled() and (x.requires_grad or w.requires_grad or (bias is not None and bias.requires_grad)
+                            or (residual is not None and residual.requires_grad) or (out is not None and out.requires_grad)):
+        _no_autograd("linear")
     dtype, dev, device = x.dtype, x.get_device(), x.device
     with _entered(dev, stream) as on:
         px, ldx = _rows(x, "x", shape, dtype, dev)
@@ -543,10 +558,13 @@ def linear_backward(dy, x, w, z=None, activation: str = "none", dropout: float =
 def dropout_add(x, residual=None, dropout: float = 0.0, seed: int = 0, offset: int = 0, out=None, stream=None):
     """residual + D(x) for x [p, r] in bfloat16, float16 or float32; the gradient with respect
     to x is dropout_add(dy, None, ...) with the same dropout, seed and offset.  `out` may be x
-    or residual itself."""
+    or residual itself.  No autograd, as linear."""
     torch = _torch or _use_torch()
     p, r = shape = _shape2(x, "x")
     kind, drop = _kind(x, "x", f32=True), _make_dropout(dropout, seed, offset)
+    if _grad_enabled() and (x.requires_grad or (residual is not None and residual.requires_grad)
+                            or (out is not None and out.requires_grad)):
+        _no_autograd("dropout_add")
     dtype, dev = x.dtype, x.get_device()
     with _entered(dev, stream) as on:
         px, ldx = _rows(x, "x", shape, dtype, dev)
@@ -581,13 +599,17 @@ def quantize_rows(x, stream=None):
 
 def linear_i8(x, v, t, bias=None, activation: str = "none", residual=None, out=None, stream=None):
     """residual + act(x w^T + bias) with w held as (v, t) = quantize_rows(w): x [p, q] in
-    bfloat16 or float16 is quantised by rows in the call.  `out` may be `residual` itself."""
+    bfloat16 or float16 is quantised by rows in the call.  `out` may be `residual` itself.  No
+    autograd, as linear."""
     torch = _torch or _use_torch()
     p, q = shape = _shape2(x, "x")
     r = _shape2(v, "v")[0]
     kind, act = _kind(x, "x"), _activation(activation)
     if t is None:
         raise ValueError("t, the scales of v's rows, is needed")
+    if _grad_enabled() and (x.requires_grad or t.requires_grad or (bias is not None and bias.requires_grad)
+                            or (residual is not None and residual.requires_grad) or (out is not None and out.requires_grad)):
+        _no_autograd("linear_i8")
     dtype, dev, device = x.dtype, x.get_device(), x.device
     with _entered(dev, stream) as on:
         px, ldx = _rows(x, "x", shape, dtype, dev)
