@@ -421,6 +421,13 @@ def _no_autograd(name):
                      "and take its gradients with linear_backward or dropout_add")
 
 
+def _written(out):
+    """`out` was written without torch's knowledge: autograd's check of saved tensors goes by
+    its version."""
+    if not out.is_inference():
+        _torch.autograd.graph.increment_version(out)
+
+
 class _NoContext:
     def __enter__(self):
         pass
@@ -517,6 +524,8 @@ def linear(x, w, bias=None, activation: str = "none", residual=None, dropout: fl
             on.record((x, w, bias, residual, out), (y if out is None else None, z))
     if rc != OZ2_OK:
         raise Oz2Error(rc, "ozaki2_linear")
+    if out is not None:
+        _written(out)
     return (y, z) if return_z else y
 
 
@@ -576,6 +585,8 @@ def dropout_add(x, residual=None, dropout: float = 0.0, seed: int = 0, offset: i
             on.record((x, residual, out), (y if out is None else None,))
     if rc != OZ2_OK:
         raise Oz2Error(rc, "ozaki2_dropout_add")
+    if out is not None:
+        _written(out)
     return y
 
 
@@ -626,4 +637,6 @@ def linear_i8(x, v, t, bias=None, activation: str = "none", residual=None, out=N
             on.record((x, v, t, bias, residual, out), (y if out is None else None,))
     if rc != OZ2_OK:
         raise Oz2Error(rc, "ozaki2_linear_i8")
+    if out is not None:
+        _written(out)
     return y

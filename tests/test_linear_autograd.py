@@ -1,5 +1,5 @@
 """The linear-layer functions beside autograd: what would lose a gradient is refused (before any
-library call, so on the CPU)."""
+library call, so on the CPU), what runs is known to autograd as written."""
 import pytest
 import torch
 
@@ -29,6 +29,18 @@ def test_a_lost_gradient_is_refused(name, operand):
             getattr(oz, name)(**operands(name, operand))
     with pytest.raises(ValueError, match="CUDA"):
         getattr(oz, name)(**operands(name))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", list(SIZES))
+def test_a_written_tensor_has_a_new_version(name):
+    t = operands(name, device="cuda")
+    scale = torch.ones(4, 8, dtype=torch.float16, device="cuda", requires_grad=True)
+    loss = (t["out"] * scale).sum()          # saves out for scale's gradient
+    before = t["out"]._version
+    assert getattr(oz, name)(**t) is t["out"] and t["out"]._version > before
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
 
 
 @pytest.mark.gpu
