@@ -79,9 +79,9 @@ enum { kAlongDepth = 0, kAlongIndex = 1 };
 // columns (block b of a pair takes rows 8 g + 4 b + v of 32, g = 0..3, v = 0..3), and its s is
 // chosen for that set.  Along the index: depth rows of BM (BN) elements, 32-byte block c of row
 // k at block c ^ f(k), read with the transposing LDS read: 16 lanes fetch 4 depth rows x 16
-// indices, each lane 8 bytes, and each receives one index's 4 depths.  f takes 16 (256
-// elements) or, within either half of the wave, as many as there are blocks (8 or 4) values
-// over the rows one read touches.
+// indices, each lane 8 bytes, and each receives one index's 4 depths.  f takes 16 values
+// (256 elements), or 8 within either half of the wave (128 elements, 8 blocks), over the rows one
+// read touches.
 //
 // With two groups of waves (GROUPS = 2), each takes one half of every stage for all of the tile
 // and their sums meet in LDS at the end: one wave to a SIMD issues matrix instructions of this
@@ -129,7 +129,8 @@ __device__ __forceinline__ int chunk_swizzle(int i) {
 // f(k) of an operand along the index, depth rows of B elements.
 template <int B>
 __device__ __forceinline__ int block_swizzle(int k) {
-  return B >= 256 ? (k & 3) | (((k >> 3) & 3) << 2) : B >= 128 ? (k & 3) | (((k >> 3) & 1) << 2) : (k & 3);
+  static_assert(B == 128 || B == 256, "64-row tiles take their left operand along the depth");
+  return B == 256 ? (k & 3) | (((k >> 3) & 3) << 2) : (k & 3) | (((k >> 3) & 1) << 2);
 }
 
 // Byte offset, from the operand's tile origin in a stage, of the 16 bytes that lane `lane`
