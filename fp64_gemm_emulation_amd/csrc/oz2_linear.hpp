@@ -282,8 +282,9 @@ __device__ __forceinline__ float activation_slope(float z) {
 // Philox4x32-10 (Salmon, Moraes, Dror, Shaw, "Parallel random numbers: as easy as 1, 2, 3",
 // 2011).  One block serves eight consecutive elements of one row, 16 bits each: the keep
 // probability is then a multiple of 2^-16, and its exact value sets the scale, so the
-// expectation is exact; two blocks of 32-bit draws would double the generator's cost, which
-// is what bounds it (20 full-width multiplies at a quarter of the vector rate per block).
+// expectation is exact; two blocks of 32-bit draws would double the generator's cost (20
+// full-width multiplies at a quarter of the vector rate per block), which the matrix cores wait
+// for in an epilogue (in dropout_add the memory's time covers it).
 __host__ __device__ __forceinline__ void philox_block(uint32_t (&c)[4], uint32_t k0, uint32_t k1) {
   // a loop: unrolled into every eight outputs of an epilogue, the rounds alone outgrow the
   // instruction cache

@@ -23,12 +23,16 @@ struct Parts {
   double join(long rows, long cols) const { return used > 1 ? 3.0 + 8e-6 / 5.0 * used * rows * cols : 0.0; }
 };
 
-// Estimated times in microseconds, measured on bf16 products of 17 to 8192 rows, 1024 to 8192
-// columns and depths 512 to 8192 (within 15% there): a stage (128 bytes of depth) takes 1.55
-// on a 256 x 256 tile, one to a CU; 0.45 on a 128 x 128 tile alone on a CU (0.52 with an
-// operand along the index) and 0.5 each on two or more; 0.27 on a 64 x 128 tile; a launch with
-// its first loads and its epilogue 5.5, a join 3, and the partial sums' bytes 5 per 25 MB
-// written and read.
+// Estimated times in microseconds, from bf16 products with columns in whole vectors: a stage
+// (128 bytes of depth) takes 1.55 on a 256 x 256 tile, one to a CU; 0.45 on a 128 x 128 tile
+// alone on a CU (0.52 with an operand along the index) and 0.5 each on two or more; 0.27 on a
+// 64 x 128 tile; a launch with its first loads and its epilogue 5.5, a join 3, and the partial
+// sums' bytes 5 per 25 MB written and read.  Of 72 products of 32 to 8192 rows, 1000 to 8192
+// columns and depths 512 to 8192 timed against them, gradients take 0.91 to 1.12 of the estimate;
+// forward in 16 bits 0.9 to 1.1, but 0.73 to 0.83 with 32 and 100 rows and 1.2 at depth 512 on
+// 256 x 256 tiles; int8 0.76 to 1.33 (1.25 and more where one round of 128 x 128 tiles takes most
+// CUs).  Odd columns, whose stores the estimate leaves out, add up to 16%, and a third on
+// 256 x 256 tiles.
 constexpr double kLaunch = 5.5;
 static double alone128(bool along_index) { return along_index ? 0.52 : 0.45; }
 

@@ -90,10 +90,11 @@ enum { kAlongDepth = 0, kAlongIndex = 1 };
 //
 // What bounds it: the matrix cores, 70 to 74% busy at depth 8192 (LDS is active 27% of the time,
 // without bank conflicts in the loop); at depth 2048 the epilogue's instructions and stores as well
-// (58% busy in bf16, 43% in int8), which no other workgroup's products overlap.  Measured (bf16):
-// 8192^3 in 780 us, 1.41 PFLOP/s; 8192 x 2048 outputs at depth 8192 in 201 to 207 us in the three
-// layouts, 1.33 to 1.37 PFLOP/s; int8 8192^3 in 420 to 438 us, 2.5 to 2.6 POP/s; 1024 x 4096 at
-// depth 2048 (256 tiles of 128 x 128, one to a CU) in 21.8 us, 0.79 PFLOP/s.  32 x 32 matrix
+// (58% busy in bf16, 43% in int8), which no other workgroup's products overlap.  Measured (bf16,
+// on several boards): 8192^3 in 720 to 780 us, 1.41 to 1.53 PFLOP/s; 8192 x 2048 outputs at depth
+// 8192 in 191 to 207 us in the three layouts, 1.33 to 1.44 PFLOP/s; int8 8192^3 in 380 to 438 us,
+// 2.5 to 2.9 POP/s; 1024 x 4096 at depth 2048 (256 tiles of 128 x 128, one to a CU) in 21.3 to 21.8
+// us, 0.8 PFLOP/s.  32 x 32 matrix
 // instructions took 905 us for the first where these took 814, both before later steps.
 constexpr int kStageBytes = 128;
 
