@@ -298,8 +298,8 @@ int ozaki2_linear(int type, int p, int q, int r, const void* X, int ldx, const v
  * for dW only, W for dX only, Z only when act is not OZ2_ACT_NONE; `dropout` has to be the
  * forward call's.  dZ is rounded to `type` before the two products, which is what feeds the
  * matrix cores, but without dropout's scale, which multiplies the 32-bit sums, and in f16 with
- * the gelus and silu as half of it: so it is exact for none and relu, and finite for every
- * finite dY.  dbias sums the unrounded values.  At an infinite Z (an A past the type's range)
+ * the gelus and silu as half of it: so it is exact for none and relu, and no finite f16 dY
+ * overflows in it.  dbias sums the unrounded values.  At an infinite Z (an A past the type's range)
  * act' is its limit, 0 or 1.  Empty sizes give zero gradients.
  */
 int ozaki2_linear_bwd(int type, int p, int q, int r, const void* dY, int lddy, const void* X, int ldx, const void* W,

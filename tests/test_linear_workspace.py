@@ -32,7 +32,7 @@ def shim(tmp_path_factory):
 def followed(shim, *needs, limit=1 << 40):
     from fp64_gemm_emulation_amd.build import LIB_PATH
     env = dict(os.environ, SHIM_LIMIT=str(limit))
-    # the harness may preload a library of its own
+    # something may be preloaded already
     env["LD_PRELOAD"] = " ".join(filter(None, [shim, env.get("LD_PRELOAD")]))
     out = subprocess.run([sys.executable, "-c", PROGRAM, LIB_PATH, *map(str, needs)], env=env, capture_output=True,
                          text=True, timeout=120)
