@@ -28,6 +28,7 @@ OZ2_BF16, OZ2_F16, OZ2_F32 = 0, 1, 2
 OZ2_ACT_NONE, OZ2_ACT_RELU, OZ2_ACT_GELU, OZ2_ACT_GELU_TANH, OZ2_ACT_SILU = 0, 1, 2, 3, 4
 OZ2_LINEAR_FWD, OZ2_LINEAR_BWD, OZ2_LINEAR_I8, OZ2_LINEAR_ALIGNED = 0, 1, 2, 16
 OZ2_LINEAR_I8_MAX_Q = 131072
+OZ2_NORM_MAX_Q = 32768
 ACTIVATIONS = {"none": OZ2_ACT_NONE, "relu": OZ2_ACT_RELU, "gelu": OZ2_ACT_GELU, "gelu_tanh": OZ2_ACT_GELU_TANH,
                "silu": OZ2_ACT_SILU}
 
@@ -90,6 +91,11 @@ def _load():
         "ozaki2_quantize_rows": (i, [i, i, i, vp, i, vp, i, vp, vp]),
         "ozaki2_linear_i8": (i, [i, i, i, i, vp, i, vp, i, vp, vp, i, vp, i, vp, i, vp, sz, vp]),
         "ozaki2_linear_workspace_size": (sz, [i, i, i, i, i]),
+        "ozaki2_linear_i8_rows": (i, [i, i, i, i, vp, i, vp, vp, i, vp, vp, i, vp, i, vp, i, vp, sz, vp]),
+        "ozaki2_rms_norm": (i, [i, i, i, vp, i, vp, i, vp, ctypes.c_double, vp, i, vp, i, vp]),
+        "ozaki2_rms_norm_i8": (i, [i, i, i, vp, i, vp, i, vp, ctypes.c_double, vp, i, vp, i, vp, vp]),
+        "ozaki2_rms_norm_bwd": (i, [i, i, i, vp, i, vp, i, vp, ctypes.c_double, vp, i, vp, i, vp, vp, sz, vp]),
+        "ozaki2_rms_norm_bwd_workspace_size": (sz, [i, i, i]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -200,6 +206,26 @@ def ozaki2_linear_i8(type, p, q, r, X, ldx, V, ldv, t, bias, act, R, ldr, Y, ldy
 
 def ozaki2_linear_workspace_size(call, type, p, q, r) -> int:
     return _LIB.ozaki2_linear_workspace_size(call, type, p, q, r)
+
+
+def ozaki2_linear_i8_rows(type, p, q, r, Q, ldq, s, V, ldv, t, bias, act, R, ldr, Y, ldy, work, work_bytes, stream) -> int:
+    return _LIB.ozaki2_linear_i8_rows(type, p, q, r, Q, ldq, s, V, ldv, t, bias, act, R, ldr, Y, ldy, work, work_bytes, stream)
+
+
+def ozaki2_rms_norm(type, p, q, X, ldx, R, ldr, w, eps, H, ldh, Y, ldy, stream) -> int:
+    return _LIB.ozaki2_rms_norm(type, p, q, X, ldx, R, ldr, w, eps, H, ldh, Y, ldy, stream)
+
+
+def ozaki2_rms_norm_i8(type, p, q, X, ldx, R, ldr, w, eps, H, ldh, Q, ldq, scale, stream) -> int:
+    return _LIB.ozaki2_rms_norm_i8(type, p, q, X, ldx, R, ldr, w, eps, H, ldh, Q, ldq, scale, stream)
+
+
+def ozaki2_rms_norm_bwd(type, p, q, dY, lddy, H, ldh, w, eps, dH, lddh, dX, lddx, dw, work, work_bytes, stream) -> int:
+    return _LIB.ozaki2_rms_norm_bwd(type, p, q, dY, lddy, H, ldh, w, eps, dH, lddh, dX, lddx, dw, work, work_bytes, stream)
+
+
+def ozaki2_rms_norm_bwd_workspace_size(type, p, q) -> int:
+    return _LIB.ozaki2_rms_norm_bwd_workspace_size(type, p, q)
 
 
 # --- torch conveniences --------------------------------------------------------------
@@ -608,35 +634,150 @@ def quantize_rows(x, stream=None):
     return out, scale
 
 
-def linear_i8(x, v, t, bias=None, activation: str = "none", residual=None, out=None, stream=None):
+def linear_i8(x, v, t, bias=None, activation: str = "none", residual=None, out=None, stream=None, x_scale=None, dtype=None):
     """residual + act(x w^T + bias) with w held as (v, t) = quantize_rows(w): x [p, q] in
-    bfloat16 or float16 is quantised by rows in the call.  `out` may be `residual` itself.  No
-    autograd, as linear."""
+    bfloat16 or float16 is quantised by rows in the call, or is int8 already, with the scales
+    x_scale [p] of its rows (quantize_rows, rms_norm_i8) and dtype, the type of bias, residual and
+    result.  `out` may be `residual` itself.  No autograd, as linear."""
     torch = _torch or _use_torch()
     p, q = shape = _shape2(x, "x")
     r = _shape2(v, "v")[0]
-    kind, act = _kind(x, "x"), _activation(activation)
+    act = _activation(activation)
+    if x_scale is None:
+        kind = _kind(x, "x")
+        if dtype is not None and dtype != x.dtype:
+            raise ValueError("dtype is for int8 x: other results have x's type")
+        dtype = x.dtype
+    else:
+        kind = _KINDS.get(dtype)
+        if kind is None or kind == OZ2_F32:
+            raise ValueError(f"dtype, the result's type, must be bfloat16 or float16 with x_scale, not {dtype}")
+        if x_scale.requires_grad and _grad_enabled():
+            _no_autograd("linear_i8")
     if t is None:
         raise ValueError("t, the scales of v's rows, is needed")
     if _grad_enabled() and (x.requires_grad or t.requires_grad or (bias is not None and bias.requires_grad)
                             or (residual is not None and residual.requires_grad) or (out is not None and out.requires_grad)):
         _no_autograd("linear_i8")
-    dtype, dev, device = x.dtype, x.get_device(), x.device
+    dev, device = x.get_device(), x.device
     with _entered(dev, stream) as on:
-        px, ldx = _rows(x, "x", shape, dtype, dev)
+        px, ldx = _rows(x, "x", shape, dtype if x_scale is None else torch.int8, dev)
+        ps = _vector(x_scale, "x_scale", p, torch.float32, dev)
         pv, ldv = _rows(v, "v", (r, q), torch.int8, dev)
         pt = _vector(t, "t", r, torch.float32, dev)
         pr, ldr = _rows(residual, "residual", (p, r), dtype, dev)
         pb = _vector(bias, "bias", r, dtype, dev)
-        y = out if out is not None else x.new_empty((p, r))
+        y = out if out is not None else x.new_empty((p, r), dtype=dtype)
         py, ldy = _rows(y, "out", (p, r), dtype, dev) if out is not None else (y.data_ptr(), r or 1)
-        work, pwork, nwork = _scratch(OZ2_LINEAR_I8 | _aligned(q, (pv, ldv)), kind, p, q, r, device)
-        rc = _LIB.ozaki2_linear_i8(kind, p, q, r, px, ldx, pv, ldv, pt, pb, act, pr, ldr, py, ldy, pwork, nwork,
-                                   _raw_stream(dev))
+        aligned = _aligned(q, (pv, ldv)) if x_scale is None else _aligned(q, (px, ldx), (pv, ldv))
+        work, pwork, nwork = _scratch(OZ2_LINEAR_I8 | aligned, kind, p, q, r, device)
+        if x_scale is None:
+            rc = _LIB.ozaki2_linear_i8(kind, p, q, r, px, ldx, pv, ldv, pt, pb, act, pr, ldr, py, ldy, pwork, nwork,
+                                       _raw_stream(dev))
+        else:
+            rc = _LIB.ozaki2_linear_i8_rows(kind, p, q, r, px, ldx, ps, pv, ldv, pt, pb, act, pr, ldr, py, ldy, pwork, nwork,
+                                            _raw_stream(dev))
         if on is not None:
-            on.record((x, v, t, bias, residual, out), (y if out is None else None,))
+            on.record((x, x_scale, v, t, bias, residual, out), (y if out is None else None,))
     if rc != OZ2_OK:
         raise Oz2Error(rc, "ozaki2_linear_i8")
     if out is not None:
         _written(out)
     return y
+
+
+# --- norm ------------------------------------------------------------------------------
+def _norm_operands(name, x, weight, residual, hidden, out):
+    """(sizes, type code) after the checks that the forward calls share."""
+    shape = _shape2(x, "x")
+    kind = _kind(x, "x", f32=True)
+    if hidden is not None and residual is None:
+        raise ValueError("hidden is the sum with residual, which is not given")
+    if _grad_enabled() and any(t is not None and t.requires_grad for t in (x, weight, residual, hidden, out)):
+        raise ValueError(f"{name} is not differentiated by autograd: call it under torch.no_grad() (or on detached tensors) "
+                         "and take its gradients with rms_norm_backward")
+    return shape, kind
+
+
+def rms_norm(x, weight=None, residual=None, eps: float = 1e-6, out=None, hidden=None, stream=None):
+    """h (mean(h^2) + eps)^(-1/2) weight by rows, for x [p, q] in bfloat16, float16 or float32 and
+    weight [q] (None: ones): h = x, or, with a residual, h = x + residual, and the result is
+    (y, h), h what the residual stream carries on and rms_norm_backward needs.  `out` and `hidden`
+    receive y and h; each may be x or residual itself.  No autograd, as linear."""
+    torch = _torch or _use_torch()
+    shape, kind = _norm_operands("rms_norm", x, weight, residual, hidden, out)
+    (p, q), dtype, dev = shape, x.dtype, x.get_device()
+    with _entered(dev, stream) as on:
+        px, ldx = _rows(x, "x", shape, dtype, dev)
+        pr, ldr = _rows(residual, "residual", shape, dtype, dev)
+        pw = _vector(weight, "weight", q, dtype, dev)
+        y = out if out is not None else x.new_empty(shape)
+        py, ldy = _rows(y, "out", shape, dtype, dev)
+        h = hidden if hidden is not None or residual is None else x.new_empty(shape)
+        ph, ldh = _rows(h, "hidden", shape, dtype, dev)
+        rc = _LIB.ozaki2_rms_norm(kind, p, q, px, ldx, pr, ldr, pw, eps, ph, ldh, py, ldy, _raw_stream(dev))
+        if on is not None:
+            on.record((x, weight, residual, out, hidden), (y if out is None else None, h if hidden is None else None))
+    if rc != OZ2_OK:
+        raise Oz2Error(rc, "ozaki2_rms_norm")
+    for t in (out, hidden):
+        if t is not None:
+            _written(t)
+    return (y, h) if residual is not None else y
+
+
+def rms_norm_i8(x, weight=None, residual=None, eps: float = 1e-6, hidden=None, stream=None):
+    """rms_norm with the rows of its result as int8 levels and float32 scales, for
+    linear_i8(levels, ..., x_scale=scale): (levels, scale), with a residual (levels, scale, h).
+    No autograd, as linear."""
+    torch = _torch or _use_torch()
+    shape, kind = _norm_operands("rms_norm_i8", x, weight, residual, hidden, None)
+    (p, q), dtype, dev, device = shape, x.dtype, x.get_device(), x.device
+    with _entered(dev, stream) as on:
+        px, ldx = _rows(x, "x", shape, dtype, dev)
+        pr, ldr = _rows(residual, "residual", shape, dtype, dev)
+        pw = _vector(weight, "weight", q, dtype, dev)
+        levels = torch.empty((p, q), dtype=torch.int8, device=device)
+        scale = torch.empty((p,), dtype=torch.float32, device=device)
+        h = hidden if hidden is not None or residual is None else x.new_empty(shape)
+        ph, ldh = _rows(h, "hidden", shape, dtype, dev)
+        rc = _LIB.ozaki2_rms_norm_i8(kind, p, q, px, ldx, pr, ldr, pw, eps, ph, ldh, levels.data_ptr(), q or 1,
+                                     scale.data_ptr(), _raw_stream(dev))
+        if on is not None:
+            on.record((x, weight, residual, hidden), (levels, scale, h if hidden is None else None))
+    if rc != OZ2_OK:
+        raise Oz2Error(rc, "ozaki2_rms_norm_i8")
+    if hidden is not None:
+        _written(hidden)
+    return (levels, scale, h) if residual is not None else (levels, scale)
+
+
+def rms_norm_backward(dy, h, weight=None, dh=None, eps: float = 1e-6, needs=("x", "weight"), stream=None):
+    """(dx, dweight) of rms_norm from dy and its h (x itself without a residual); those not named in
+    `needs` are None.  dh is the gradient that reaches h from its other uses; dx, which holds it
+    too, is the gradient of x and of residual alike."""
+    torch = _torch or _use_torch()
+    p, q = shape = _shape2(dy, "dy")
+    kind = _kind(dy, "dy", f32=True)
+    unknown = set(needs) - {"x", "weight"}
+    if unknown:
+        raise ValueError(f"needs names {sorted(unknown)}: only x and weight have gradients here")
+    dtype, dev, device = dy.dtype, dy.get_device(), dy.device
+    with _entered(dev, stream) as on:
+        pdy, lddy = _rows(dy, "dy", shape, dtype, dev)
+        ph, ldh = _rows(h, "h", shape, dtype, dev)
+        pw = _vector(weight, "weight", q, dtype, dev)
+        pdh, lddh = _rows(dh, "dh", shape, dtype, dev)
+        dx = torch.empty((p, q), dtype=dtype, device=device) if "x" in needs else None
+        dw = torch.empty((q,), dtype=dtype, device=device) if "weight" in needs else None
+        n = _LIB.ozaki2_rms_norm_bwd_workspace_size(kind, p, q) if dw is not None else 0
+        work = torch.empty(n, dtype=torch.uint8, device=device) if n else None
+        rc = _LIB.ozaki2_rms_norm_bwd(kind, p, q, pdy, lddy, ph, ldh, pw, eps, pdh, lddh,
+                                      dx.data_ptr() if dx is not None else None, q or 1,
+                                      dw.data_ptr() if dw is not None else None, work.data_ptr() if n else None, n,
+                                      _raw_stream(dev))
+        if on is not None:
+            on.record((dy, h, weight, dh), (dx, dw))
+    if rc != OZ2_OK:
+        raise Oz2Error(rc, "ozaki2_rms_norm_bwd")
+    return dx, dw

@@ -7,56 +7,23 @@
 #include <cstdint>
 
 #include "oz2.h"
-#include "oz2_internal.hpp"
+#include "oz2_args.hpp"
 #include "oz2_linear.hpp"
 
-namespace {
+using namespace oz2::args;
 
-constexpr size_t kAlign = 256;
-constexpr long kMaxDim = 1L << 23;  // as for the FP64 products
+namespace {
 
 static_assert(OZ2_BF16 == oz2::kTypeBf16 && OZ2_F16 == oz2::kTypeF16 && OZ2_F32 == oz2::kTypeF32, "types");
 static_assert(OZ2_ACT_RELU == oz2::kActRelu && OZ2_ACT_GELU == oz2::kActGelu &&
                   OZ2_ACT_GELU_TANH == oz2::kActGeluTanh && OZ2_ACT_SILU == oz2::kActSilu,
               "activations");
 
-// One matrix argument: rows x cols elements, row stride ld.
-struct Mat {
-  const void* ptr;
-  long rows, cols, ld;
-  size_t elem;
-  bool empty() const { return ptr == nullptr || rows == 0 || cols == 0; }
-  size_t bytes() const { return elem * (static_cast<size_t>(ld) * (rows - 1) + cols); }
-};
-
-// Whether two matrices share an element: their address ranges meet, and, where their rows have
-// the same stride, so do the columns they take of it (two column ranges of one wide buffer are
-// apart although their address ranges interleave).
-bool overlap(const Mat& a, const Mat& b) {
-  if (a.empty() || b.empty()) return false;
-  const auto pa = reinterpret_cast<uintptr_t>(a.ptr), pb = reinterpret_cast<uintptr_t>(b.ptr);
-  if (pa >= pb + b.bytes() || pb >= pa + a.bytes()) return false;
-  const size_t pitch = a.elem * a.ld;
-  if (pitch != b.elem * b.ld) return true;
-  const size_t d = pb >= pa ? (pb - pa) % pitch : (pitch - (pa - pb) % pitch) % pitch;
-  return d < a.elem * a.cols || d + b.elem * b.cols > pitch;
-}
-
-bool same(const Mat& a, const Mat& b) { return a.ptr == b.ptr && a.ld == b.ld; }
-
-bool sizes_ok(int p, int q, int r) {
-  return p >= 0 && q >= 0 && r >= 0 && p <= kMaxDim && q <= kMaxDim && r <= kMaxDim;
-}
-
-bool ld_ok(const Mat& m) { return m.ptr == nullptr || m.ld >= std::max(1L, m.cols); }
-
 // One launch puts every 128 x 128 output tile along grid x (256 work-items each): that work-item
 // count has to stay in 32 bits.
 bool grid_ok(long rows, long cols) {
   return static_cast<uint64_t>((rows + 127) / 128) * static_cast<uint64_t>((cols + 127) / 128) * 256u < (1ull << 32);
 }
-
-size_t elem_of(int type) { return type == OZ2_F32 ? 4 : 2; }
 
 bool drop_ok(const oz2_dropout_t* d) { return d == nullptr || (d->probability >= 0.0 && d->probability <= 1.0); }
 
@@ -71,17 +38,6 @@ oz2::Drop make_drop(const oz2_dropout_t* d) {
   o.c3 = static_cast<uint32_t>(d->offset >> 32);
   return o;
 }
-
-// Workspace: consecutive aligned pieces of `base` (null while only the size is asked for).
-struct Carver {
-  char* base = nullptr;
-  size_t used = 0;
-  void* take(size_t bytes) {
-    void* const p = base != nullptr ? base + used : nullptr;
-    used += (bytes + kAlign - 1) / kAlign * kAlign;
-    return p;
-  }
-};
 
 // The workspace of each call: copies of operands that need packing, and what it makes itself.
 struct FwdWork {
@@ -141,22 +97,62 @@ I8Work carve_i8(Carver& c, long p, long q, long r, bool pack_v) {
   return w;
 }
 
-// Lays out the call's workspace, carve(carver), in the caller's memory if given, else in the
-// library's (where the size has to be known first).
-template <typename Work, typename F>
-int workspace(void* work, size_t work_bytes, Work& ws, F carve) {
-  if (reinterpret_cast<uintptr_t>(work) % kAlign != 0) return OZ2_ERR_ARG;
-  Carver c{static_cast<char*>(work)};
-  ws = carve(c);
-  if (work != nullptr) return work_bytes < c.used ? OZ2_ERR_WORKSPACE : OZ2_OK;
-  if (c.used == 0) return OZ2_OK;
-  Carver owned;
-  const int rc = oz2::acquire_linear_workspace(c.used, &owned.base);
-  if (rc == OZ2_OK) ws = carve(owned);
-  return rc;
+// The same for rows that are int8 already, whose copy q then is.
+I8Work carve_i8_rows(Carver& c, long p, long q, long r, bool pack_q, bool pack_v) {
+  I8Work w{};
+  w.plan = oz2::plan_product(true, p, r, q, false, false);
+  if (oz2::few_rows(w.plan)) return w;  // takes any rows
+  if (pack_q) w.q = static_cast<int8_t*>(c.take(p * oz2::packed_ld(q, 1)));
+  if (pack_v) w.v = static_cast<int8_t*>(c.take(r * oz2::packed_ld(q, 1)));
+  w.partial = c.take(oz2::partial_bytes(w.plan, p, r));
+  return w;
 }
 
-int status(hipError_t e) { return e == hipSuccess ? OZ2_OK : OZ2_ERR_HIP; }
+// linear_i8 on rows X of the outputs' type, or, where their scales are given, of int8.
+int linear_i8(int type, int p, int q, int r, const void* X, int ldx, const float* s, const int8_t* V, int ldv, const float* t,
+              const void* bias, int act, const void* R, int ldr, void* Y, int ldy, void* work, size_t work_bytes,
+              void* stream) {
+  if (type != OZ2_BF16 && type != OZ2_F16) return OZ2_ERR_ARG;
+  if (act < OZ2_ACT_NONE || act > OZ2_ACT_SILU || !sizes_ok(p, q, r)) return OZ2_ERR_ARG;
+  const size_t e = elem_of(type);
+  const bool levels = s != nullptr;
+  const Mat x{X, p, q, ldx, levels ? 1 : e}, xs{s, 1, p, p, sizeof(float)}, v{V, r, q, ldv, 1}, sc{t, 1, r, r, sizeof(float)},
+      b{bias, 1, r, r, e}, res{R, p, r, ldr, e}, y{Y, p, r, ldy, e};
+  if (!ld_ok(x) || !ld_ok(v) || !ld_ok(res) || !ld_ok(y)) return OZ2_ERR_ARG;
+  if (p == 0 || r == 0) return OZ2_OK;
+  if (q > OZ2_LINEAR_I8_MAX_Q || !grid_ok(p, r)) return OZ2_ERR_UNSUPPORTED;
+  if (Y == nullptr || t == nullptr || (q > 0 && (X == nullptr || V == nullptr))) return OZ2_ERR_ARG;
+  if (overlap(y, x) || overlap(y, xs) || overlap(y, v) || overlap(y, sc) || overlap(y, b) || (overlap(y, res) && !same(y, res)))
+    return OZ2_ERR_ARG;
+  const bool pack_v = !oz2::rows_aligned(V, ldv, q, 1), pack_q = levels && !oz2::rows_aligned(X, ldx, q, 1);
+  I8Work ws;
+  int rc = workspace(work, work_bytes, ws, [&](Carver& c) {
+    return levels ? carve_i8_rows(c, p, q, r, pack_q, pack_v) : carve_i8(c, p, q, r, pack_v);
+  });
+  if (rc != OZ2_OK) return rc;
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  const long lq = oz2::packed_ld(q, 1);
+  const bool quantize = !levels && ws.q == nullptr;  // in the product
+  if (!levels && !quantize) {
+    rc = status(oz2::launch_quantize_rows(type, p, q, X, ldx, ws.q, lq, static_cast<int>(lq), ws.scale, st));
+    if (rc != OZ2_OK) return rc;
+  }
+  const oz2::PackJob jq{p, q, X, ldx, ws.q, lq}, jv{r, q, V, ldv, ws.v, lq};
+  rc = status(oz2::launch_pack_rows(1, levels && ws.q != nullptr ? &jq : nullptr, ws.v != nullptr ? &jv : nullptr, st));
+  if (rc != OZ2_OK) return rc;
+  // (where q is cut inside 16 bytes, V is packed too, or read element by element)
+  oz2::Product pr{type,  true, p, r, q, ws.q != nullptr ? ws.q : X, ws.q != nullptr ? lq : ldx,
+                  false, ws.v != nullptr ? ws.v : V, ws.v != nullptr ? lq : ldv, false, {}, ws.plan, ws.partial, quantize};
+  pr.epi.bias = bias;
+  pr.epi.act = act;
+  pr.epi.res = R;
+  pr.epi.ldr = ldr;
+  pr.epi.y = Y;
+  pr.epi.ldy = ldy;
+  pr.epi.xs = levels ? s : ws.scale;
+  pr.epi.ws = t;
+  return status(oz2::launch_product(pr, st));
+}
 
 }  // namespace
 
@@ -289,41 +285,14 @@ int ozaki2_quantize_rows(int type, int p, int q, const void* X, int ldx, int8_t*
 int ozaki2_linear_i8(int type, int p, int q, int r, const void* X, int ldx, const int8_t* V, int ldv, const float* t,
                      const void* bias, int act, const void* R, int ldr, void* Y, int ldy, void* work,
                      size_t work_bytes, void* stream) {
-  if (type != OZ2_BF16 && type != OZ2_F16) return OZ2_ERR_ARG;
-  if (act < OZ2_ACT_NONE || act > OZ2_ACT_SILU || !sizes_ok(p, q, r)) return OZ2_ERR_ARG;
-  const size_t e = elem_of(type);
-  const Mat x{X, p, q, ldx, e}, v{V, r, q, ldv, 1}, sc{t, 1, r, r, sizeof(float)}, b{bias, 1, r, r, e},
-      res{R, p, r, ldr, e}, y{Y, p, r, ldy, e};
-  if (!ld_ok(x) || !ld_ok(v) || !ld_ok(res) || !ld_ok(y)) return OZ2_ERR_ARG;
-  if (p == 0 || r == 0) return OZ2_OK;
-  if (q > OZ2_LINEAR_I8_MAX_Q || !grid_ok(p, r)) return OZ2_ERR_UNSUPPORTED;
-  if (Y == nullptr || t == nullptr || (q > 0 && (X == nullptr || V == nullptr))) return OZ2_ERR_ARG;
-  if (overlap(y, x) || overlap(y, v) || overlap(y, sc) || overlap(y, b) || (overlap(y, res) && !same(y, res))) return OZ2_ERR_ARG;
-  const bool pack_v = !oz2::rows_aligned(V, ldv, q, 1);
-  I8Work ws;
-  int rc = workspace(work, work_bytes, ws, [&](Carver& c) { return carve_i8(c, p, q, r, pack_v); });
-  if (rc != OZ2_OK) return rc;
-  const hipStream_t st = static_cast<hipStream_t>(stream);
-  const long lq = oz2::packed_ld(q, 1);
-  const bool quantize = ws.q == nullptr;  // in the product
-  if (!quantize) {
-    rc = status(oz2::launch_quantize_rows(type, p, q, X, ldx, ws.q, lq, static_cast<int>(lq), ws.scale, st));
-    if (rc != OZ2_OK) return rc;
-  }
-  const oz2::PackJob jv{r, q, V, ldv, ws.v, lq};
-  if ((rc = status(oz2::launch_pack_rows(1, ws.v != nullptr ? &jv : nullptr, nullptr, st))) != OZ2_OK) return rc;
-  // (where q is cut inside 16 bytes, V is packed too, or read element by element)
-  oz2::Product pr{type,  true, p, r, q, quantize ? X : ws.q, quantize ? ldx : lq,
-                  false, ws.v != nullptr ? ws.v : V, ws.v != nullptr ? lq : ldv, false, {}, ws.plan, ws.partial, quantize};
-  pr.epi.bias = bias;
-  pr.epi.act = act;
-  pr.epi.res = R;
-  pr.epi.ldr = ldr;
-  pr.epi.y = Y;
-  pr.epi.ldy = ldy;
-  pr.epi.xs = ws.scale;
-  pr.epi.ws = t;
-  return status(oz2::launch_product(pr, st));
+  return linear_i8(type, p, q, r, X, ldx, nullptr, V, ldv, t, bias, act, R, ldr, Y, ldy, work, work_bytes, stream);
+}
+
+int ozaki2_linear_i8_rows(int type, int p, int q, int r, const int8_t* Q, int ldq, const float* s, const int8_t* V, int ldv,
+                          const float* t, const void* bias, int act, const void* R, int ldr, void* Y, int ldy, void* work,
+                          size_t work_bytes, void* stream) {
+  if (s == nullptr && p > 0 && r > 0) return OZ2_ERR_ARG;
+  return linear_i8(type, p, q, r, Q, ldq, s, V, ldv, t, bias, act, R, ldr, Y, ldy, work, work_bytes, stream);
 }
 
 size_t ozaki2_linear_workspace_size(int call, int type, int p, int q, int r) {

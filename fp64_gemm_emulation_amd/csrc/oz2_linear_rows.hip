@@ -126,7 +126,7 @@ __global__ __launch_bounds__(256) void column_sums_kernel(ColumnSums sums) {
 }
 
 hipError_t launch_column_sums(int type, const ColumnSums& sums, hipStream_t st) {
-  const auto kernel = type == kTypeBf16 ? column_sums_kernel<bf16> : column_sums_kernel<f16>;
+  const auto kernel = type == kTypeBf16 ? column_sums_kernel<bf16> : type == kTypeF16 ? column_sums_kernel<f16> : column_sums_kernel<float>;
   hipLaunchKernelGGL(kernel, dim3((sums.r + kSumColumns - 1) / kSumColumns), dim3(256), 0, st, sums);
   return hipGetLastError();
 }

@@ -340,6 +340,51 @@ typedef enum { OZ2_LINEAR_FWD = 0, OZ2_LINEAR_BWD = 1, OZ2_LINEAR_I8 = 2, OZ2_LI
  * need more. */
 size_t ozaki2_linear_workspace_size(int call, int type, int p, int q, int r);
 
+/* ozaki2_linear_i8_rows -- ozaki2_linear_i8 for rows that are int8 already: Q (p x q) and their
+ * scales s (p floats), as ozaki2_quantize_rows or ozaki2_rms_norm_i8 makes them.  `type` is that of
+ * bias, R and Y.  Workspace: as for ozaki2_linear_i8; with OZ2_LINEAR_ALIGNED the rows of Q are
+ * aligned too. */
+int ozaki2_linear_i8_rows(int type, int p, int q, int r, const int8_t* Q, int ldq, const float* s, const int8_t* V, int ldv,
+                          const float* t, const void* bias, int act, const void* R, int ldr, void* Y, int ldy, void* work,
+                          size_t work_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Root-mean-square norm, before the products of a layer.  Conventions as for the linear layers;
+ * type OZ2_BF16, OZ2_F16 or OZ2_F32 (of every matrix and of w).
+ */
+
+/* Longest row of the norm's calls; longer ones give OZ2_ERR_UNSUPPORTED. */
+#define OZ2_NORM_MAX_Q 32768
+
+/*
+ * ozaki2_rms_norm -- H = X + R, rounded to its type (R NULL: H = X), and, row by row,
+ * Y_ij = H_ij (mean_j H_ij^2 + eps)^(-1/2) w_j (w, q elements, NULL: ones).
+ *   eps : FLT_MIN to 1e6.
+ *   H   : NULL, or p x q that receives H: what a residual stream carries on, and what
+ *         ozaki2_rms_norm_bwd needs.  H and Y may each be X or R itself (same pointer and
+ *         leading dimension), but not the same one.
+ * The mean is held in f32; squares past f32's range are scaled, so any finite row has its norm.
+ */
+int ozaki2_rms_norm(int type, int p, int q, const void* X, int ldx, const void* R, int ldr, const void* w, double eps,
+                    void* H, int ldh, void* Y, int ldy, void* stream);
+
+/* ozaki2_rms_norm_i8 -- the same with Y's rows, unrounded, as int8 levels and one scale each, by the
+ * rule of ozaki2_quantize_rows: what ozaki2_linear_i8_rows takes. */
+int ozaki2_rms_norm_i8(int type, int p, int q, const void* X, int ldx, const void* R, int ldr, const void* w, double eps,
+                       void* H, int ldh, int8_t* Q, int ldq, float* scale, void* stream);
+
+/*
+ * ozaki2_rms_norm_bwd -- gradients of ozaki2_rms_norm from dY and H: with n_ij = H_ij rstd_i and
+ * g = dY w,  dX = rstd (g - n mean_j(g n)) + dH,  dw_j = sum_i dY_ij n_ij.
+ *   dH : NULL, or the gradient that reaches H from its other uses.
+ * dX is the gradient of X and of R alike.  dX and dw that are NULL are not computed; dX may be dY
+ * or dH itself.  work / work_bytes as in the linear layers, ozaki2_rms_norm_bwd_workspace_size
+ * bytes (none without dw).
+ */
+int ozaki2_rms_norm_bwd(int type, int p, int q, const void* dY, int lddy, const void* H, int ldh, const void* w, double eps,
+                        const void* dH, int lddh, void* dX, int lddx, void* dw, void* work, size_t work_bytes, void* stream);
+size_t ozaki2_rms_norm_bwd_workspace_size(int type, int p, int q);
+
 /* Static description of a status code. */
 const char* ozaki2_status_string(int status);
 
