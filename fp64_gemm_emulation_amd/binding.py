@@ -13,6 +13,7 @@ from __future__ import annotations
 import ctypes
 import importlib.util
 import os
+from typing import Any, NamedTuple
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG_DIR, "liboz2.so")
@@ -29,6 +30,7 @@ OZ2_ACT_NONE, OZ2_ACT_RELU, OZ2_ACT_GELU, OZ2_ACT_GELU_TANH, OZ2_ACT_SILU = 0, 1
 OZ2_LINEAR_FWD, OZ2_LINEAR_BWD, OZ2_LINEAR_I8, OZ2_LINEAR_ALIGNED = 0, 1, 2, 16
 OZ2_LINEAR_I8_MAX_Q = 131072
 OZ2_NORM_MAX_Q = 32768
+OZ2_MAX_TOP = 64
 ACTIVATIONS = {"none": OZ2_ACT_NONE, "relu": OZ2_ACT_RELU, "gelu": OZ2_ACT_GELU, "gelu_tanh": OZ2_ACT_GELU_TANH,
                "silu": OZ2_ACT_SILU}
 
@@ -96,6 +98,9 @@ def _load():
         "ozaki2_rms_norm_i8": (i, [i, i, i, vp, i, vp, i, vp, ctypes.c_double, vp, i, vp, i, vp, vp]),
         "ozaki2_rms_norm_bwd": (i, [i, i, i, vp, i, vp, i, vp, ctypes.c_double, vp, i, vp, i, vp, vp, sz, vp]),
         "ozaki2_rms_norm_bwd_workspace_size": (sz, [i, i, i]),
+        "ozaki2_token_logprobs": (i, [i, i, i, vp, i, vp, i, vp, vp, vp, vp, vp, vp, sz, vp]),
+        "ozaki2_token_logprobs_workspace_size": (sz, [i, i, i]),
+        "ozaki2_token_logprobs_bwd": (i, [i, i, i, vp, vp, i, vp, vp, vp, vp, vp, i, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -226,6 +231,20 @@ def ozaki2_rms_norm_bwd(type, p, q, dY, lddy, H, ldh, w, eps, dH, lddh, dX, lddx
 
 def ozaki2_rms_norm_bwd_workspace_size(type, p, q) -> int:
     return _LIB.ozaki2_rms_norm_bwd_workspace_size(type, p, q)
+
+
+def ozaki2_token_logprobs(type, p, v, L, ldl, tokens, top, logprob, lse, entropy, top_tokens, top_logprob, work, work_bytes,
+                          stream) -> int:
+    return _LIB.ozaki2_token_logprobs(type, p, v, L, ldl, tokens, top, logprob, lse, entropy, top_tokens, top_logprob, work,
+                                      work_bytes, stream)
+
+
+def ozaki2_token_logprobs_workspace_size(p, v, top) -> int:
+    return _LIB.ozaki2_token_logprobs_workspace_size(p, v, top)
+
+
+def ozaki2_token_logprobs_bwd(type, p, v, dlogprob, L, ldl, tokens, lse, dentropy, entropy, dL, lddl, stream) -> int:
+    return _LIB.ozaki2_token_logprobs_bwd(type, p, v, dlogprob, L, ldl, tokens, lse, dentropy, entropy, dL, lddl, stream)
 
 
 # --- torch conveniences --------------------------------------------------------------
@@ -781,3 +800,84 @@ def rms_norm_backward(dy, h, weight=None, dh=None, eps: float = 1e-6, needs=("x"
     if rc != OZ2_OK:
         raise Oz2Error(rc, "ozaki2_rms_norm_bwd")
     return dx, dw
+
+
+# --- log probabilities of tokens ----------------------------------------------------------
+class TokenLogprobs(NamedTuple):
+    """What token_logprobs gives for each row of the logits; None for what was not asked for."""
+
+    logprobs: Any       # [p] of the given tokens
+    lse: Any            # [p] log of the sum of exp(logits)
+    entropy: Any        # [p]
+    top_logprobs: Any   # [p, top], falling
+    top_tokens: Any     # [p, top] int64
+
+
+def token_logprobs(logits, tokens=None, top: int = 0, entropy: bool = False, stream=None):
+    """TokenLogprobs of logits [p, v] in bfloat16, float16 or float32: the log probability of each
+    row's token (tokens [p] int64; 0 where it is negative, as in padded places), lse, and, where
+    asked for, the entropy and the `top` largest log probabilities with their tokens.  Logits of
+    -Inf are masked.  No autograd, as linear: token_logprobs_backward gives the logits' gradient."""
+    torch = _torch or _use_torch()
+    p, v = shape = _shape2(logits, "logits")
+    kind = _kind(logits, "logits", f32=True)
+    if not 0 <= top <= min(v, OZ2_MAX_TOP):
+        raise ValueError(f"top must be 0 to {min(v, OZ2_MAX_TOP)}, not {top}")
+    if _grad_enabled() and logits.requires_grad:
+        raise ValueError("token_logprobs is not differentiated by autograd: call it under torch.no_grad() (or on detached "
+                         "tensors) and take its gradient with token_logprobs_backward")
+    dev, device = logits.get_device(), logits.device
+    with _entered(dev, stream) as on:
+        pl, ldl = _rows(logits, "logits", shape, logits.dtype, dev)
+        pt = _vector(tokens, "tokens", p, torch.int64, dev)
+        # the row's numbers in one allocation
+        made = torch.empty((1 + (tokens is not None) + bool(entropy), p), dtype=torch.float32, device=device)
+        lse, *rest = made.unbind(0)
+        logprobs = rest.pop(0) if tokens is not None else None
+        h = rest.pop(0) if entropy else None
+        best = torch.empty((p, top), dtype=torch.float32, device=device) if top else None
+        which = torch.empty((p, top), dtype=torch.int64, device=device) if top else None
+        n = _LIB.ozaki2_token_logprobs_workspace_size(p, v, top)
+        work = torch.empty(n, dtype=torch.uint8, device=device) if n else None
+        rc = _LIB.ozaki2_token_logprobs(kind, p, v, pl, ldl, pt, top, logprobs.data_ptr() if logprobs is not None else None,
+                                        lse.data_ptr(), h.data_ptr() if h is not None else None,
+                                        which.data_ptr() if top else None, best.data_ptr() if top else None,
+                                        work.data_ptr() if n else None, n, _raw_stream(dev))
+        if on is not None:
+            on.record((logits, tokens), (made, best, which))
+    if rc != OZ2_OK:
+        raise Oz2Error(rc, "ozaki2_token_logprobs")
+    return TokenLogprobs(logprobs, lse, h, best, which)
+
+
+def token_logprobs_backward(dlogprobs, logits, tokens, lse, dentropy=None, entropy=None, out=None, stream=None):
+    """The logits' gradient from dlogprobs [p] float32 (None: none) and dentropy [p] (None: none),
+    with lse and, for dentropy, entropy from token_logprobs.  `out` may be logits itself."""
+    torch = _torch or _use_torch()
+    p, v = shape = _shape2(logits, "logits")
+    kind = _kind(logits, "logits", f32=True)
+    if dlogprobs is not None and tokens is None:
+        raise ValueError("the gradient of log probabilities needs tokens")
+    if dentropy is not None and entropy is None:
+        raise ValueError("the gradient of the entropy needs entropy")
+    if lse is None:
+        raise ValueError("lse, as token_logprobs gives it, is needed")
+    if out is not None and out.requires_grad and _grad_enabled():
+        raise ValueError("out requires a gradient: token_logprobs_backward is not differentiated by autograd")
+    dtype, dev = logits.dtype, logits.get_device()
+    f32 = torch.float32
+    with _entered(dev, stream) as on:
+        pl, ldl = _rows(logits, "logits", shape, dtype, dev)
+        pd, pt = _vector(dlogprobs, "dlogprobs", p, f32, dev), _vector(tokens, "tokens", p, torch.int64, dev)
+        ps, pdh, ph = (_vector(lse, "lse", p, f32, dev), _vector(dentropy, "dentropy", p, f32, dev),
+                       _vector(entropy, "entropy", p, f32, dev))
+        d = out if out is not None else logits.new_empty(shape)
+        po, ldo = _rows(d, "out", shape, dtype, dev)
+        rc = _LIB.ozaki2_token_logprobs_bwd(kind, p, v, pd, pl, ldl, pt, ps, pdh, ph, po, ldo, _raw_stream(dev))
+        if on is not None:
+            on.record((dlogprobs, logits, tokens, lse, dentropy, entropy, out), (d if out is None else None,))
+    if rc != OZ2_OK:
+        raise Oz2Error(rc, "ozaki2_token_logprobs_bwd")
+    if out is not None:
+        _written(out)
+    return d

@@ -385,6 +385,45 @@ int ozaki2_rms_norm_bwd(int type, int p, int q, const void* dY, int lddy, const 
                         const void* dH, int lddh, void* dX, int lddx, void* dw, void* work, size_t work_bytes, void* stream);
 size_t ozaki2_rms_norm_bwd_workspace_size(int type, int p, int q);
 
+/* ------------------------------------------------------------------------------------------
+ * Log probabilities of tokens, behind a model's last product.  Conventions as for the linear
+ * layers; the logits L are p x v (one row per token, v the vocabulary's size), type OZ2_BF16,
+ * OZ2_F16 or OZ2_F32; everything else is f32 and int64.
+ */
+
+/* Most alternatives a call gives. */
+#define OZ2_MAX_TOP 64
+
+/*
+ * ozaki2_token_logprobs -- of each row l of L:
+ *   lse      log sum_j exp(l_j)
+ *   logprob  l_t - lse for the row's token t = tokens[i]; 0 for t < 0 (a padded place), NaN for
+ *            t >= v
+ *   entropy  -sum_j p_j log p_j, p = exp(l - lse)
+ *   top_tokens, top_logprob  p x top: the largest log probabilities, falling, and their indices;
+ *            of equal logits the lowest index first
+ * lse, entropy and logprob may each be NULL (tokens too without logprob); top is 0 to OZ2_MAX_TOP, and at
+ * most v.  Logits of -Inf are masked: probability 0.  A row of nothing else has lse and log
+ * probabilities of -Inf and entropy 0.  A row that holds +Inf or NaN has NaN for all its values;
+ * among its largest logits NaN counts as -Inf.  Sums are held in f32 relative to the row's
+ * maximum, and log probabilities taken relative to it, so large logits lose nothing.
+ * work / work_bytes as in the linear layers, ozaki2_token_logprobs_workspace_size bytes.
+ */
+int ozaki2_token_logprobs(int type, int p, int v, const void* L, int ldl, const int64_t* tokens, int top, float* logprob,
+                          float* lse, float* entropy, int64_t* top_tokens, float* top_logprob, void* work,
+                          size_t work_bytes, void* stream);
+size_t ozaki2_token_logprobs_workspace_size(int p, int v, int top);
+
+/*
+ * ozaki2_token_logprobs_bwd -- gradient of the logits from those of logprob and entropy (each may
+ * be NULL), with lse and, for dentropy, entropy as the forward call gave them:
+ *   dL_ij = dlogprob_i (delta_{j t_i} - p_ij) - dentropy_i p_ij (log p_ij + entropy_i)
+ * Rows with t < 0 have no part of logprob, rows with t >= v give NaN, rows of -Inf alone zeros.
+ * dL may be L itself (same pointer and leading dimension).
+ */
+int ozaki2_token_logprobs_bwd(int type, int p, int v, const float* dlogprob, const void* L, int ldl, const int64_t* tokens,
+                              const float* lse, const float* dentropy, const float* entropy, void* dL, int lddl, void* stream);
+
 /* Static description of a status code. */
 const char* ozaki2_status_string(int status);
 
