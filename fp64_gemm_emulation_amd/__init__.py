@@ -18,6 +18,7 @@ _BINDING_NAMES = {
     "OZ2_ERR_ARG", "OZ2_ERR_UNSUPPORTED", "OZ2_ERR_WORKSPACE", "OZ2_ERR_HIP",
     "linear", "linear_backward", "dropout_add", "quantize_rows", "linear_i8",
     "rms_norm", "rms_norm_i8", "rms_norm_backward", "token_logprobs", "token_logprobs_backward", "TokenLogprobs",
+    "linear_adapters",
 }
 
 

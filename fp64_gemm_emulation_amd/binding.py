@@ -29,6 +29,7 @@ OZ2_BF16, OZ2_F16, OZ2_F32 = 0, 1, 2
 OZ2_ACT_NONE, OZ2_ACT_RELU, OZ2_ACT_GELU, OZ2_ACT_GELU_TANH, OZ2_ACT_SILU = 0, 1, 2, 3, 4
 OZ2_LINEAR_FWD, OZ2_LINEAR_BWD, OZ2_LINEAR_I8, OZ2_LINEAR_ALIGNED = 0, 1, 2, 16
 OZ2_LINEAR_I8_MAX_Q = 131072
+OZ2_ADAPTER_MAX_RANK = 256
 OZ2_NORM_MAX_Q = 32768
 OZ2_MAX_TOP = 64
 ACTIVATIONS = {"none": OZ2_ACT_NONE, "relu": OZ2_ACT_RELU, "gelu": OZ2_ACT_GELU, "gelu_tanh": OZ2_ACT_GELU_TANH,
@@ -53,6 +54,14 @@ class OZ2Dropout(ctypes.Structure):
     """Mirror of oz2_dropout_t."""
 
     _fields_ = [("probability", ctypes.c_double), ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64)]
+
+
+class OZ2Adapters(ctypes.Structure):
+    """Mirror of oz2_adapters_t."""
+
+    _fields_ = [("count", ctypes.c_int32), ("rank", ctypes.c_int32), ("A", ctypes.c_void_p), ("lda", ctypes.c_int64),
+                ("stride_a", ctypes.c_int64), ("B", ctypes.c_void_p), ("ldb", ctypes.c_int64), ("stride_b", ctypes.c_int64),
+                ("index", ctypes.c_void_p), ("scale", ctypes.c_void_p)]
 
 
 def _share_hip_runtime():
@@ -94,6 +103,8 @@ def _load():
         "ozaki2_linear_i8": (i, [i, i, i, i, vp, i, vp, i, vp, vp, i, vp, i, vp, i, vp, sz, vp]),
         "ozaki2_linear_workspace_size": (sz, [i, i, i, i, i]),
         "ozaki2_linear_i8_rows": (i, [i, i, i, i, vp, i, vp, vp, i, vp, vp, i, vp, i, vp, i, vp, sz, vp]),
+        "ozaki2_linear_adapters": (i, [i, i, i, i, vp, i, vp, i, vp, i, vp, vp, i, vp, i, vp, sz, vp]),
+        "ozaki2_linear_adapters_workspace_size": (sz, [i, i, i, i, i, i]),
         "ozaki2_rms_norm": (i, [i, i, i, vp, i, vp, i, vp, ctypes.c_double, vp, i, vp, i, vp]),
         "ozaki2_rms_norm_i8": (i, [i, i, i, vp, i, vp, i, vp, ctypes.c_double, vp, i, vp, i, vp, vp]),
         "ozaki2_rms_norm_bwd": (i, [i, i, i, vp, i, vp, i, vp, ctypes.c_double, vp, i, vp, i, vp, vp, sz, vp]),
@@ -215,6 +226,17 @@ def ozaki2_linear_workspace_size(call, type, p, q, r) -> int:
 
 def ozaki2_linear_i8_rows(type, p, q, r, Q, ldq, s, V, ldv, t, bias, act, R, ldr, Y, ldy, work, work_bytes, stream) -> int:
     return _LIB.ozaki2_linear_i8_rows(type, p, q, r, Q, ldq, s, V, ldv, t, bias, act, R, ldr, Y, ldy, work, work_bytes, stream)
+
+
+def ozaki2_linear_adapters(type, p, q, r, X, ldx, W, ldw, bias, act, adapters: OZ2Adapters | None, R, ldr, Y, ldy, work,
+                           work_bytes, stream) -> int:
+    return _LIB.ozaki2_linear_adapters(type, p, q, r, X, ldx, W, ldw, bias, act,
+                                       ctypes.addressof(adapters) if adapters is not None else None, R, ldr, Y, ldy, work,
+                                       work_bytes, stream)
+
+
+def ozaki2_linear_adapters_workspace_size(type, p, q, r, rank, aligned) -> int:
+    return _LIB.ozaki2_linear_adapters_workspace_size(type, p, q, r, rank, aligned)
 
 
 def ozaki2_rms_norm(type, p, q, X, ldx, R, ldr, w, eps, H, ldh, Y, ldy, stream) -> int:
@@ -700,6 +722,61 @@ def linear_i8(x, v, t, bias=None, activation: str = "none", residual=None, out=N
             on.record((x, x_scale, v, t, bias, residual, out), (y if out is None else None,))
     if rc != OZ2_OK:
         raise Oz2Error(rc, "ozaki2_linear_i8")
+    if out is not None:
+        _written(out)
+    return y
+
+
+# --- adapters ---------------------------------------------------------------------------
+def _stack(t, name, shape, dtype, dev):
+    """(pointer, row stride, matrix stride) of a stack of row-major matrices."""
+    _check_operand(t, name, shape, dtype, dev)
+    count, rows, cols = shape
+    if 0 in shape:
+        return t.data_ptr(), cols or 1, 0
+    stride, ld, step = t.stride()
+    if (step != 1 and cols > 1) or (ld < cols and rows > 1):
+        raise ValueError(f"{name} must be a stack of row-major matrices (stride (any, ld >= columns, 1)), not stride {tuple(t.stride())}")
+    return t.data_ptr(), ld if rows > 1 else cols, stride if count > 1 else 0
+
+
+def linear_adapters(x, w, a, b, index, scale=None, bias=None, activation: str = "none", residual=None, out=None, stream=None):
+    """residual + act(x w^T + bias + scale_j (x a_j^T) b_j^T), j = index[i] for the row i of x, as
+    linear with low-rank adapters a [n, k, q], b [n, r, k] of many requests beside the shared w.
+    index [p] is int32; rows whose index is not in 0 .. n - 1 have no adapter.  scale [n] is
+    float32 (None: ones).  `out` may be `residual` itself.  No autograd, as linear."""
+    torch = _torch or _use_torch()
+    p, q = shape = _shape2(x, "x")
+    r = _shape2(w, "w")[0]
+    kind, act = _kind(x, "x"), _activation(activation)
+    if a.dim() != 3:
+        raise ValueError(f"a must be a 3-D tensor, not {a.dim()}-D")
+    n, k = a.shape[:2]
+    if index is None:
+        raise ValueError("index, the adapter of each row, is needed")
+    if _grad_enabled() and any(t is not None and t.requires_grad for t in (x, w, a, b, scale, bias, residual, out)):
+        raise ValueError("linear_adapters is not differentiated by autograd: call it under torch.no_grad() (or on detached tensors)")
+    dtype, dev, device = x.dtype, x.get_device(), x.device
+    with _entered(dev, stream) as on:
+        px, ldx = _rows(x, "x", shape, dtype, dev)
+        pw, ldw = _rows(w, "w", (r, q), dtype, dev)
+        pa, lda, stride_a = _stack(a, "a", (n, k, q), dtype, dev)
+        pb, ldb, stride_b = _stack(b, "b", (n, r, k), dtype, dev)
+        pi, ps = _vector(index, "index", p, torch.int32, dev), _vector(scale, "scale", n, torch.float32, dev)
+        pr, ldr = _rows(residual, "residual", (p, r), dtype, dev)
+        pbias = _vector(bias, "bias", r, dtype, dev)
+        y = out if out is not None else x.new_empty((p, r))
+        py, ldy = _rows(y, "out", (p, r), dtype, dev) if out is not None else (y.data_ptr(), r or 1)
+        aligned = 1 if _aligned(2 * q, (px, 2 * ldx), (pw, 2 * ldw)) else 0
+        nwork = _LIB.ozaki2_linear_adapters_workspace_size(kind, p, q, r, k, aligned)
+        work = torch.empty(nwork, dtype=torch.uint8, device=device) if nwork else None
+        adapters = OZ2Adapters(n, k, pa, lda, stride_a, pb, ldb, stride_b, pi, ps)
+        rc = _LIB.ozaki2_linear_adapters(kind, p, q, r, px, ldx, pw, ldw, pbias, act, ctypes.addressof(adapters), pr, ldr, py, ldy,
+                                         work.data_ptr() if nwork else None, nwork, _raw_stream(dev))
+        if on is not None:
+            on.record((x, w, a, b, index, scale, bias, residual, out), (y if out is None else None,))
+    if rc != OZ2_OK:
+        raise Oz2Error(rc, "ozaki2_linear_adapters")
     if out is not None:
         _written(out)
     return y

@@ -69,6 +69,26 @@ inline size_t partial_bytes(const Plan& plan, long rows, long cols) {
   return plan.splits > 1 ? 4 * static_cast<size_t>(plan.splits) * rows * ((cols + 7) / 8 * 8) : 0;
 }
 
+// Low-rank adapters beside a product, adapter a = index[m] of the row m (none outside 0 .. count - 1):
+// the row's sum gets S_m B_a^T before the epilogue, S_m = scale_a X_m A_a^T.
+struct Adapters {
+  int count, rank;
+  const void* a;  // [adapter][rank][depth], rows lda apart, adapters stride_a
+  long lda, stride_a;
+  const void* b;  // [adapter][cols][rank]
+  long ldb, stride_b;
+  const int32_t* index;
+  const float* scale;  // null: ones
+  // S as `parts` sums over parts of the depth, [part][row][pitch] f32; rows without an adapter are not
+  // written
+  float* s;
+  int parts;
+  __host__ __device__ int pitch() const { return (rank + 15) / 16 * 16; }
+};
+// Workgroups that share the depth of S.
+int adapter_parts(long rows, long depth);
+hipError_t launch_adapter_sums(int type, int rows, int depth, const void* x, long ldx, const Adapters& ad, hipStream_t st);
+
 // out[m][n] = epilogue(sum_k left(m, k) right(n, k)), m < rows, n < cols, k < depth.  An operand
 // lies along the depth (element (i, k) at i * ld + k) or along its index (at k * ld + i; products
 // without an epilogue only).  Rows must be as rows_aligned says, except for
@@ -109,6 +129,10 @@ struct PackJob {
 hipError_t launch_pack_rows(int elem, const PackJob* a, const PackJob* b, hipStream_t st);
 
 hipError_t launch_product(const Product& pr, hipStream_t st);
+// With adapters, whose S is there: 16-bit operands along the depth.
+hipError_t launch_product_adapters(const Product& pr, const Adapters& ad, hipStream_t st);
+hipError_t launch_adapters_bf16(const Product& pr, const Adapters& ad, hipStream_t st);
+hipError_t launch_adapters_f16(const Product& pr, const Adapters& ad, hipStream_t st);
 // Sums of a gradient's dZ over its rows: db = scale times the sum over `blocks` partial rows of
 // r floats (db null: none).
 struct ColumnSums {

@@ -43,10 +43,16 @@ oz2::Drop make_drop(const oz2_dropout_t* d) {
 struct FwdWork {
   oz2::Plan plan;
   void *x, *w, *partial;
+  float* s;  // of adapters
 };
 
-FwdWork carve_fwd(Carver& c, long p, long q, long r, bool pack_x, bool pack_w) {
+FwdWork carve_fwd(Carver& c, long p, long q, long r, bool pack_x, bool pack_w, int rank = 0) {
   FwdWork w{};
+  if (rank > 0) {
+    oz2::Adapters ad{};
+    ad.rank = rank;
+    w.s = static_cast<float*>(c.take(sizeof(float) * oz2::adapter_parts(p, q) * p * ad.pitch()));
+  }
   w.plan = oz2::plan_product(false, p, r, q, false, false);
   if (oz2::few_rows(w.plan)) return w;  // takes any rows
   if (pack_x) w.x = c.take(2 * p * oz2::packed_ld(q, 2));
@@ -108,6 +114,74 @@ I8Work carve_i8_rows(Carver& c, long p, long q, long r, bool pack_q, bool pack_v
   return w;
 }
 
+// Strides and sizes of adapters beside a product of depth q.
+bool adapters_ok(const oz2_adapters_t& a, int q) {
+  constexpr int64_t kMost = int64_t{1} << 36;  // so that offsets stay within 64 bits
+  return a.count >= 0 && a.count <= kMaxDim && a.rank >= 0 && a.lda >= std::max(1, q) && a.ldb >= std::max(1, a.rank) &&
+         a.stride_a >= 0 && a.stride_b >= 0 && std::max({a.lda, a.ldb, a.stride_a, a.stride_b}) < kMost;
+}
+
+// The elements from the first to the last of `count` matrices of rows x cols, as one row.
+Mat span(const void* ptr, long count, long stride, long rows, long ld, long cols, size_t elem) {
+  const long n = rows == 0 || cols == 0 ? 0 : (count - 1) * stride + (rows - 1) * ld + cols;
+  return {ptr, 1, n, n, elem};
+}
+
+// linear, with adapters where they are given.
+int linear(int type, int p, int q, int r, const void* X, int ldx, const void* W, int ldw, const void* bias, int act,
+           const oz2_dropout_t* dropout, const void* R, int ldr, void* Z, int ldz, void* Y, int ldy,
+           const oz2_adapters_t* adapters, void* work, size_t work_bytes, void* stream) {
+  if (type != OZ2_BF16 && type != OZ2_F16) return OZ2_ERR_ARG;
+  if (act < OZ2_ACT_NONE || act > OZ2_ACT_SILU || !drop_ok(dropout) || !sizes_ok(p, q, r)) return OZ2_ERR_ARG;
+  const size_t e = elem_of(type);
+  const Mat x{X, p, q, ldx, e}, w{W, r, q, ldw, e}, b{bias, 1, r, r, e}, res{R, p, r, ldr, e}, z{Z, p, r, ldz, e},
+      y{Y, p, r, ldy, e};
+  if (!ld_ok(x) || !ld_ok(w) || !ld_ok(res) || !ld_ok(z) || !ld_ok(y)) return OZ2_ERR_ARG;
+  if (adapters != nullptr && !adapters_ok(*adapters, q)) return OZ2_ERR_ARG;
+  if (p == 0 || r == 0) return OZ2_OK;
+  if (Y == nullptr || (q > 0 && (X == nullptr || W == nullptr))) return OZ2_ERR_ARG;
+  if (!grid_ok(p, r)) return OZ2_ERR_UNSUPPORTED;
+  if (overlap(y, x) || overlap(y, w) || overlap(y, b) || overlap(y, z) || (overlap(y, res) && !same(y, res))) return OZ2_ERR_ARG;
+  if (overlap(z, x) || overlap(z, w) || overlap(z, b) || overlap(z, res)) return OZ2_ERR_ARG;
+  const bool adapted = adapters != nullptr && adapters->count > 0 && adapters->rank > 0;
+  if (adapted) {
+    const oz2_adapters_t& a = *adapters;
+    if (a.rank > OZ2_ADAPTER_MAX_RANK) return OZ2_ERR_UNSUPPORTED;
+    if ((q > 0 && a.A == nullptr) || a.B == nullptr || a.index == nullptr) return OZ2_ERR_ARG;
+    const Mat read[] = {span(a.A, a.count, a.stride_a, a.rank, a.lda, q, e), span(a.B, a.count, a.stride_b, r, a.ldb, a.rank, e),
+                        {a.index, 1, p, p, sizeof(int32_t)}, {a.scale, 1, a.count, a.count, sizeof(float)}};
+    for (const Mat& m : read)
+      if (overlap(y, m)) return OZ2_ERR_ARG;
+  }
+  const bool pack_x = !oz2::rows_aligned(X, ldx, q, 2), pack_w = !oz2::rows_aligned(W, ldw, q, 2);
+  FwdWork ws;
+  int rc = workspace(work, work_bytes, ws, [&](Carver& c) { return carve_fwd(c, p, q, r, pack_x, pack_w, adapted ? adapters->rank : 0); });
+  if (rc != OZ2_OK) return rc;
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  const long lp = oz2::packed_ld(q, 2);
+  const oz2::PackJob jx{p, q, X, ldx, ws.x, lp}, jw{r, q, W, ldw, ws.w, lp};
+  rc = status(oz2::launch_pack_rows(2, ws.x != nullptr ? &jx : nullptr, ws.w != nullptr ? &jw : nullptr, st));
+  if (rc != OZ2_OK) return rc;
+  // (where q is cut inside 16 bytes, both are packed, with zeros behind)
+  oz2::Product pr{type,  false, p, r, q, ws.x != nullptr ? ws.x : X, ws.x != nullptr ? lp : ldx,
+                  false, ws.w != nullptr ? ws.w : W, ws.w != nullptr ? lp : ldw, false, {}, ws.plan, ws.partial, false};
+  pr.epi.bias = bias;
+  pr.epi.act = act;
+  pr.epi.drop = make_drop(dropout);
+  pr.epi.res = R;
+  pr.epi.ldr = ldr;
+  pr.epi.z = Z;
+  pr.epi.ldz = ldz;
+  pr.epi.y = Y;
+  pr.epi.ldy = ldy;
+  if (!adapted) return status(oz2::launch_product(pr, st));
+  const oz2_adapters_t& a = *adapters;
+  const oz2::Adapters ad{a.count, a.rank, a.A, a.lda, a.stride_a, a.B, a.ldb, a.stride_b, a.index, a.scale, ws.s, oz2::adapter_parts(p, q)};
+  rc = status(oz2::launch_adapter_sums(type, p, q, X, ldx, ad, st));
+  return rc != OZ2_OK ? rc : status(oz2::launch_product_adapters(pr, ad, st));
+}
+
+
 // linear_i8 on rows X of the outputs' type, or, where their scales are given, of int8.
 int linear_i8(int type, int p, int q, int r, const void* X, int ldx, const float* s, const int8_t* V, int ldv, const float* t,
               const void* bias, int act, const void* R, int ldr, void* Y, int ldy, void* work, size_t work_bytes,
@@ -161,39 +235,14 @@ extern "C" {
 int ozaki2_linear(int type, int p, int q, int r, const void* X, int ldx, const void* W, int ldw, const void* bias,
                   int act, const oz2_dropout_t* dropout, const void* R, int ldr, void* Z, int ldz, void* Y, int ldy,
                   void* work, size_t work_bytes, void* stream) {
-  if (type != OZ2_BF16 && type != OZ2_F16) return OZ2_ERR_ARG;
-  if (act < OZ2_ACT_NONE || act > OZ2_ACT_SILU || !drop_ok(dropout) || !sizes_ok(p, q, r)) return OZ2_ERR_ARG;
-  const size_t e = elem_of(type);
-  const Mat x{X, p, q, ldx, e}, w{W, r, q, ldw, e}, b{bias, 1, r, r, e}, res{R, p, r, ldr, e}, z{Z, p, r, ldz, e},
-      y{Y, p, r, ldy, e};
-  if (!ld_ok(x) || !ld_ok(w) || !ld_ok(res) || !ld_ok(z) || !ld_ok(y)) return OZ2_ERR_ARG;
-  if (p == 0 || r == 0) return OZ2_OK;
-  if (Y == nullptr || (q > 0 && (X == nullptr || W == nullptr))) return OZ2_ERR_ARG;
-  if (!grid_ok(p, r)) return OZ2_ERR_UNSUPPORTED;
-  if (overlap(y, x) || overlap(y, w) || overlap(y, b) || overlap(y, z) || (overlap(y, res) && !same(y, res))) return OZ2_ERR_ARG;
-  if (overlap(z, x) || overlap(z, w) || overlap(z, b) || overlap(z, res)) return OZ2_ERR_ARG;
-  const bool pack_x = !oz2::rows_aligned(X, ldx, q, 2), pack_w = !oz2::rows_aligned(W, ldw, q, 2);
-  FwdWork ws;
-  int rc = workspace(work, work_bytes, ws, [&](Carver& c) { return carve_fwd(c, p, q, r, pack_x, pack_w); });
-  if (rc != OZ2_OK) return rc;
-  const hipStream_t st = static_cast<hipStream_t>(stream);
-  const long lp = oz2::packed_ld(q, 2);
-  const oz2::PackJob jx{p, q, X, ldx, ws.x, lp}, jw{r, q, W, ldw, ws.w, lp};
-  rc = status(oz2::launch_pack_rows(2, ws.x != nullptr ? &jx : nullptr, ws.w != nullptr ? &jw : nullptr, st));
-  if (rc != OZ2_OK) return rc;
-  // (where q is cut inside 16 bytes, both are packed, with zeros behind)
-  oz2::Product pr{type,  false, p, r, q, ws.x != nullptr ? ws.x : X, ws.x != nullptr ? lp : ldx,
-                  false, ws.w != nullptr ? ws.w : W, ws.w != nullptr ? lp : ldw, false, {}, ws.plan, ws.partial, false};
-  pr.epi.bias = bias;
-  pr.epi.act = act;
-  pr.epi.drop = make_drop(dropout);
-  pr.epi.res = R;
-  pr.epi.ldr = ldr;
-  pr.epi.z = Z;
-  pr.epi.ldz = ldz;
-  pr.epi.y = Y;
-  pr.epi.ldy = ldy;
-  return status(oz2::launch_product(pr, st));
+  return linear(type, p, q, r, X, ldx, W, ldw, bias, act, dropout, R, ldr, Z, ldz, Y, ldy, nullptr, work, work_bytes, stream);
+}
+
+int ozaki2_linear_adapters(int type, int p, int q, int r, const void* X, int ldx, const void* W, int ldw, const void* bias,
+                           int act, const oz2_adapters_t* adapters, const void* R, int ldr, void* Y, int ldy, void* work,
+                           size_t work_bytes, void* stream) {
+  if (adapters == nullptr) return OZ2_ERR_ARG;
+  return linear(type, p, q, r, X, ldx, W, ldw, bias, act, nullptr, R, ldr, nullptr, r, Y, ldy, adapters, work, work_bytes, stream);
 }
 
 int ozaki2_linear_bwd(int type, int p, int q, int r, const void* dY, int lddy, const void* X, int ldx, const void* W,
@@ -316,6 +365,13 @@ size_t ozaki2_linear_workspace_size(int call, int type, int p, int q, int r) {
       carve_i8(c, p, q, r, !aligned);
       break;
   }
+  return c.used;
+}
+
+size_t ozaki2_linear_adapters_workspace_size(int type, int p, int q, int r, int rank, int aligned) {
+  if ((type != OZ2_BF16 && type != OZ2_F16) || !sizes_ok(p, q, r) || rank < 0 || rank > OZ2_ADAPTER_MAX_RANK) return 0;
+  Carver c;
+  carve_fwd(c, p, q, r, !aligned, !aligned, p > 0 && r > 0 ? rank : 0);
   return c.used;
 }
 

@@ -128,6 +128,10 @@ hipError_t launch_product(const Product& pr, hipStream_t st) {
   return pr.type == kTypeBf16 ? launch_product_bf16(pr, st) : launch_product_f16(pr, st);
 }
 
+hipError_t launch_product_adapters(const Product& pr, const Adapters& ad, hipStream_t st) {
+  return pr.type == kTypeBf16 ? launch_adapters_bf16(pr, ad, st) : launch_adapters_f16(pr, ad, st);
+}
+
 // ---- packing ------------------------------------------------------------------------------
 // Rows copied to a row stride of ld_out elements (a multiple of 16 bytes), zeros behind each
 // row's end: for operands whose rows do not all start on 16-byte boundaries, which the tile

@@ -175,12 +175,12 @@ __device__ __forceinline__ s16x4 read_transposed(__attribute__((address_space(3)
 
 // One workgroup: tile number wg, stages kt0 .. kt0 + per - 1 of the depth (as many as there
 // are), kt0 = per * part.  smem: RING stages.
-template <typename M, typename T, typename S, int LL, int RL, int OUT>
+template <typename M, typename T, typename S, int LL, int RL, int OUT, bool ADAPT = false>
 __device__ __forceinline__ void product_tile(char* smem, unsigned wg, int part, int rows, int cols, int depth, int per,
                                              const typename M::elem* __restrict__ left, long left_ld,
                                              const typename M::elem* __restrict__ right, long right_ld,
                                              const Epilogue& e, typename M::acc* __restrict__ partial, int tiles_m,
-                                             int tiles_n) {
+                                             int tiles_n, const Adapters* ad = nullptr) {
   typedef typename M::acc Acc;
   constexpr int E = sizeof(typename M::elem);
   constexpr int kDepth = kStageBytes / E;  // elements of depth per stage
@@ -439,6 +439,84 @@ __device__ __forceinline__ void product_tile(char* smem, unsigned wg, int part, 
     }
     OZ2_WAIT_LGKMCNT(0);
   }
+  if constexpr (ADAPT) {
+    // Adapters, with the first part of the depth: each adapter among the tile's rows in turn, its S and
+    // B as stages of 64 elements of rank in LDS like those of the depth.  Their products go to the rows
+    // that are the adapter's by selection, not by zeros in S: an infinity in one request's adapter
+    // stays out of the others' rows.  S is rounded to the operands' type, which is what feeds the
+    // matrix cores: half a step, 2^-8 in bf16 and 2^-11 in f16, of this term alone.
+    static_assert(E == 2 && LL == kAlongDepth && RL == kAlongDepth, "stages of both operands along the depth");
+    int own[MB];
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb) {
+      const long m = m0 + wm * (16 * MB) + 16 * mb + li;
+      own[mb] = m < rows && part == 0 ? ad->index[m] : -1;
+      if (own[mb] >= ad->count) own[mb] = -1;
+    }
+    int* const least = reinterpret_cast<int*>(smem + S::STAGE);
+    const int pitch = ad->pitch();
+    const long plane = static_cast<long>(rows) * pitch;
+    for (int current = -1;;) {
+      constexpr int kNone = 0x7FFFFFFF;
+      int next = kNone;
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb) next = own[mb] > current ? min(next, own[mb]) : next;
+#pragma unroll
+      for (int off = 8; off > 0; off >>= 1) next = min(next, __shfl_xor(next, off, 64));
+      __syncthreads();
+      if (lane == 0) least[wave] = next;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < S::WAVES; ++w) next = min(next, least[w]);
+      if (next == kNone) break;
+      current = next;
+      const T* const b = static_cast<const T*>(ad->b) + current * ad->stride_b;
+      for (int k0 = 0; k0 < ad->rank; k0 += 64) {
+        __syncthreads();
+        for (int n = tid; n < S::BM * 8; n += 64 * S::WAVES) {
+          const int i = n / 8, c = n % 8, k = k0 + 8 * c;
+          const long m = m0 + i;
+          T t[8] = {};
+          if (m < rows && k < ad->rank && ad->index[m] == current) {
+            float v[8] = {};
+            for (int j = 0; j < ad->parts; ++j) {
+              float x[8];
+              load8(ad->s + j * plane + m * pitch + k, 8, x);
+#pragma unroll
+              for (int u = 0; u < 8; ++u) v[u] += x[u];
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) t[u] = static_cast<T>(k + u < ad->rank ? v[u] : 0.0f);
+          }
+          __builtin_memcpy(smem + kStageBytes * i + 16 * (c ^ chunk_swizzle<false>(i)), t, 16);
+        }
+        for (int n = tid; n < S::BN * 8; n += 64 * S::WAVES) {
+          const int i = n / 8, c = n % 8, k = k0 + 8 * c;
+          i32x4 t = {0, 0, 0, 0};
+          if (n0 + i < cols && k < ad->rank) {
+            const raw8 r = load_raw8<T, false>(b, (n0 + i) * ad->ldb + k, ad->rank - k);
+            __builtin_memcpy(&t, &r, 16);
+          }
+          *reinterpret_cast<i32x4*>(smem + S::LEFT + kStageBytes * i + 16 * (c ^ chunk_swizzle<true>(i))) = t;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          if (S::GROUPS == 2 && half != group) continue;
+#pragma unroll
+          for (int g = 0; g < FR; ++g) read1(0, half, x0, g);
+#pragma unroll
+          for (int u = 0; u < kMma; ++u) {
+            const int mb = u / NB, nb = u % NB;
+            const Acc t = M::mma(x0[MB + nb], x0[mb], Acc{0, 0, 0, 0});
+            // (a row's products are all selected or none)
+            if (own[mb] == current) acc[mb][nb] += t;
+          }
+        }
+      }
+    }
+    __syncthreads();
+  }
   // Two groups: each gives the other half of its blocks and finishes the other half.
   constexpr int EMB = S::GROUPS == 1 ? MB : MB / 2;
   Acc sum[EMB][NB];
@@ -591,6 +669,16 @@ __global__ __launch_bounds__(64 * S::WAVES, S::PER_CU) void product_tile_kernel(
   __shared__ __attribute__((aligned(1024))) char smem[S::RING * S::STAGE];
   product_tile<M, T, S, LL, RL, OUT>(smem, blockIdx.x, blockIdx.y, rows, cols, depth, per, left, left_ld, right,
                                      right_ld, e, partial, tiles_m, tiles_n);
+}
+
+template <typename M, typename T, typename S, int OUT>
+__global__ __launch_bounds__(64 * S::WAVES, S::PER_CU) void product_adapters_kernel(
+    int rows, int cols, int depth, int per, const typename M::elem* __restrict__ left, long left_ld,
+    const typename M::elem* __restrict__ right, long right_ld, Epilogue e, typename M::acc* __restrict__ partial,
+    int tiles_m, int tiles_n, Adapters ad) {
+  __shared__ __attribute__((aligned(1024))) char smem[S::RING * S::STAGE];
+  product_tile<M, T, S, kAlongDepth, kAlongDepth, OUT, true>(smem, blockIdx.x, blockIdx.y, rows, cols, depth, per, left,
+                                                             left_ld, right, right_ld, e, partial, tiles_m, tiles_n, &ad);
 }
 
 // Two gradient products and the column sums in one launch: dX = dZ W on the first workgroups,
@@ -785,11 +873,12 @@ __device__ __forceinline__ i32x4 load_chunk(const E* row, int k, int depth) {
 
 constexpr int kFewWaves = 8;
 
-template <typename M, typename T, int R, bool QUANT, int ACT, bool FULL>
-__global__ __launch_bounds__(64 * kFewWaves) void product_few_kernel(int rows, int cols, int depth, int per,
-                                                                     const void* __restrict__ left, long left_ld,
-                                                                     const typename M::elem* __restrict__ right,
-                                                                     long right_ld, Epilogue e) {
+// ADAPT: the adapters' term, worked out behind the first loads of weights: S goes through LDS, and a
+// thread per output reads its row of B.
+template <typename M, typename T, int R, bool QUANT, int ACT, bool FULL, bool ADAPT = false>
+__device__ __forceinline__ void product_few(int rows, int cols, int depth, int per, const void* __restrict__ left, long left_ld,
+                                            const typename M::elem* __restrict__ right, long right_ld, Epilogue e,
+                                            const Adapters* ad = nullptr) {
   typedef typename M::elem E;
   typedef typename M::acc Acc;
   constexpr int G = 16 / R, kStep = G * 64 / sizeof(E), kDeep = 8;
@@ -861,6 +950,28 @@ __global__ __launch_bounds__(64 * kFewWaves) void product_few_kernel(int rows, i
     __syncthreads();
     e.xs = scales;
   }
+  float adapted = 0.0f;  // of output row threadIdx.x / R, column threadIdx.x % R
+  if constexpr (ADAPT) {
+    float* const s = reinterpret_cast<float*>(levels);  // rows of `pitch` floats
+    const int width = ad->pitch(), count = rows * width;
+    for (int i = threadIdx.x; i < count; i += blockDim.x) {
+      float v = 0.0f;
+      for (int j = 0; j < ad->parts; ++j) v += ad->s[static_cast<long>(j) * count + i];
+      s[i] = v;  // (of a row without an adapter something that is not used)
+    }
+    __syncthreads();
+    const int m = threadIdx.x / R, n = n0 + threadIdx.x % R;
+    const int a = m < rows && n < cols ? ad->index[m] : -1;
+    if (a >= 0 && a < ad->count) {
+      const T* const b = static_cast<const T*>(ad->b) + a * ad->stride_b + n * ad->ldb;
+      for (int k = 0; k < ad->rank; k += 8) {
+        float v[8];
+        load8(b + k, ad->rank - k, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) adapted += k + i < ad->rank ? v[i] * s[m * width + k + i] : 0.0f;
+      }
+    }
+  }
   const E* const lrow = QUANT ? nullptr : static_cast<const E*>(left) + lm * left_ld;
   auto load_left = [&](int k) {
     i32x4 v;
@@ -911,6 +1022,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void product_few_kernel(int rows, i
 #pragma unroll
       for (int g = 0; g < G; ++g) a += sums[v][g * R + m][(g * R + n) >> 2][n & 3];
     out[m][n] = static_cast<float>(a);
+    if constexpr (ADAPT) out[m][n] += adapted;  // (as many threads as outputs: one step)
   }
   __syncthreads();
   for (int i = threadIdx.x; i < rows * (R / 8); i += blockDim.x) {
@@ -921,6 +1033,22 @@ __global__ __launch_bounds__(64 * kFewWaves) void product_few_kernel(int rows, i
     for (int j = 0; j < 8; ++j) v[j] = out[m][c + j];
     finish8<T, ACT, FULL>(v, e, m, n0 + c, cols);
   }
+}
+
+template <typename M, typename T, int R, bool QUANT, int ACT, bool FULL>
+__global__ __launch_bounds__(64 * kFewWaves) void product_few_kernel(int rows, int cols, int depth, int per,
+                                                                     const void* __restrict__ left, long left_ld,
+                                                                     const typename M::elem* __restrict__ right,
+                                                                     long right_ld, Epilogue e) {
+  product_few<M, T, R, QUANT, ACT, FULL>(rows, cols, depth, per, left, left_ld, right, right_ld, e);
+}
+
+template <typename M, typename T, int R, int ACT, bool FULL>
+__global__ __launch_bounds__(64 * kFewWaves) void product_few_adapters_kernel(int rows, int cols, int depth, int per,
+                                                                              const void* __restrict__ left, long left_ld,
+                                                                              const typename M::elem* __restrict__ right,
+                                                                              long right_ld, Epilogue e, Adapters ad) {
+  product_few<M, T, R, false, ACT, FULL, true>(rows, cols, depth, per, left, left_ld, right, right_ld, e, &ad);
 }
 
 template <typename M, typename T, int R, bool QUANT>
@@ -940,6 +1068,63 @@ static hipError_t launch_few(const Product& pr, hipStream_t st) {
                        pr.left, pr.left_ld, static_cast<const E*>(pr.right), pr.right_ld, pr.epi);
   });
   return hipGetLastError();
+}
+
+// ---- products with adapters ---------------------------------------------------------------
+template <typename M, typename T, int R>
+static hipError_t launch_few_adapters(const Product& pr, const Adapters& ad, hipStream_t st) {
+  typedef typename M::elem E;
+  const int step = 16 / R * 64;
+  const int steps = (pr.depth * static_cast<int>(sizeof(E)) + step - 1) / step;
+  const int waves = steps >= 64 ? 8 : 4;  // as without adapters
+  const int per = (steps + waves - 1) / waves;
+  with_activation(pr.epi.act, [&](auto act) {
+    constexpr int ACT = decltype(act)::value;
+    const auto kernel = pr.cols % 8 == 0 ? product_few_adapters_kernel<M, T, R, ACT, true> : product_few_adapters_kernel<M, T, R, ACT, false>;
+    hipLaunchKernelGGL(kernel, dim3((pr.cols + R - 1) / R), dim3(64 * waves), sizeof(float) * pr.rows * ad.pitch(), st, pr.rows,
+                       pr.cols, pr.depth, per, pr.left, pr.left_ld, static_cast<const E*>(pr.right), pr.right_ld, pr.epi, ad);
+  });
+  return hipGetLastError();
+}
+
+template <typename M, typename T, typename S>
+static hipError_t launch_tile_adapters(const Product& pr, const Adapters& ad, hipStream_t st) {
+  typedef typename M::elem E;
+  const int tiles_m = (pr.rows + S::BM - 1) / S::BM, tiles_n = (pr.cols + S::BN - 1) / S::BN;
+  const int stages = (pr.depth * static_cast<int>(sizeof(E)) + kStageBytes - 1) / kStageBytes;
+  auto launch = [&](auto kernel, int parts) {
+    hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(tiles_m) * static_cast<unsigned>(tiles_n), parts), dim3(64 * S::WAVES), 0,
+                       st, pr.rows, pr.cols, pr.depth, (stages + parts - 1) / parts, static_cast<const E*>(pr.left), pr.left_ld,
+                       static_cast<const E*>(pr.right), pr.right_ld, pr.epi, static_cast<typename M::acc*>(pr.partial), tiles_m,
+                       tiles_n, ad);
+    return hipGetLastError();
+  };
+  if constexpr (S::BM < 256) {  // (a 256 x 256 tile's plan has one part)
+    if (pr.plan.splits > 1) {
+      const hipError_t err = launch(product_adapters_kernel<M, T, S, kOutPartial>, pr.plan.splits);
+      return err != hipSuccess ? err : launch_join<M, T>(pr, st);
+    }
+  }
+  return launch(product_adapters_kernel<M, T, S, kOutEpilogue>, 1);
+}
+
+template <typename M, typename T>
+static hipError_t launch_adapters(const Product& pr, const Adapters& ad, hipStream_t st) {
+  switch (pr.plan.tile) {
+    case kFew8:
+      return launch_few_adapters<M, T, 8>(pr, ad, st);
+    case kFew16:
+      return launch_few_adapters<M, T, 16>(pr, ad, st);
+    case kTile256:
+      return launch_tile_adapters<M, T, Tile256>(pr, ad, st);
+    case kTile128:
+      return launch_tile_adapters<M, T, Tile128>(pr, ad, st);
+    case kTile128Deep:
+      return launch_tile_adapters<M, T, Tile128Deep>(pr, ad, st);
+    case kTile64:
+      return launch_tile_adapters<M, T, Tile64>(pr, ad, st);
+  }
+  return hipErrorInvalidValue;
 }
 
 // Every product of one operand type.

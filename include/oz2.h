@@ -348,6 +348,36 @@ int ozaki2_linear_i8_rows(int type, int p, int q, int r, const int8_t* Q, int ld
                           const float* t, const void* bias, int act, const void* R, int ldr, void* Y, int ldy, void* work,
                           size_t work_bytes, void* stream);
 
+/* Low-rank adapters of many requests beside a shared projection.  Adapter a is A_a (rank x q, row
+ * stride lda, at A + a stride_a) and B_a (r x rank, row stride ldb, at B + a stride_b), strides in
+ * elements of the call's type; a stride of 0 shares one matrix among all.  index[i] is row i's
+ * adapter; a row whose index is outside 0 .. count - 1 has none.  scale (count floats, NULL: ones)
+ * multiplies each adapter's term. */
+#define OZ2_ADAPTER_MAX_RANK 256
+typedef struct oz2_adapters {
+  int32_t count;
+  int32_t rank; /* above OZ2_ADAPTER_MAX_RANK: OZ2_ERR_UNSUPPORTED */
+  const void* A;
+  int64_t lda, stride_a;
+  const void* B;
+  int64_t ldb, stride_b;
+  const int32_t* index; /* p of them, on the device */
+  const float* scale;
+} oz2_adapters_t;
+
+/*
+ * ozaki2_linear_adapters -- Y = R + act(A), A_i = X_i W^T + bias + scale_a (X_i A_a^T) B_a^T with
+ * a = index[i]: ozaki2_linear with the adapters' term in its product, for serving.  X_i A_a^T is
+ * summed in f32; on products of more than a few rows it is rounded to `type` before it meets B_a, as
+ * the matrix cores' operands are.  An adapter reaches its own rows only, whatever it holds.
+ * work / work_bytes: ozaki2_linear_adapters_workspace_size bytes, `aligned` 0 or, where rows are as
+ * OZ2_LINEAR_ALIGNED says, 1.
+ */
+int ozaki2_linear_adapters(int type, int p, int q, int r, const void* X, int ldx, const void* W, int ldw, const void* bias,
+                           int act, const oz2_adapters_t* adapters, const void* R, int ldr, void* Y, int ldy, void* work,
+                           size_t work_bytes, void* stream);
+size_t ozaki2_linear_adapters_workspace_size(int type, int p, int q, int r, int rank, int aligned);
+
 /* ------------------------------------------------------------------------------------------
  * Root-mean-square norm, before the products of a layer.  Conventions as for the linear layers;
  * type OZ2_BF16, OZ2_F16 or OZ2_F32 (of every matrix and of w).
