@@ -301,6 +301,85 @@ __device__ __forceinline__ void product_tile(char* smem, unsigned wg, int part, 
     for (int nb = 0; nb < NB; ++nb) acc[mb][nb] = Acc{0, 0, 0, 0};
   i32x4 x0[FR], x1[FR];
 
+  // Adapters: the sums start from S_m B_a^T, worked out while the first stages' copies are under way.
+  // A wave goes through the adapters of its rows, 64 at a time; where the depth has several parts or the
+  // tile two groups of waves, these share the adapters.  Fragments come straight from memory (a cache,
+  // mostly), and their products go to the rows that are the adapter's by selection, not by zeros in S:
+  // an infinity in one request's adapter stays out of the others' rows.  S is rounded to the operands'
+  // type, which is what feeds the matrix cores: half a step, 2^-8 in bf16 and 2^-11 in f16, of this
+  // term alone.
+  auto adapters_term = [&]() {
+    static_assert(!ADAPT || (E == 2 && LL == kAlongDepth && RL == kAlongDepth && MB % 4 == 0), "16-bit operands along the depth");
+    const int shares = static_cast<int>(gridDim.y) * S::GROUPS, share = part * S::GROUPS + group;
+    const int pitch = ad->pitch(), rank = ad->rank;
+    const long plane = static_cast<long>(rows) * pitch;
+#pragma unroll
+    for (int h = 0; h < MB / 4; ++h) {
+      const long base = m0 + wm * (16 * MB) + 64 * h;
+      int own = base + lane < rows ? ad->index[base + lane] : -1;
+      if (own >= ad->count) own = -1;
+      bool first = own >= 0;
+      for (int j = 0; j < 63; ++j) {
+        const int before = __builtin_amdgcn_readlane(own, j);
+        first = first && (j >= lane || before != own);
+      }
+      unsigned long todo = __ballot(first);
+      for (int n = 0; todo != 0; ++n) {
+        const int token = __builtin_ctzl(todo);
+        todo &= todo - 1;
+        if (n % shares != share) continue;
+        const int adapter = __builtin_amdgcn_readlane(own, token);
+        const unsigned long match = __ballot(own == adapter);
+        const T* const b = static_cast<const T*>(ad->b) + adapter * ad->stride_b;
+        for (int k0 = 0; k0 < rank; k0 += 64) {
+          i32x4 bf[NB][2];
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            const int col = n0 + wn * (16 * NB) + 32 * (nb >> 1) + 4 * (nb & 1) + 8 * (li >> 2) + (li & 3);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              const int k = k0 + 32 * half + 8 * lg;
+              bf[nb][half] = i32x4{0, 0, 0, 0};
+              if (col < cols && k < rank) {
+                const raw8 r = load_raw8<T, false>(b, col * ad->ldb + k, rank - k);
+                __builtin_memcpy(&bf[nb][half], &r, 16);
+              }
+            }
+          }
+#pragma unroll
+          for (int mb = 0; mb < 4; ++mb) {
+            if ((match >> (16 * mb) & 0xFFFF) == 0) continue;
+            const bool mine = match >> (16 * mb + li) & 1;
+            i32x4 sf[2];
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              const int k = k0 + 32 * half + 8 * lg;
+              float v[8] = {};
+              if (mine && k < pitch) {
+                const float* const s = ad->s + (base + 16 * mb + li) * pitch + k;
+                for (int j = 0; j < ad->parts; ++j) {
+                  float x[8];
+                  load8(s + j * plane, 8, x);
+#pragma unroll
+                  for (int u = 0; u < 8; ++u) v[u] += x[u];
+                }
+              }
+              T t[8];
+#pragma unroll
+              for (int u = 0; u < 8; ++u) t[u] = static_cast<T>(v[u]);
+              __builtin_memcpy(&sf[half], t, 16);
+            }
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+              Acc t = M::mma(bf[nb][0], sf[0], Acc{0, 0, 0, 0});
+              if (k0 + 32 < rank) t = M::mma(bf[nb][1], sf[1], t);
+              if (mine) acc[4 * h + mb][nb] += t;
+            }
+          }
+        }
+      }
+    }
+  };
   auto mma1 = [&](const i32x4 (&x)[FR], int u) {
     // block rows in order, the columns of every other one reversed: each step changes one operand
     const int mb = u / NB, nb = (mb & 1) ? NB - 1 - u % NB : u % NB;
@@ -384,6 +463,7 @@ __device__ __forceinline__ void product_tile(char* smem, unsigned wg, int part, 
 #pragma unroll
       for (int j = 0; j < COPIES; ++j) copy1(kt, j);
     }
+    if constexpr (ADAPT) adapters_term();
     wait_copies(0, S::RING - 1);
     OZ2_SCHED_FENCE();
     __builtin_amdgcn_s_barrier();
@@ -438,84 +518,6 @@ __device__ __forceinline__ void product_tile(char* smem, unsigned wg, int part, 
       }
     }
     OZ2_WAIT_LGKMCNT(0);
-  }
-  if constexpr (ADAPT) {
-    // Adapters, with the first part of the depth: each adapter among the tile's rows in turn, its S and
-    // B as stages of 64 elements of rank in LDS like those of the depth.  Their products go to the rows
-    // that are the adapter's by selection, not by zeros in S: an infinity in one request's adapter
-    // stays out of the others' rows.  S is rounded to the operands' type, which is what feeds the
-    // matrix cores: half a step, 2^-8 in bf16 and 2^-11 in f16, of this term alone.
-    static_assert(E == 2 && LL == kAlongDepth && RL == kAlongDepth, "stages of both operands along the depth");
-    int own[MB];
-#pragma unroll
-    for (int mb = 0; mb < MB; ++mb) {
-      const long m = m0 + wm * (16 * MB) + 16 * mb + li;
-      own[mb] = m < rows && part == 0 ? ad->index[m] : -1;
-      if (own[mb] >= ad->count) own[mb] = -1;
-    }
-    int* const least = reinterpret_cast<int*>(smem + S::STAGE);
-    const int pitch = ad->pitch();
-    const long plane = static_cast<long>(rows) * pitch;
-    for (int current = -1;;) {
-      constexpr int kNone = 0x7FFFFFFF;
-      int next = kNone;
-#pragma unroll
-      for (int mb = 0; mb < MB; ++mb) next = own[mb] > current ? min(next, own[mb]) : next;
-#pragma unroll
-      for (int off = 8; off > 0; off >>= 1) next = min(next, __shfl_xor(next, off, 64));
-      __syncthreads();
-      if (lane == 0) least[wave] = next;
-      __syncthreads();
-#pragma unroll
-      for (int w = 0; w < S::WAVES; ++w) next = min(next, least[w]);
-      if (next == kNone) break;
-      current = next;
-      const T* const b = static_cast<const T*>(ad->b) + current * ad->stride_b;
-      for (int k0 = 0; k0 < ad->rank; k0 += 64) {
-        __syncthreads();
-        for (int n = tid; n < S::BM * 8; n += 64 * S::WAVES) {
-          const int i = n / 8, c = n % 8, k = k0 + 8 * c;
-          const long m = m0 + i;
-          T t[8] = {};
-          if (m < rows && k < ad->rank && ad->index[m] == current) {
-            float v[8] = {};
-            for (int j = 0; j < ad->parts; ++j) {
-              float x[8];
-              load8(ad->s + j * plane + m * pitch + k, 8, x);
-#pragma unroll
-              for (int u = 0; u < 8; ++u) v[u] += x[u];
-            }
-#pragma unroll
-            for (int u = 0; u < 8; ++u) t[u] = static_cast<T>(k + u < ad->rank ? v[u] : 0.0f);
-          }
-          __builtin_memcpy(smem + kStageBytes * i + 16 * (c ^ chunk_swizzle<false>(i)), t, 16);
-        }
-        for (int n = tid; n < S::BN * 8; n += 64 * S::WAVES) {
-          const int i = n / 8, c = n % 8, k = k0 + 8 * c;
-          i32x4 t = {0, 0, 0, 0};
-          if (n0 + i < cols && k < ad->rank) {
-            const raw8 r = load_raw8<T, false>(b, (n0 + i) * ad->ldb + k, ad->rank - k);
-            __builtin_memcpy(&t, &r, 16);
-          }
-          *reinterpret_cast<i32x4*>(smem + S::LEFT + kStageBytes * i + 16 * (c ^ chunk_swizzle<true>(i))) = t;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          if (S::GROUPS == 2 && half != group) continue;
-#pragma unroll
-          for (int g = 0; g < FR; ++g) read1(0, half, x0, g);
-#pragma unroll
-          for (int u = 0; u < kMma; ++u) {
-            const int mb = u / NB, nb = u % NB;
-            const Acc t = M::mma(x0[MB + nb], x0[mb], Acc{0, 0, 0, 0});
-            // (a row's products are all selected or none)
-            if (own[mb] == current) acc[mb][nb] += t;
-          }
-        }
-      }
-    }
-    __syncthreads();
   }
   // Two groups: each gives the other half of its blocks and finishes the other half.
   constexpr int EMB = S::GROUPS == 1 ? MB : MB / 2;
@@ -873,8 +875,8 @@ __device__ __forceinline__ i32x4 load_chunk(const E* row, int k, int depth) {
 
 constexpr int kFewWaves = 8;
 
-// ADAPT: the adapters' term, worked out behind the first loads of weights: S goes through LDS, and a
-// thread per output reads its row of B.
+// ADAPT: the adapters' term, S and B read behind the first loads of weights: a thread per output adds
+// up its row of B with its token's S, which goes through LDS.
 template <typename M, typename T, int R, bool QUANT, int ACT, bool FULL, bool ADAPT = false>
 __device__ __forceinline__ void product_few(int rows, int cols, int depth, int per, const void* __restrict__ left, long left_ld,
                                             const typename M::elem* __restrict__ right, long right_ld, Epilogue e,
@@ -891,6 +893,13 @@ __device__ __forceinline__ void product_few(int rows, int cols, int depth, int p
   const int k0 = (li / R) * (64 / static_cast<int>(sizeof(E))) + (lane >> 4) * (16 / static_cast<int>(sizeof(E)));
   const E* const rrow = right + min(n0 + li % R, cols - 1) * right_ld;
   const int lm = min(li % R, rows - 1);
+  // adapters: thread m R + n has the output of row m, column n0 + n
+  const T* brow = nullptr;
+  if constexpr (ADAPT) {
+    const int m = threadIdx.x / R, n = n0 + static_cast<int>(threadIdx.x) % R;
+    const int a = m < rows && n < cols ? ad->index[m] : -1;
+    if (a >= 0 && a < ad->count) brow = static_cast<const T*>(ad->b) + a * ad->stride_b + n * ad->ldb;
+  }
   // this wave's steps: `per` of them, the last wave's the rest; whole steps in groups of kDeep
   const int steps = (depth + kStep - 1) / kStep, whole = depth / kStep;
   const int s0 = wave * per, s1 = min((wave + 1) * per, steps), s1w = min(s1, whole);
@@ -902,7 +911,20 @@ __device__ __forceinline__ void product_few(int rows, int cols, int depth, int p
   const bool deep = s0 + kDeep <= s1w;
   if (deep) load_weights(s0);
 
-  extern __shared__ __attribute__((aligned(16))) int8_t levels[];  // QUANT: rows of `pitch` bytes
+  // the first of B's row and of S are under way with the weights
+  constexpr int kHeldRank = 16;
+  raw8 held_b[kHeldRank / 8];
+  float held_s = 0.0f;
+  if constexpr (ADAPT) {
+#pragma unroll
+    for (int c = 0; c < kHeldRank / 8; ++c)
+      if (brow != nullptr && 8 * c < ad->rank) held_b[c] = load_raw8<T, false>(brow, 8 * c, ad->rank - 8 * c);
+    const int count = rows * ad->pitch();
+    if (static_cast<int>(threadIdx.x) < count)
+      for (int j = 0; j < ad->parts; ++j) held_s += ad->s[static_cast<long>(j) * count + threadIdx.x];
+  }
+
+  extern __shared__ __attribute__((aligned(16))) int8_t levels[];  // QUANT: rows of `pitch` bytes; ADAPT: S
   const int pitch = (depth + 15) / 16 * 16;
   if constexpr (QUANT) {
     // the thread's first kHeld groups of eight of each row stay in registers where there is one row
@@ -950,28 +972,6 @@ __device__ __forceinline__ void product_few(int rows, int cols, int depth, int p
     __syncthreads();
     e.xs = scales;
   }
-  float adapted = 0.0f;  // of output row threadIdx.x / R, column threadIdx.x % R
-  if constexpr (ADAPT) {
-    float* const s = reinterpret_cast<float*>(levels);  // rows of `pitch` floats
-    const int width = ad->pitch(), count = rows * width;
-    for (int i = threadIdx.x; i < count; i += blockDim.x) {
-      float v = 0.0f;
-      for (int j = 0; j < ad->parts; ++j) v += ad->s[static_cast<long>(j) * count + i];
-      s[i] = v;  // (of a row without an adapter something that is not used)
-    }
-    __syncthreads();
-    const int m = threadIdx.x / R, n = n0 + threadIdx.x % R;
-    const int a = m < rows && n < cols ? ad->index[m] : -1;
-    if (a >= 0 && a < ad->count) {
-      const T* const b = static_cast<const T*>(ad->b) + a * ad->stride_b + n * ad->ldb;
-      for (int k = 0; k < ad->rank; k += 8) {
-        float v[8];
-        load8(b + k, ad->rank - k, v);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) adapted += k + i < ad->rank ? v[i] * s[m * width + k + i] : 0.0f;
-      }
-    }
-  }
   const E* const lrow = QUANT ? nullptr : static_cast<const E*>(left) + lm * left_ld;
   auto load_left = [&](int k) {
     i32x4 v;
@@ -1013,6 +1013,16 @@ __device__ __forceinline__ void product_few(int rows, int cols, int depth, int p
     acc = M::mma(load_chunk(rrow, k, depth), x, acc);
   }
   sums[wave][li][lane >> 4] = acc;
+  if constexpr (ADAPT) {
+    float* const s = reinterpret_cast<float*>(levels);
+    const int count = rows * ad->pitch();
+    if (static_cast<int>(threadIdx.x) < count) s[threadIdx.x] = held_s;
+    for (int i = threadIdx.x + blockDim.x; i < count; i += blockDim.x) {
+      float v = 0.0f;
+      for (int j = 0; j < ad->parts; ++j) v += ad->s[static_cast<long>(j) * count + i];
+      s[i] = v;  // (of a row without an adapter something that is not used)
+    }
+  }
   __syncthreads();
   for (int i = threadIdx.x; i < R * R; i += blockDim.x) {
     const int m = i / R, n = i % R;
@@ -1022,7 +1032,24 @@ __device__ __forceinline__ void product_few(int rows, int cols, int depth, int p
 #pragma unroll
       for (int g = 0; g < G; ++g) a += sums[v][g * R + m][(g * R + n) >> 2][n & 3];
     out[m][n] = static_cast<float>(a);
-    if constexpr (ADAPT) out[m][n] += adapted;  // (as many threads as outputs: one step)
+    if constexpr (ADAPT) {  // (as many threads as outputs: one step)
+      if (brow != nullptr) {
+        const float* const s = reinterpret_cast<const float*>(levels) + m * ad->pitch();
+        float v = 0.0f;
+#pragma unroll
+        for (int c = 0; c < kHeldRank / 8; ++c)
+          if (8 * c < ad->rank) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v += raw_element<T>(held_b[c], j) * s[8 * c + j];
+          }
+        for (int k = kHeldRank; k < ad->rank; k += 8) {
+          const raw8 b = load_raw8<T, false>(brow, k, ad->rank - k);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v += raw_element<T>(b, j) * s[k + j];
+        }
+        out[m][n] += v;
+      }
+    }
   }
   __syncthreads();
   for (int i = threadIdx.x; i < rows * (R / 8); i += blockDim.x) {
