@@ -104,7 +104,7 @@ def _load():
         "ozaki2_linear_workspace_size": (sz, [i, i, i, i, i]),
         "ozaki2_linear_i8_rows": (i, [i, i, i, i, vp, i, vp, vp, i, vp, vp, i, vp, i, vp, i, vp, sz, vp]),
         "ozaki2_linear_adapters": (i, [i, i, i, i, vp, i, vp, i, vp, i, vp, vp, i, vp, i, vp, sz, vp]),
-        "ozaki2_linear_adapters_workspace_size": (sz, [i, i, i, i, i, i]),
+        "ozaki2_linear_adapters_workspace_size": (sz, [i, i, i, i, i, i, i]),
         "ozaki2_rms_norm": (i, [i, i, i, vp, i, vp, i, vp, ctypes.c_double, vp, i, vp, i, vp]),
         "ozaki2_rms_norm_i8": (i, [i, i, i, vp, i, vp, i, vp, ctypes.c_double, vp, i, vp, i, vp, vp]),
         "ozaki2_rms_norm_bwd": (i, [i, i, i, vp, i, vp, i, vp, ctypes.c_double, vp, i, vp, i, vp, vp, sz, vp]),
@@ -235,8 +235,8 @@ def ozaki2_linear_adapters(type, p, q, r, X, ldx, W, ldw, bias, act, adapters: O
                                        work_bytes, stream)
 
 
-def ozaki2_linear_adapters_workspace_size(type, p, q, r, rank, aligned) -> int:
-    return _LIB.ozaki2_linear_adapters_workspace_size(type, p, q, r, rank, aligned)
+def ozaki2_linear_adapters_workspace_size(type, p, q, r, count, rank, aligned) -> int:
+    return _LIB.ozaki2_linear_adapters_workspace_size(type, p, q, r, count, rank, aligned)
 
 
 def ozaki2_rms_norm(type, p, q, X, ldx, R, ldr, w, eps, H, ldh, Y, ldy, stream) -> int:
@@ -768,7 +768,7 @@ def linear_adapters(x, w, a, b, index, scale=None, bias=None, activation: str = 
         y = out if out is not None else x.new_empty((p, r))
         py, ldy = _rows(y, "out", (p, r), dtype, dev) if out is not None else (y.data_ptr(), r or 1)
         aligned = 1 if _aligned(2 * q, (px, 2 * ldx), (pw, 2 * ldw)) else 0
-        nwork = _LIB.ozaki2_linear_adapters_workspace_size(kind, p, q, r, k, aligned)
+        nwork = _LIB.ozaki2_linear_adapters_workspace_size(kind, p, q, r, n, k, aligned)
         work = torch.empty(nwork, dtype=torch.uint8, device=device) if nwork else None
         adapters = OZ2Adapters(n, k, pa, lda, stride_a, pb, ldb, stride_b, pi, ps)
         rc = _LIB.ozaki2_linear_adapters(kind, p, q, r, px, ldx, pw, ldw, pbias, act, ctypes.addressof(adapters), pr, ldr, py, ldy,

@@ -5,130 +5,176 @@
 
 namespace oz2 {
 
-// 16 TB tokens and one of their adapters per workgroup, blockIdx.y the first of them that it
-// takes (in the order of their first tokens) and blockIdx.z the part of the depth.  The matrix
+// 16 TB tokens and one of their adapters per workgroup, blockIdx.y the first of them that it takes (in
+// the order of their first tokens) and blockIdx.z the part of the depth.  The matrix
 // instruction's rows are 16 of the adapter's, its columns 16 tokens.  Operands go straight from
-// memory to registers: a wave has a block of tokens and a contiguous piece of the depth, in steps
-// of 32 elements, kDeep of them under way; the pieces start at different memory channels (rows a
-// power of two apart would otherwise all ask the same one).  Every column is computed and the
-// adapter's own tokens are stored.  RB: blocks of 16 rows that share the tokens' fragments; ranks above
-// 64 take several passes.
-constexpr int kSumWaves = 16;
-
-template <typename M, typename T, int RB, int TB>
-__global__ __launch_bounds__(64 * kSumWaves) void adapter_sums_kernel(int rows, int depth, int per, const T* __restrict__ x,
-                                                                      long ldx, Adapters ad) {
+// memory to registers: a wave has a piece of the depth, in steps of 32 elements, DEEP of them
+// under way.  Every token is computed and the adapter's own are stored.  RB: blocks of 16 rows of A
+// that share the tokens' fragments; ranks above 64 take several passes.
+template <typename M, typename T, int RB, int TB, int WAVES, int DEEP>
+__global__ __launch_bounds__(64 * WAVES) void adapter_sums_kernel(int rows, int depth, int per, const T* __restrict__ x, long ldx,
+                                                                  Adapters ad) {
   typedef typename M::acc Acc;
-  constexpr int kDeep = RB == 4 ? 2 : 4, kPieces = kSumWaves / TB;
-  __shared__ Acc sums[kPieces][TB][RB][64];
+  constexpr int kTokens = 16 * TB;
+  __shared__ Acc sums[WAVES][TB][RB][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int block = wave % TB, piece = wave / TB;
   const int li = lane & 15, lk = 8 * (lane >> 4);
-  const long m0 = 16l * TB * blockIdx.x;
-  // the adapter of the lane's token, and the tokens that are the first of theirs
-  int own = lane < 16 * TB && m0 + lane < rows ? ad.index[m0 + lane] : -1;
-  if (own >= ad.count) own = -1;
-  bool first = own >= 0;
-#pragma unroll
-  for (int j = 0; j < 16 * TB - 1; ++j) {
-    const int before = __builtin_amdgcn_readlane(own, j);
-    first = first && (j >= lane || before != own);
-  }
-  unsigned long firsts = __ballot(first);
-  const int part_begin = per * static_cast<int>(blockIdx.z), part_end = min(part_begin + per, depth);
-  const int steps = max(part_end - part_begin + 31, 0) / 32, each = (steps + kPieces - 1) / kPieces;
-  const int k_begin = part_begin + 32 * each * piece, k_end = min(k_begin + 32 * each, part_end);
-  const T* const xrow = x + min(m0 + 16 * block + li, static_cast<long>(rows) - 1) * ldx;
+  const long m0 = static_cast<long>(kTokens) * blockIdx.x;
+  const int own = lane < kTokens && m0 + lane < rows ? ad.index[m0 + lane] : -1;  // the adapter of the lane's token
+  unsigned long todo = __ballot(own >= 0 && own < ad.count);
   const int pitch = ad.pitch();
-  for (int n = 0; firsts != 0; ++n) {
-    const int token = __builtin_ctzl(firsts);
-    firsts &= firsts - 1;
-    if (n % gridDim.y != blockIdx.y) continue;
-    const int adapter = __builtin_amdgcn_readlane(own, token);
+  const int part_begin = per * static_cast<int>(blockIdx.z), part_end = min(part_begin + per, depth);
+  const int steps = max(part_end - part_begin + 31, 0) / 32, each = (steps + WAVES - 1) / WAVES;
+  const int k_begin = part_begin + 32 * each * wave, k_end = min(k_begin + 32 * each, part_end);
+  const int whole = max(k_end - k_begin, 0) / 32;  // steps that the depth does not cut
+  for (int n = 0; todo != 0; ++n) {
+    const int token = __builtin_ctzl(todo), adapter = __builtin_amdgcn_readlane(own, token);
     const unsigned long match = __ballot(own == adapter);
+    todo &= ~match;
+    if (n % gridDim.y != blockIdx.y) continue;
+    const float scale = ad.scale != nullptr ? ad.scale[adapter] : 1.0f;
+    // a block without a token of the adapter's reads the first token's block again
+    const T* xrow[TB];
+#pragma unroll
+    for (int t = 0; t < TB; ++t) {
+      const int block = match >> (16 * t) & 0xFFFF ? t : token / 16;
+      xrow[t] = x + min(m0 + 16 * block + li, static_cast<long>(rows) - 1) * ldx;
+    }
     for (int r0 = 0; r0 < ad.rank; r0 += 16 * RB) {
       const T* arow[RB];
 #pragma unroll
       for (int b = 0; b < RB; ++b)
         arow[b] = static_cast<const T*>(ad.a) + adapter * ad.stride_a + min(r0 + 16 * b + li, ad.rank - 1) * ad.lda;
-      Acc acc[RB] = {};
-      if (match >> (16 * block) & 0xFFFF) {
-        int k = k_begin;
-        for (; k + 32 * kDeep <= k_end; k += 32 * kDeep) {
-          i32x4 xv[kDeep], av[kDeep][RB];
+      Acc acc[TB][RB] = {};
+      // N steps' loads under way together: without the fence the compiler puts each next to its use
+      auto group = [&](int s, auto n) {
+        constexpr int N = decltype(n)::value;
+        i32x4 xv[N][TB], av[N][RB];
 #pragma unroll
-          for (int j = 0; j < kDeep; ++j) {
-            __builtin_memcpy(&xv[j], xrow + k + 32 * j + lk, 16);
+        for (int j = 0; j < N; ++j) {
+          const int k = k_begin + 32 * (s + j) + lk;
 #pragma unroll
-            for (int b = 0; b < RB; ++b) __builtin_memcpy(&av[j][b], arow[b] + k + 32 * j + lk, 16);
-          }
+          for (int b = 0; b < RB; ++b) __builtin_memcpy(&av[j][b], arow[b] + k, 16);
 #pragma unroll
-          for (int j = 0; j < kDeep; ++j)
-#pragma unroll
-            for (int b = 0; b < RB; ++b) acc[b] = M::mma(av[j][b], xv[j], acc[b]);
+          for (int t = 0; t < TB; ++t) __builtin_memcpy(&xv[j][t], xrow[t] + k, 16);
         }
-        for (; k < k_end; k += 32) {
-          const i32x4 xv = load_chunk(xrow, k + lk, k_end);
-          i32x4 av[RB];
+        OZ2_SCHED_FENCE();
 #pragma unroll
-          for (int b = 0; b < RB; ++b) av[b] = load_chunk(arow[b], k + lk, k_end);
+        for (int j = 0; j < N; ++j)
 #pragma unroll
-          for (int b = 0; b < RB; ++b) acc[b] = M::mma(av[b], xv, acc[b]);
+          for (int t = 0; t < TB; ++t)
+#pragma unroll
+            for (int b = 0; b < RB; ++b) acc[t][b] = M::mma(av[j][b], xv[j][t], acc[t][b]);
+      };
+      int s = 0;
+      for (; s + DEEP <= whole; s += DEEP) group(s, std::integral_constant<int, DEEP>{});
+      for (; s + 2 <= whole; s += 2) group(s, std::integral_constant<int, 2>{});
+      if (s < whole) group(s, std::integral_constant<int, 1>{});
+      if (k_begin + 32 * whole < k_end) {
+        const int k = k_begin + 32 * whole + lk;
+        i32x4 av[RB];
+#pragma unroll
+        for (int b = 0; b < RB; ++b) av[b] = load_chunk(arow[b], k, k_end);
+#pragma unroll
+        for (int t = 0; t < TB; ++t) {
+          const i32x4 xv = load_chunk(xrow[t], k, k_end);
+#pragma unroll
+          for (int b = 0; b < RB; ++b) acc[t][b] = M::mma(av[b], xv, acc[t][b]);
         }
       }
       __syncthreads();
 #pragma unroll
-      for (int b = 0; b < RB; ++b) sums[piece][block][b][lane] = acc[b];
+      for (int t = 0; t < TB; ++t)
+#pragma unroll
+        for (int b = 0; b < RB; ++b) sums[wave][t][b][lane] = acc[t][b];
       __syncthreads();
       // four rows of one block for one token each
-      for (int i = threadIdx.x; i < TB * RB * 64; i += 64 * kSumWaves) {
+      for (int i = threadIdx.x; i < TB * RB * 64; i += 64 * WAVES) {
         const int t = i / (64 * RB), b = i / 64 % RB, l = i % 64, r = r0 + 16 * b + 4 * (l / 16);
         if ((match >> (16 * t + l % 16) & 1) == 0 || r >= pitch) continue;
         Acc s = sums[0][t][b][l];
 #pragma unroll
-        for (int w = 1; w < kPieces; ++w) s += sums[w][t][b][l];
-        s *= ad.scale != nullptr ? ad.scale[adapter] : 1.0f;
+        for (int w = 1; w < WAVES; ++w) s += sums[w][t][b][l];
 #pragma unroll
-        for (int v = 0; v < 4; ++v)
-          if (r + v >= ad.rank) s[v] = 0.0f;
-        *reinterpret_cast<Acc*>(ad.s + (static_cast<long>(blockIdx.z) * rows + m0 + 16 * t + l % 16) * pitch + r) = s;
+        for (int v = 0; v < 4; ++v) s[v] = r + v < ad.rank ? s[v] * scale : 0.0f;
+        const long m = m0 + 16 * t + l % 16;
+        if (ad.rounded) {
+          T half[4];
+#pragma unroll
+          for (int v = 0; v < 4; ++v) half[v] = static_cast<T>(s[v]);
+          __builtin_memcpy(static_cast<T*>(ad.s) + m * pitch + r, half, sizeof(half));
+        } else {
+          *reinterpret_cast<Acc*>(static_cast<float*>(ad.s) + (static_cast<long>(blockIdx.z) * rows + m) * pitch + r) = s;
+        }
       }
     }
   }
 }
 
-// Few tokens: the depth is divided until there are about as many workgroups as CUs, into parts of
-// at least 512.
-int adapter_parts(long rows, long depth) {
-  const long groups = rows <= 256 ? (rows + 15) / 16 * std::min(rows, 16L) : (rows + 31) / 32;
-  const long wanted = std::min({(256 + groups - 1) / std::max(groups, 1L), depth / 512, 16L});
-  return static_cast<int>(std::max(wanted, 1L));
+constexpr int kSmallGroups = 256;  // rows up to which a workgroup takes 16 tokens, not 64
+
+// Parts of the depth for few rows (the product adds them up): where a wave's piece would be longer than
+// what it has under way.
+int adapter_parts(const Plan& plan, long rows, long depth) {
+  if (plan.tile == kTile256) return 1;
+  return static_cast<int>(std::max(1L, std::min({depth / 1024, 256 / std::max(rows, 1L), 16L})));
 }
 
 template <typename M, typename T>
 static hipError_t adapter_sums(int rows, int depth, const void* x, long ldx, const Adapters& ad, hipStream_t st) {
   const int per = ((depth + ad.parts - 1) / ad.parts + 31) / 32 * 32;
-  auto launch = [&](auto ranks, auto tokens) {
-    constexpr int RB = decltype(ranks)::value, TB = decltype(tokens)::value;
-    // few tokens may have an adapter each; many, in long requests, mostly share one
-    const dim3 grid((rows + 16 * TB - 1) / (16 * TB), TB == 1 ? std::min(rows, 16) : 1, ad.parts);
-    hipLaunchKernelGGL((adapter_sums_kernel<M, T, RB, TB>), grid, dim3(64 * kSumWaves), 0, st, rows, depth, per,
+  auto launch = [&](auto rb, auto tb, auto waves, auto deep) {
+    constexpr int RB = decltype(rb)::value, TB = decltype(tb)::value, WAVES = decltype(waves)::value, DEEP = decltype(deep)::value;
+    const int groups = (rows + 16 * TB - 1) / (16 * TB);
+    // workgroups that find no adapter left to them end at once
+    const dim3 grid(groups, std::min({rows, 16 * TB, std::max(2, 1024 / groups)}), ad.parts);
+    hipLaunchKernelGGL((adapter_sums_kernel<M, T, RB, TB, WAVES, DEEP>), grid, dim3(64 * WAVES), 0, st, rows, depth, per,
                        static_cast<const T*>(x), ldx, ad);
   };
-  auto blocks = [&](auto ranks) {
-    rows <= 256 ? launch(ranks, std::integral_constant<int, 1>{}) : launch(ranks, std::integral_constant<int, 2>{});
-  };
-  if (ad.rank <= 16)
-    blocks(std::integral_constant<int, 1>{});
-  else if (ad.rank <= 32)
-    blocks(std::integral_constant<int, 2>{});
-  else
-    blocks(std::integral_constant<int, 4>{});
+  using std::integral_constant;
+  if (rows <= kSmallGroups) {
+    constexpr integral_constant<int, 1> tb;
+    constexpr integral_constant<int, 16> waves;
+    if (ad.rank <= 16)
+      launch(integral_constant<int, 1>{}, tb, waves, integral_constant<int, 8>{});
+    else if (ad.rank <= 32)
+      launch(integral_constant<int, 2>{}, tb, waves, integral_constant<int, 8>{});
+    else
+      launch(integral_constant<int, 4>{}, tb, waves, integral_constant<int, 4>{});
+  } else {
+    constexpr integral_constant<int, 4> tb;
+    constexpr integral_constant<int, 8> waves;
+    if (ad.rank <= 16)
+      launch(integral_constant<int, 1>{}, tb, waves, integral_constant<int, 4>{});
+    else if (ad.rank <= 32)
+      launch(integral_constant<int, 2>{}, tb, waves, integral_constant<int, 4>{});
+    else
+      launch(integral_constant<int, 4>{}, tb, waves, integral_constant<int, 4>{});
+  }
   return hipGetLastError();
 }
 
 hipError_t launch_adapter_sums(int type, int rows, int depth, const void* x, long ldx, const Adapters& ad, hipStream_t st) {
   return type == kTypeBf16 ? adapter_sums<MmaBf16, bf16>(rows, depth, x, ldx, ad, st) : adapter_sums<MmaF16, f16>(rows, depth, x, ldx, ad, st);
+}
+
+// A thread per 16 bytes; blockIdx.y the adapter.
+__global__ __launch_bounds__(256) void pack_adapters_kernel(Adapters ad, int cols, uint16_t* dst) {
+  const int per_row = packed_rank(ad.rank) / 8;
+  const long n = static_cast<long>(blockIdx.x) * 256 + threadIdx.x, row = n / per_row;
+  if (row >= cols) return;
+  for (int a = blockIdx.y; a < ad.count; a += gridDim.y) {
+    const uint16_t* const src = static_cast<const uint16_t*>(ad.b) + a * ad.stride_b + row * ad.ldb;
+    const i32x4 v = load_chunk(src, 8 * static_cast<int>(n % per_row), ad.rank);
+    *reinterpret_cast<i32x4*>(dst + 8 * (a * static_cast<long>(cols) * per_row + n)) = v;
+  }
+}
+
+hipError_t launch_pack_adapters(const Adapters& ad, int cols, void* dst, hipStream_t st) {
+  const long n = static_cast<long>(cols) * (packed_rank(ad.rank) / 8);
+  const dim3 grid(static_cast<unsigned>((n + 255) / 256), std::min(ad.count, 32768));
+  hipLaunchKernelGGL(pack_adapters_kernel, grid, dim3(256), 0, st, ad, cols, static_cast<uint16_t*>(dst));
+  return hipGetLastError();
 }
 
 }  // namespace oz2

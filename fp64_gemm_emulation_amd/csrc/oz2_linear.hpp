@@ -79,14 +79,20 @@ struct Adapters {
   long ldb, stride_b;
   const int32_t* index;
   const float* scale;  // null: ones
-  // S as `parts` sums over parts of the depth, [part][row][pitch] f32; rows without an adapter are not
-  // written
-  float* s;
+  // S, pitch() elements to a row; rows without an adapter are not written.  For a product of few rows
+  // as `parts` sums over parts of the depth, [part][row][pitch] in f32, for the others rounded to the
+  // operands' type where that is one part.
+  void* s;
   int parts;
+  bool rounded;
+  // (a product of more than a few rows reads B in pieces of 8 elements of rank: ranks between are packed)
   __host__ __device__ int pitch() const { return (rank + 15) / 16 * 16; }
 };
+// B with rows of ad.rank rounded up to a multiple of 8, zeros behind.
+hipError_t launch_pack_adapters(const Adapters& ad, int cols, void* dst, hipStream_t st);
+__host__ __device__ inline int packed_rank(int rank) { return (rank + 7) / 8 * 8; }
 // Workgroups that share the depth of S.
-int adapter_parts(long rows, long depth);
+int adapter_parts(const Plan& plan, long rows, long depth);
 hipError_t launch_adapter_sums(int type, int rows, int depth, const void* x, long ldx, const Adapters& ad, hipStream_t st);
 
 // out[m][n] = epilogue(sum_k left(m, k) right(n, k)), m < rows, n < cols, k < depth.  An operand

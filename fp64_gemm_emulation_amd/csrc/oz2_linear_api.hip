@@ -43,17 +43,18 @@ oz2::Drop make_drop(const oz2_dropout_t* d) {
 struct FwdWork {
   oz2::Plan plan;
   void *x, *w, *partial;
-  float* s;  // of adapters
+  void *s, *b;  // of adapters
 };
 
-FwdWork carve_fwd(Carver& c, long p, long q, long r, bool pack_x, bool pack_w, int rank = 0) {
+FwdWork carve_fwd(Carver& c, long p, long q, long r, bool pack_x, bool pack_w, long adapters = 0, int rank = 0) {
   FwdWork w{};
-  if (rank > 0) {
+  w.plan = oz2::plan_product(false, p, r, q, false, false);
+  if (adapters > 0 && rank > 0) {
     oz2::Adapters ad{};
     ad.rank = rank;
-    w.s = static_cast<float*>(c.take(sizeof(float) * oz2::adapter_parts(p, q) * p * ad.pitch()));
+    w.s = c.take(sizeof(float) * oz2::adapter_parts(w.plan, p, q) * p * ad.pitch());
+    if (rank % 8 != 0 && !oz2::few_rows(w.plan)) w.b = c.take(2 * adapters * r * oz2::packed_rank(rank));
   }
-  w.plan = oz2::plan_product(false, p, r, q, false, false);
   if (oz2::few_rows(w.plan)) return w;  // takes any rows
   if (pack_x) w.x = c.take(2 * p * oz2::packed_ld(q, 2));
   if (pack_w) w.w = c.take(2 * r * oz2::packed_ld(q, 2));
@@ -155,7 +156,7 @@ int linear(int type, int p, int q, int r, const void* X, int ldx, const void* W,
   }
   const bool pack_x = !oz2::rows_aligned(X, ldx, q, 2), pack_w = !oz2::rows_aligned(W, ldw, q, 2);
   FwdWork ws;
-  int rc = workspace(work, work_bytes, ws, [&](Carver& c) { return carve_fwd(c, p, q, r, pack_x, pack_w, adapted ? adapters->rank : 0); });
+  int rc = workspace(work, work_bytes, ws, [&](Carver& c) { return carve_fwd(c, p, q, r, pack_x, pack_w, adapted ? adapters->count : 0, adapted ? adapters->rank : 0); });
   if (rc != OZ2_OK) return rc;
   const hipStream_t st = static_cast<hipStream_t>(stream);
   const long lp = oz2::packed_ld(q, 2);
@@ -176,11 +177,18 @@ int linear(int type, int p, int q, int r, const void* X, int ldx, const void* W,
   pr.epi.ldy = ldy;
   if (!adapted) return status(oz2::launch_product(pr, st));
   const oz2_adapters_t& a = *adapters;
-  const oz2::Adapters ad{a.count, a.rank, a.A, a.lda, a.stride_a, a.B, a.ldb, a.stride_b, a.index, a.scale, ws.s, oz2::adapter_parts(p, q)};
-  rc = status(oz2::launch_adapter_sums(type, p, q, X, ldx, ad, st));
-  return rc != OZ2_OK ? rc : status(oz2::launch_product_adapters(pr, ad, st));
+  oz2::Adapters ad{a.count, a.rank, a.A, a.lda, a.stride_a, a.B, a.ldb, a.stride_b, a.index, a.scale, ws.s,
+                   oz2::adapter_parts(ws.plan, p, q), false};
+  ad.rounded = ad.parts == 1 && !oz2::few_rows(ws.plan);  // (a product of few rows adds S in f32)
+  if ((rc = status(oz2::launch_adapter_sums(type, p, q, X, ldx, ad, st))) != OZ2_OK) return rc;
+  if (ws.b != nullptr) {
+    if ((rc = status(oz2::launch_pack_adapters(ad, r, ws.b, st))) != OZ2_OK) return rc;
+    ad.b = ws.b;
+    ad.ldb = oz2::packed_rank(a.rank);
+    ad.stride_b = r * ad.ldb;
+  }
+  return status(oz2::launch_product_adapters(pr, ad, st));
 }
-
 
 // linear_i8 on rows X of the outputs' type, or, where their scales are given, of int8.
 int linear_i8(int type, int p, int q, int r, const void* X, int ldx, const float* s, const int8_t* V, int ldv, const float* t,
@@ -368,10 +376,12 @@ size_t ozaki2_linear_workspace_size(int call, int type, int p, int q, int r) {
   return c.used;
 }
 
-size_t ozaki2_linear_adapters_workspace_size(int type, int p, int q, int r, int rank, int aligned) {
-  if ((type != OZ2_BF16 && type != OZ2_F16) || !sizes_ok(p, q, r) || rank < 0 || rank > OZ2_ADAPTER_MAX_RANK) return 0;
+size_t ozaki2_linear_adapters_workspace_size(int type, int p, int q, int r, int count, int rank, int aligned) {
+  if ((type != OZ2_BF16 && type != OZ2_F16) || !sizes_ok(p, q, r) || count < 0 || count > kMaxDim || rank < 0 ||
+      rank > OZ2_ADAPTER_MAX_RANK)
+    return 0;
   Carver c;
-  carve_fwd(c, p, q, r, !aligned, !aligned, p > 0 && r > 0 ? rank : 0);
+  carve_fwd(c, p, q, r, !aligned, !aligned, p > 0 && r > 0 ? count : 0, rank);
   return c.used;
 }
 

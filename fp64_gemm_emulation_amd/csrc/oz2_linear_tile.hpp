@@ -308,73 +308,86 @@ __device__ __forceinline__ void product_tile(char* smem, unsigned wg, int part, 
   // an infinity in one request's adapter stays out of the others' rows.  S is rounded to the operands'
   // type, which is what feeds the matrix cores: half a step, 2^-8 in bf16 and 2^-11 in f16, of this
   // term alone.
-  auto adapters_term = [&]() {
-    static_assert(!ADAPT || (E == 2 && LL == kAlongDepth && RL == kAlongDepth && MB % 4 == 0), "16-bit operands along the depth");
-    const int shares = static_cast<int>(gridDim.y) * S::GROUPS, share = part * S::GROUPS + group;
-    const int pitch = ad->pitch(), rank = ad->rank;
-    const long plane = static_cast<long>(rows) * pitch;
+  int own[ADAPT ? MB / 4 : 1];  // the adapter of row 64 h + lane of the wave's
+  if constexpr (ADAPT) {
 #pragma unroll
     for (int h = 0; h < MB / 4; ++h) {
-      const long base = m0 + wm * (16 * MB) + 64 * h;
-      int own = base + lane < rows ? ad->index[base + lane] : -1;
-      if (own >= ad->count) own = -1;
-      bool first = own >= 0;
-      for (int j = 0; j < 63; ++j) {
-        const int before = __builtin_amdgcn_readlane(own, j);
-        first = first && (j >= lane || before != own);
+      const long m = m0 + wm * (16 * MB) + 64 * h + lane;
+      own[h] = m < rows ? ad->index[m] : -1;
+    }
+  }
+  auto adapters_term = [&]() {
+    static_assert(!ADAPT || (E == 2 && LL == kAlongDepth && RL == kAlongDepth && MB % 4 == 0), "16-bit operands along the depth");
+    constexpr bool kAlone = S::BM == 256;  // one part, one group of waves, S rounded (see adapter_parts)
+    const int shares = static_cast<int>(gridDim.y) * S::GROUPS, share = part * S::GROUPS + group;
+    const int pitch = ad->pitch(), rank = ad->rank;
+    // Places beyond the rank are read inside it and set to zero (rows and columns outside the output are
+    // computed, not stored).
+    auto load_b = [&](const T* b, int nb, int k) {
+      const int col = min(n0 + wn * (16 * NB) + 32 * (nb >> 1) + 4 * (nb & 1) + 8 * (li >> 2) + (li & 3), cols - 1);
+      i32x4 v;
+      __builtin_memcpy(&v, b + col * ad->ldb + (k < rank ? k : 0), 16);
+      return v;
+    };
+    auto load_s = [&](long m, int k) {
+      const long at = min(m, static_cast<long>(rows) - 1) * pitch + (k < pitch ? k : 0);
+      if (kAlone || ad->rounded) return *reinterpret_cast<const i32x4*>(static_cast<const T*>(ad->s) + at);
+      const f32x4* const s = reinterpret_cast<const f32x4*>(static_cast<const float*>(ad->s) + at);
+      const long plane = static_cast<long>(rows) * pitch / 4;
+      f32x4 u = s[0], v = s[1];
+      for (int j = 1; j < ad->parts; ++j) {
+        u += s[j * plane];
+        v += s[j * plane + 1];
       }
-      unsigned long todo = __ballot(first);
+      T t[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t[i] = static_cast<T>(i < 4 ? u[i] : v[i - 4]);
+      i32x4 r;
+      __builtin_memcpy(&r, t, 16);
+      return r;
+    };
+#pragma unroll
+    for (int h = 0; h < MB / 4; ++h) {
+      const long base = m0 + wm * (16 * MB) + 64 * h + li;
+      unsigned long todo = __ballot(own[h] >= 0 && own[h] < ad->count);
       for (int n = 0; todo != 0; ++n) {
-        const int token = __builtin_ctzl(todo);
-        todo &= todo - 1;
-        if (n % shares != share) continue;
-        const int adapter = __builtin_amdgcn_readlane(own, token);
-        const unsigned long match = __ballot(own == adapter);
+        const int adapter = __builtin_amdgcn_readlane(own[h], __builtin_ctzl(todo));
+        const unsigned long match = __ballot(own[h] == adapter);
+        todo &= ~match;
+        if (!kAlone && n % shares != share) continue;
         const T* const b = static_cast<const T*>(ad->b) + adapter * ad->stride_b;
         for (int k0 = 0; k0 < rank; k0 += 64) {
-          i32x4 bf[NB][2];
+          const int k = k0 + 8 * lg;
+          i32x4 bf[NB][2], sf[4][2];
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
-            const int col = n0 + wn * (16 * NB) + 32 * (nb >> 1) + 4 * (nb & 1) + 8 * (li >> 2) + (li & 3);
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              const int k = k0 + 32 * half + 8 * lg;
-              bf[nb][half] = i32x4{0, 0, 0, 0};
-              if (col < cols && k < rank) {
-                const raw8 r = load_raw8<T, false>(b, col * ad->ldb + k, rank - k);
-                __builtin_memcpy(&bf[nb][half], &r, 16);
-              }
-            }
+            bf[nb][0] = load_b(b, nb, k);
+            bf[nb][1] = load_b(b, nb, k + 32);
           }
 #pragma unroll
           for (int mb = 0; mb < 4; ++mb) {
-            if ((match >> (16 * mb) & 0xFFFF) == 0) continue;
+            sf[mb][0] = load_s(base + 16 * mb, k);
+            sf[mb][1] = load_s(base + 16 * mb, k + 32);
+          }
+          OZ2_SCHED_FENCE();
+          const i32x4 zero = {0, 0, 0, 0};
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            bf[nb][0] = k < rank ? bf[nb][0] : zero;
+            bf[nb][1] = k + 32 < rank ? bf[nb][1] : zero;
+          }
+#pragma unroll
+          for (int mb = 0; mb < 4; ++mb) {
+            sf[mb][0] = k < pitch ? sf[mb][0] : zero;
+            sf[mb][1] = k + 32 < pitch ? sf[mb][1] : zero;
             const bool mine = match >> (16 * mb + li) & 1;
-            i32x4 sf[2];
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              const int k = k0 + 32 * half + 8 * lg;
-              float v[8] = {};
-              if (mine && k < pitch) {
-                const float* const s = ad->s + (base + 16 * mb + li) * pitch + k;
-                for (int j = 0; j < ad->parts; ++j) {
-                  float x[8];
-                  load8(s + j * plane, 8, x);
-#pragma unroll
-                  for (int u = 0; u < 8; ++u) v[u] += x[u];
-                }
-              }
-              T t[8];
-#pragma unroll
-              for (int u = 0; u < 8; ++u) t[u] = static_cast<T>(v[u]);
-              __builtin_memcpy(&sf[half], t, 16);
-            }
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
-              Acc t = M::mma(bf[nb][0], sf[0], Acc{0, 0, 0, 0});
-              if (k0 + 32 < rank) t = M::mma(bf[nb][1], sf[1], t);
-              if (mine) acc[4 * h + mb][nb] += t;
+              const Acc t = M::mma(bf[nb][1], sf[mb][1], M::mma(bf[nb][0], sf[mb][0], Acc{0, 0, 0, 0}));
+#pragma unroll
+              for (int v = 0; v < 4; ++v) acc[4 * h + mb][nb][v] = mine ? acc[4 * h + mb][nb][v] + t[v] : acc[4 * h + mb][nb][v];
             }
+            OZ2_SCHED_FENCE();
           }
         }
       }
@@ -463,7 +476,12 @@ __device__ __forceinline__ void product_tile(char* smem, unsigned wg, int part, 
 #pragma unroll
       for (int j = 0; j < COPIES; ++j) copy1(kt, j);
     }
-    if constexpr (ADAPT) adapters_term();
+    if constexpr (ADAPT) {
+      // The condition holds whenever this kernel runs.  It is called unlikely so that the compiler, which
+      // takes nested loops for the hot part, does not spill in the loop over the depth, where a reload
+      // waits for the copies under way, or between the epilogue's stores, where it waits for them.
+      if (__builtin_expect_with_probability(ad->rank > 0, 0, 1.0)) adapters_term();
+    }
     wait_copies(0, S::RING - 1);
     OZ2_SCHED_FENCE();
     __builtin_amdgcn_s_barrier();
@@ -921,7 +939,7 @@ __device__ __forceinline__ void product_few(int rows, int cols, int depth, int p
       if (brow != nullptr && 8 * c < ad->rank) held_b[c] = load_raw8<T, false>(brow, 8 * c, ad->rank - 8 * c);
     const int count = rows * ad->pitch();
     if (static_cast<int>(threadIdx.x) < count)
-      for (int j = 0; j < ad->parts; ++j) held_s += ad->s[static_cast<long>(j) * count + threadIdx.x];
+      for (int j = 0; j < ad->parts; ++j) held_s += static_cast<const float*>(ad->s)[static_cast<long>(j) * count + threadIdx.x];
   }
 
   extern __shared__ __attribute__((aligned(16))) int8_t levels[];  // QUANT: rows of `pitch` bytes; ADAPT: S
@@ -1019,7 +1037,7 @@ __device__ __forceinline__ void product_few(int rows, int cols, int depth, int p
     if (static_cast<int>(threadIdx.x) < count) s[threadIdx.x] = held_s;
     for (int i = threadIdx.x + blockDim.x; i < count; i += blockDim.x) {
       float v = 0.0f;
-      for (int j = 0; j < ad->parts; ++j) v += ad->s[static_cast<long>(j) * count + i];
+      for (int j = 0; j < ad->parts; ++j) v += static_cast<const float*>(ad->s)[static_cast<long>(j) * count + i];
       s[i] = v;  // (of a row without an adapter something that is not used)
     }
   }

@@ -371,12 +371,13 @@ typedef struct oz2_adapters {
  * summed in f32; on products of more than a few rows it is rounded to `type` before it meets B_a, as
  * the matrix cores' operands are.  An adapter reaches its own rows only, whatever it holds.
  * work / work_bytes: ozaki2_linear_adapters_workspace_size bytes, `aligned` 0 or, where rows are as
- * OZ2_LINEAR_ALIGNED says, 1.
+ * OZ2_LINEAR_ALIGNED says, 1.  (On products of more than a few rows a rank that is no multiple of 8 has
+ * every B copied into it.)
  */
 int ozaki2_linear_adapters(int type, int p, int q, int r, const void* X, int ldx, const void* W, int ldw, const void* bias,
                            int act, const oz2_adapters_t* adapters, const void* R, int ldr, void* Y, int ldy, void* work,
                            size_t work_bytes, void* stream);
-size_t ozaki2_linear_adapters_workspace_size(int type, int p, int q, int r, int rank, int aligned);
+size_t ozaki2_linear_adapters_workspace_size(int type, int p, int q, int r, int count, int rank, int aligned);
 
 /* ------------------------------------------------------------------------------------------
  * Root-mean-square norm, before the products of a layer.  Conventions as for the linear layers;

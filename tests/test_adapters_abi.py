@@ -41,11 +41,14 @@ def test_other_statuses():
     assert call(p=0) == oz.OZ2_OK and call(r=0, ldr=1, ldy=1) == oz.OZ2_OK
     assert call(work=0x100, work_bytes=64) == oz.OZ2_ERR_WORKSPACE
     size = oz.ozaki2_linear_adapters_workspace_size
-    assert size(oz.OZ2_F32, 8, 16, 24, 4, 0) == 0 and size(oz.OZ2_F16, 8, 16, 24, 257, 0) == 0 and size(oz.OZ2_F16, 8, 16, 24, -1, 0) == 0
+    assert size(oz.OZ2_F32, 8, 16, 24, 3, 4, 0) == 0 and size(oz.OZ2_F16, 8, 16, 24, 3, 257, 0) == 0
+    assert size(oz.OZ2_F16, 8, 16, 24, 3, -1, 0) == 0 and size(oz.OZ2_F16, 8, 16, 24, -1, 4, 0) == 0
     for p, q, r in ((1, 2048, 8192), (37, 8192, 2048), (8192, 2048, 8192), (777, 1999, 4099)):
         base = oz.ozaki2_linear_workspace_size(oz.OZ2_LINEAR_FWD, oz.OZ2_F16, p, q, r)
-        assert size(oz.OZ2_F16, p, q, r, 0, 0) == base
-        assert base + 4 * p * 64 <= size(oz.OZ2_F16, p, q, r, 50, 0) <= base + 16 * 4 * p * 64 + 256
+        assert size(oz.OZ2_F16, p, q, r, 3, 0, 0) == base and size(oz.OZ2_F16, p, q, r, 0, 50, 0) == base
+        assert base + 4 * p * 64 <= size(oz.OZ2_F16, p, q, r, 3, 56, 0) <= base + 16 * 4 * p * 64 + 256
+        packed = 2 * 3 * r * 56 if p > 16 else 0
+        assert size(oz.OZ2_F16, p, q, r, 3, 50, 0) >= size(oz.OZ2_F16, p, q, r, 3, 56, 0) + packed
 
 
 SIZES = dict(x=(4, 16), w=(8, 16), a=(3, 2, 16), b=(3, 8, 2), scale=(3,), bias=(8,), residual=(4, 8), out=(4, 8))
