@@ -113,11 +113,10 @@ __global__ __launch_bounds__(64 * WAVES) void adapter_sums_kernel(int rows, int 
 
 constexpr int kSmallGroups = 256;  // rows up to which a workgroup takes 16 tokens, not 64
 
-// Parts of the depth for few rows (the product adds them up): where a wave's piece would be longer than
-// what it has under way.
+// Parts of the depth where a product of few rows adds them up: so many that a wave's piece is not longer
+// than what it has under way.
 int adapter_parts(const Plan& plan, long rows, long depth) {
-  if (plan.tile == kTile256) return 1;
-  return static_cast<int>(std::max(1L, std::min({depth / 1024, 256 / std::max(rows, 1L), 16L})));
+  return few_rows(plan) ? static_cast<int>(std::max(1L, std::min({depth / 1024, 256 / std::max(rows, 1L), 16L}))) : 1;
 }
 
 template <typename M, typename T>

@@ -81,7 +81,7 @@ struct Adapters {
   const float* scale;  // null: ones
   // S, pitch() elements to a row; rows without an adapter are not written.  For a product of few rows
   // as `parts` sums over parts of the depth, [part][row][pitch] in f32, for the others rounded to the
-  // operands' type where that is one part.
+  // operands' type.
   void* s;
   int parts;
   bool rounded;

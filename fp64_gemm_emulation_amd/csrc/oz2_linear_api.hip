@@ -179,7 +179,7 @@ int linear(int type, int p, int q, int r, const void* X, int ldx, const void* W,
   const oz2_adapters_t& a = *adapters;
   oz2::Adapters ad{a.count, a.rank, a.A, a.lda, a.stride_a, a.B, a.ldb, a.stride_b, a.index, a.scale, ws.s,
                    oz2::adapter_parts(ws.plan, p, q), false};
-  ad.rounded = ad.parts == 1 && !oz2::few_rows(ws.plan);  // (a product of few rows adds S in f32)
+  ad.rounded = !oz2::few_rows(ws.plan);
   if ((rc = status(oz2::launch_adapter_sums(type, p, q, X, ldx, ad, st))) != OZ2_OK) return rc;
   if (ws.b != nullptr) {
     if ((rc = status(oz2::launch_pack_adapters(ad, r, ws.b, st))) != OZ2_OK) return rc;

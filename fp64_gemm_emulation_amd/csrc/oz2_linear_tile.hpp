@@ -308,68 +308,81 @@ __device__ __forceinline__ void product_tile(char* smem, unsigned wg, int part, 
   // an infinity in one request's adapter stays out of the others' rows.  S is rounded to the operands'
   // type, which is what feeds the matrix cores: half a step, 2^-8 in bf16 and 2^-11 in f16, of this
   // term alone.
+  // Order matters: loads return in order, and the first stages' copies keep a tile's start busy.  The
+  // rows' adapters and S (which no adapter's number is needed for) are asked for before the copies,
+  // the first adapter's B behind the first stage's.
+  typedef i32x4 Frags[4][2];
   int own[ADAPT ? MB / 4 : 1];  // the adapter of row 64 h + lane of the wave's
-  if constexpr (ADAPT) {
+  Frags sf;                     // S of four blocks, 64 elements of rank
+  i32x4 bf[NB][2];              // B of `held`
+  int held = -1;
+  const int shares = static_cast<int>(gridDim.y) * S::GROUPS, share = part * S::GROUPS + group;
+  constexpr bool kAlone = S::BM == 256;  // one part, one group of waves
+  // (places beyond the rank are read inside it and set to zero; rows and columns outside the output are
+  // computed, not stored)
+  auto load_b = [&](int adapter, int k0) {
+    const T* const b = static_cast<const T*>(ad->b) + adapter * ad->stride_b;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      const int col = min(n0 + wn * (16 * NB) + 32 * (nb >> 1) + 4 * (nb & 1) + 8 * (li >> 2) + (li & 3), cols - 1);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int k = k0 + 32 * half + 8 * lg;
+        __builtin_memcpy(&bf[nb][half], b + col * ad->ldb + (k < ad->rank ? k : 0), 16);
+      }
+    }
+    held = adapter;
+  };
+  auto load_s = [&](int h, int k0) {
+#pragma unroll
+    for (int mb = 0; mb < 4; ++mb)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int k = k0 + 32 * half + 8 * lg, pitch = ad->pitch();
+        const long m = min(m0 + wm * (16 * MB) + 64 * h + 16 * mb + li, static_cast<long>(rows) - 1);
+        sf[mb][half] = *reinterpret_cast<const i32x4*>(static_cast<const T*>(ad->s) + m * pitch + (k < pitch ? k : 0));
+      }
+  };
+  // the next adapter among `todo` that this part and group of waves has (todo: without those up to it)
+  auto next_adapter = [&](int h, unsigned long& todo, int& n, unsigned long& match) {
+    while (todo != 0) {
+      const int adapter = __builtin_amdgcn_readlane(own[h], __builtin_ctzl(todo));
+      match = __ballot(own[h] == adapter);
+      todo &= ~match;
+      if (kAlone || n++ % shares == share) return adapter;
+    }
+    return -1;
+  };
+  auto adapters_early = [&]() {
 #pragma unroll
     for (int h = 0; h < MB / 4; ++h) {
       const long m = m0 + wm * (16 * MB) + 64 * h + lane;
       own[h] = m < rows ? ad->index[m] : -1;
     }
-  }
+    load_s(0, 0);
+  };
+  auto adapters_first = [&]() {
+    unsigned long todo = __ballot(own[0] >= 0 && own[0] < ad->count), match;
+    int n = 0;
+    const int adapter = next_adapter(0, todo, n, match);
+    if (adapter >= 0) load_b(adapter, 0);
+  };
   auto adapters_term = [&]() {
     static_assert(!ADAPT || (E == 2 && LL == kAlongDepth && RL == kAlongDepth && MB % 4 == 0), "16-bit operands along the depth");
-    constexpr bool kAlone = S::BM == 256;  // one part, one group of waves, S rounded (see adapter_parts)
-    const int shares = static_cast<int>(gridDim.y) * S::GROUPS, share = part * S::GROUPS + group;
     const int pitch = ad->pitch(), rank = ad->rank;
-    // Places beyond the rank are read inside it and set to zero (rows and columns outside the output are
-    // computed, not stored).
-    auto load_b = [&](const T* b, int nb, int k) {
-      const int col = min(n0 + wn * (16 * NB) + 32 * (nb >> 1) + 4 * (nb & 1) + 8 * (li >> 2) + (li & 3), cols - 1);
-      i32x4 v;
-      __builtin_memcpy(&v, b + col * ad->ldb + (k < rank ? k : 0), 16);
-      return v;
-    };
-    auto load_s = [&](long m, int k) {
-      const long at = min(m, static_cast<long>(rows) - 1) * pitch + (k < pitch ? k : 0);
-      if (kAlone || ad->rounded) return *reinterpret_cast<const i32x4*>(static_cast<const T*>(ad->s) + at);
-      const f32x4* const s = reinterpret_cast<const f32x4*>(static_cast<const float*>(ad->s) + at);
-      const long plane = static_cast<long>(rows) * pitch / 4;
-      f32x4 u = s[0], v = s[1];
-      for (int j = 1; j < ad->parts; ++j) {
-        u += s[j * plane];
-        v += s[j * plane + 1];
-      }
-      T t[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) t[i] = static_cast<T>(i < 4 ? u[i] : v[i - 4]);
-      i32x4 r;
-      __builtin_memcpy(&r, t, 16);
-      return r;
-    };
 #pragma unroll
     for (int h = 0; h < MB / 4; ++h) {
-      const long base = m0 + wm * (16 * MB) + 64 * h + li;
-      unsigned long todo = __ballot(own[h] >= 0 && own[h] < ad->count);
-      for (int n = 0; todo != 0; ++n) {
-        const int adapter = __builtin_amdgcn_readlane(own[h], __builtin_ctzl(todo));
-        const unsigned long match = __ballot(own[h] == adapter);
-        todo &= ~match;
-        if (!kAlone && n % shares != share) continue;
-        const T* const b = static_cast<const T*>(ad->b) + adapter * ad->stride_b;
+      unsigned long todo = __ballot(own[h] >= 0 && own[h] < ad->count), match;
+      for (int n = 0;;) {
+        const int adapter = next_adapter(h, todo, n, match);
+        if (adapter < 0) break;
         for (int k0 = 0; k0 < rank; k0 += 64) {
-          const int k = k0 + 8 * lg;
-          i32x4 bf[NB][2], sf[4][2];
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb) {
-            bf[nb][0] = load_b(b, nb, k);
-            bf[nb][1] = load_b(b, nb, k + 32);
-          }
-#pragma unroll
-          for (int mb = 0; mb < 4; ++mb) {
-            sf[mb][0] = load_s(base + 16 * mb, k);
-            sf[mb][1] = load_s(base + 16 * mb, k + 32);
+          if (h > 0 || held != adapter || rank > 64) {  // (kept over the groups of rows they are spilled)
+            load_b(adapter, k0);
+            load_s(h, k0);
           }
           OZ2_SCHED_FENCE();
+          const int k = k0 + 8 * lg;
           const i32x4 zero = {0, 0, 0, 0};
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
@@ -469,12 +482,16 @@ __device__ __forceinline__ void product_tile(char* smem, unsigned wg, int part, 
   if (nk > 0) {
     const bool partial = last_depth < kDepth;
     set_offsets(kDepth);
+    if constexpr (ADAPT) adapters_early();
 #pragma unroll
     for (int kt = 0; kt < S::RING; ++kt) {
       if (kt >= nk) break;
       if (kt == nk - 1) set_offsets(last_depth);
 #pragma unroll
       for (int j = 0; j < COPIES; ++j) copy1(kt, j);
+      if constexpr (ADAPT) {
+        if (kt == 0) adapters_first();
+      }
     }
     if constexpr (ADAPT) {
       // The condition holds whenever this kernel runs.  It is called unlikely so that the compiler, which
