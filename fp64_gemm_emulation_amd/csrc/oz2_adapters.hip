@@ -111,50 +111,76 @@ __global__ __launch_bounds__(64 * WAVES) void adapter_sums_kernel(int rows, int 
   }
 }
 
-constexpr int kSmallGroups = 256;  // rows up to which a workgroup takes 16 tokens, not 64
+constexpr int kFewTokens = 256;  // rows up to which a workgroup takes 16 tokens and a part of the depth
 
-// Parts of the depth where a product of few rows adds them up: so many that a wave's piece is not longer
-// than what it has under way.
-int adapter_parts(const Plan& plan, long rows, long depth) {
-  return few_rows(plan) ? static_cast<int>(std::max(1L, std::min({depth / 1024, 256 / std::max(rows, 1L), 16L}))) : 1;
+// A CU draws some 40 GB/s from memory, so few rows are spread over the CUs by parts of the depth (37 rows
+// with 32 adapters of rank 32 at depth 8192: 24 us in one part, 8.6 in 4, 7.0 in 16).  Many have
+// workgroups enough; dividing those made them no faster (8192 rows, rank 64, depth 2048: 19.6 us in one
+// part and in two, 25 in four).
+int adapter_parts(long rows, long depth) {
+  return rows <= kFewTokens ? static_cast<int>(std::max(1L, std::min({depth / 512, 1024 / std::max(rows, 1L), 16L}))) : 1;
 }
 
 template <typename M, typename T>
 static hipError_t adapter_sums(int rows, int depth, const void* x, long ldx, const Adapters& ad, hipStream_t st) {
   const int per = ((depth + ad.parts - 1) / ad.parts + 31) / 32 * 32;
-  auto launch = [&](auto rb, auto tb, auto waves, auto deep) {
-    constexpr int RB = decltype(rb)::value, TB = decltype(tb)::value, WAVES = decltype(waves)::value, DEEP = decltype(deep)::value;
+  auto launch = [&](auto rb, auto tb, auto deep) {
+    constexpr int RB = decltype(rb)::value, TB = decltype(tb)::value, DEEP = decltype(deep)::value, kWaves = 4;
     const int groups = (rows + 16 * TB - 1) / (16 * TB);
     // workgroups that find no adapter left to them end at once
     const dim3 grid(groups, std::min({rows, 16 * TB, std::max(2, 1024 / groups)}), ad.parts);
-    hipLaunchKernelGGL((adapter_sums_kernel<M, T, RB, TB, WAVES, DEEP>), grid, dim3(64 * WAVES), 0, st, rows, depth, per,
+    hipLaunchKernelGGL((adapter_sums_kernel<M, T, RB, TB, kWaves, DEEP>), grid, dim3(64 * kWaves), 0, st, rows, depth, per,
                        static_cast<const T*>(x), ldx, ad);
   };
   using std::integral_constant;
-  if (rows <= kSmallGroups) {
-    constexpr integral_constant<int, 1> tb;
-    constexpr integral_constant<int, 16> waves;
+  auto ranks = [&](auto tb, auto deep) {
     if (ad.rank <= 16)
-      launch(integral_constant<int, 1>{}, tb, waves, integral_constant<int, 8>{});
+      launch(integral_constant<int, 1>{}, tb, integral_constant<int, 2 * decltype(deep)::value>{});
     else if (ad.rank <= 32)
-      launch(integral_constant<int, 2>{}, tb, waves, integral_constant<int, 8>{});
+      launch(integral_constant<int, 2>{}, tb, deep);
     else
-      launch(integral_constant<int, 4>{}, tb, waves, integral_constant<int, 4>{});
-  } else {
-    constexpr integral_constant<int, 4> tb;
-    constexpr integral_constant<int, 8> waves;
-    if (ad.rank <= 16)
-      launch(integral_constant<int, 1>{}, tb, waves, integral_constant<int, 4>{});
-    else if (ad.rank <= 32)
-      launch(integral_constant<int, 2>{}, tb, waves, integral_constant<int, 4>{});
-    else
-      launch(integral_constant<int, 4>{}, tb, waves, integral_constant<int, 4>{});
-  }
+      launch(integral_constant<int, 4>{}, tb, integral_constant<int, decltype(deep)::value / 2>{});
+  };
+  if (rows <= kFewTokens)
+    ranks(integral_constant<int, 1>{}, integral_constant<int, 8>{});
+  else
+    ranks(integral_constant<int, 4>{}, integral_constant<int, 4>{});
   return hipGetLastError();
 }
 
 hipError_t launch_adapter_sums(int type, int rows, int depth, const void* x, long ldx, const Adapters& ad, hipStream_t st) {
   return type == kTypeBf16 ? adapter_sums<MmaBf16, bf16>(rows, depth, x, ldx, ad, st) : adapter_sums<MmaF16, f16>(rows, depth, x, ldx, ad, st);
+}
+
+// Adds up the parts of S, rounded: four elements per thread, four parts' loads at a time.
+template <typename T>
+__global__ __launch_bounds__(64) void join_adapter_sums_kernel(long n, int parts, const f32x4* __restrict__ s, T* __restrict__ out) {
+  const long at = static_cast<long>(blockIdx.x) * 64 + threadIdx.x;
+  if (at >= n) return;
+  f32x4 sum = {};
+  for (int j = 0; j < parts; j += 4) {
+    f32x4 v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) v[u] = s[min(j + u, parts - 1) * n + at];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (j + u < parts) sum += v[u];
+  }
+  T t[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) t[i] = static_cast<T>(sum[i]);
+  __builtin_memcpy(out + 4 * at, t, sizeof(t));
+}
+
+hipError_t launch_join_adapter_sums(int type, int rows, const Adapters& ad, void* out, hipStream_t st) {
+  const long n = static_cast<long>(rows) * ad.pitch() / 4;
+  const dim3 grid(static_cast<unsigned>((n + 63) / 64));
+  const f32x4* const s = static_cast<const f32x4*>(ad.s);
+  if (type == kTypeBf16)
+    hipLaunchKernelGGL(join_adapter_sums_kernel<bf16>, grid, dim3(64), 0, st, n, ad.parts, s, static_cast<bf16*>(out));
+  else
+    hipLaunchKernelGGL(join_adapter_sums_kernel<f16>, grid, dim3(64), 0, st, n, ad.parts, s, static_cast<f16*>(out));
+  return hipGetLastError();
 }
 
 // A thread per 16 bytes; blockIdx.y the adapter.

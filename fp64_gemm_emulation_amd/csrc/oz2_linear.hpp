@@ -92,7 +92,9 @@ struct Adapters {
 hipError_t launch_pack_adapters(const Adapters& ad, int cols, void* dst, hipStream_t st);
 __host__ __device__ inline int packed_rank(int rank) { return (rank + 7) / 8 * 8; }
 // Workgroups that share the depth of S.
-int adapter_parts(const Plan& plan, long rows, long depth);
+int adapter_parts(long rows, long depth);
+// The sum of ad's parts of S, rounded to the type.
+hipError_t launch_join_adapter_sums(int type, int rows, const Adapters& ad, void* out, hipStream_t st);
 hipError_t launch_adapter_sums(int type, int rows, int depth, const void* x, long ldx, const Adapters& ad, hipStream_t st);
 
 // out[m][n] = epilogue(sum_k left(m, k) right(n, k)), m < rows, n < cols, k < depth.  An operand

@@ -343,15 +343,9 @@ __device__ __forceinline__ void product_tile(char* smem, unsigned wg, int part, 
         sf[mb][half] = *reinterpret_cast<const i32x4*>(static_cast<const T*>(ad->s) + m * pitch + (k < pitch ? k : 0));
       }
   };
-  // the next adapter among `todo` that this part and group of waves has (todo: without those up to it)
-  auto next_adapter = [&](int h, unsigned long& todo, int& n, unsigned long& match) {
-    while (todo != 0) {
-      const int adapter = __builtin_amdgcn_readlane(own[h], __builtin_ctzl(todo));
-      match = __ballot(own[h] == adapter);
-      todo &= ~match;
-      if (kAlone || n++ % shares == share) return adapter;
-    }
-    return -1;
+  // rows of group h whose adapter is this part's and group of waves's to add
+  auto shared_rows = [&](int h) {
+    return __ballot(own[h] >= 0 && own[h] < ad->count && (kAlone || own[h] % shares == share));
   };
   auto adapters_early = [&]() {
 #pragma unroll
@@ -362,20 +356,18 @@ __device__ __forceinline__ void product_tile(char* smem, unsigned wg, int part, 
     load_s(0, 0);
   };
   auto adapters_first = [&]() {
-    unsigned long todo = __ballot(own[0] >= 0 && own[0] < ad->count), match;
-    int n = 0;
-    const int adapter = next_adapter(0, todo, n, match);
-    if (adapter >= 0) load_b(adapter, 0);
+    const unsigned long todo = shared_rows(0);
+    if (todo != 0) load_b(__builtin_amdgcn_readlane(own[0], __builtin_ctzl(todo)), 0);
   };
   auto adapters_term = [&]() {
     static_assert(!ADAPT || (E == 2 && LL == kAlongDepth && RL == kAlongDepth && MB % 4 == 0), "16-bit operands along the depth");
     const int pitch = ad->pitch(), rank = ad->rank;
 #pragma unroll
     for (int h = 0; h < MB / 4; ++h) {
-      unsigned long todo = __ballot(own[h] >= 0 && own[h] < ad->count), match;
-      for (int n = 0;;) {
-        const int adapter = next_adapter(h, todo, n, match);
-        if (adapter < 0) break;
+      for (unsigned long todo = shared_rows(h); todo != 0;) {
+        const int adapter = __builtin_amdgcn_readlane(own[h], __builtin_ctzl(todo));
+        const unsigned long match = __ballot(own[h] == adapter);
+        todo &= ~match;
         for (int k0 = 0; k0 < rank; k0 += 64) {
           if (h > 0 || held != adapter || rank > 64) {  // (kept over the groups of rows they are spilled)
             load_b(adapter, k0);
@@ -910,6 +902,21 @@ __device__ __forceinline__ i32x4 load_chunk(const E* row, int k, int depth) {
 
 constexpr int kFewWaves = 8;
 
+// Element i of S, `count` elements to a part, the parts' loads four at a time (of a row without an
+// adapter something that is not used).
+__device__ __forceinline__ float adapter_sum(const Adapters& ad, int count, int i) {
+  const float* const s = static_cast<const float*>(ad.s) + i;
+  float sum = 0.0f;
+  for (int j = 0; j < ad.parts; j += 4) {
+    float v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) v[u] = s[static_cast<long>(min(j + u, ad.parts - 1)) * count];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) sum += j + u < ad.parts ? v[u] : 0.0f;
+  }
+  return sum;
+}
+
 // ADAPT: the adapters' term, S and B read behind the first loads of weights: a thread per output adds
 // up its row of B with its token's S, which goes through LDS.
 template <typename M, typename T, int R, bool QUANT, int ACT, bool FULL, bool ADAPT = false>
@@ -955,8 +962,7 @@ __device__ __forceinline__ void product_few(int rows, int cols, int depth, int p
     for (int c = 0; c < kHeldRank / 8; ++c)
       if (brow != nullptr && 8 * c < ad->rank) held_b[c] = load_raw8<T, false>(brow, 8 * c, ad->rank - 8 * c);
     const int count = rows * ad->pitch();
-    if (static_cast<int>(threadIdx.x) < count)
-      for (int j = 0; j < ad->parts; ++j) held_s += static_cast<const float*>(ad->s)[static_cast<long>(j) * count + threadIdx.x];
+    if (static_cast<int>(threadIdx.x) < count) held_s = adapter_sum(*ad, count, threadIdx.x);
   }
 
   extern __shared__ __attribute__((aligned(16))) int8_t levels[];  // QUANT: rows of `pitch` bytes; ADAPT: S
@@ -1052,11 +1058,7 @@ __device__ __forceinline__ void product_few(int rows, int cols, int depth, int p
     float* const s = reinterpret_cast<float*>(levels);
     const int count = rows * ad->pitch();
     if (static_cast<int>(threadIdx.x) < count) s[threadIdx.x] = held_s;
-    for (int i = threadIdx.x + blockDim.x; i < count; i += blockDim.x) {
-      float v = 0.0f;
-      for (int j = 0; j < ad->parts; ++j) v += static_cast<const float*>(ad->s)[static_cast<long>(j) * count + i];
-      s[i] = v;  // (of a row without an adapter something that is not used)
-    }
+    for (int i = threadIdx.x + blockDim.x; i < count; i += blockDim.x) s[i] = adapter_sum(*ad, count, i);
   }
   __syncthreads();
   for (int i = threadIdx.x; i < R * R; i += blockDim.x) {
