@@ -754,9 +754,11 @@ def linear_adapters(x, w, a, b, index, scale=None, bias=None, activation: str = 
     n, k = a.shape[:2]
     if index is None:
         raise ValueError("index, the adapter of each row, is needed")
-    if _grad_enabled() and any(t is not None and t.requires_grad for t in (x, w, a, b, scale, bias, residual, out)):
+    if _grad_enabled() and (x.requires_grad or w.requires_grad or a.requires_grad or b.requires_grad
+                            or (scale is not None and scale.requires_grad) or (bias is not None and bias.requires_grad)
+                            or (residual is not None and residual.requires_grad) or (out is not None and out.requires_grad)):
         raise ValueError("linear_adapters is not differentiated by autograd: call it under torch.no_grad() (or on detached tensors)")
-    dtype, dev, device = x.dtype, x.get_device(), x.device
+    dtype, dev = x.dtype, x.get_device()
     with _entered(dev, stream) as on:
         px, ldx = _rows(x, "x", shape, dtype, dev)
         pw, ldw = _rows(w, "w", (r, q), dtype, dev)
@@ -769,7 +771,7 @@ def linear_adapters(x, w, a, b, index, scale=None, bias=None, activation: str = 
         py, ldy = _rows(y, "out", (p, r), dtype, dev) if out is not None else (y.data_ptr(), r or 1)
         aligned = 1 if _aligned(2 * q, (px, 2 * ldx), (pw, 2 * ldw)) else 0
         nwork = _LIB.ozaki2_linear_adapters_workspace_size(kind, p, q, r, n, k, aligned)
-        work = torch.empty(nwork, dtype=torch.uint8, device=device) if nwork else None
+        work = x.new_empty((nwork,), dtype=torch.uint8) if nwork else None
         adapters = OZ2Adapters(n, k, pa, lda, stride_a, pb, ldb, stride_b, pi, ps)
         rc = _LIB.ozaki2_linear_adapters(kind, p, q, r, px, ldx, pw, ldw, pbias, act, ctypes.addressof(adapters), pr, ldr, py, ldy,
                                          work.data_ptr() if nwork else None, nwork, _raw_stream(dev))
@@ -789,7 +791,9 @@ def _norm_operands(name, x, weight, residual, hidden, out):
     kind = _kind(x, "x", f32=True)
     if hidden is not None and residual is None:
         raise ValueError("hidden is the sum with residual, which is not given")
-    if _grad_enabled() and any(t is not None and t.requires_grad for t in (x, weight, residual, hidden, out)):
+    if _grad_enabled() and (x.requires_grad or (weight is not None and weight.requires_grad)
+                            or (residual is not None and residual.requires_grad)
+                            or (hidden is not None and hidden.requires_grad) or (out is not None and out.requires_grad)):
         raise ValueError(f"{name} is not differentiated by autograd: call it under torch.no_grad() (or on detached tensors) "
                          "and take its gradients with rms_norm_backward")
     return shape, kind
@@ -828,13 +832,12 @@ def rms_norm_i8(x, weight=None, residual=None, eps: float = 1e-6, hidden=None, s
     No autograd, as linear."""
     torch = _torch or _use_torch()
     shape, kind = _norm_operands("rms_norm_i8", x, weight, residual, hidden, None)
-    (p, q), dtype, dev, device = shape, x.dtype, x.get_device(), x.device
+    (p, q), dtype, dev = shape, x.dtype, x.get_device()
     with _entered(dev, stream) as on:
         px, ldx = _rows(x, "x", shape, dtype, dev)
         pr, ldr = _rows(residual, "residual", shape, dtype, dev)
         pw = _vector(weight, "weight", q, dtype, dev)
-        levels = torch.empty((p, q), dtype=torch.int8, device=device)
-        scale = torch.empty((p,), dtype=torch.float32, device=device)
+        levels, scale = x.new_empty(shape, dtype=torch.int8), x.new_empty((p,), dtype=torch.float32)
         h = hidden if hidden is not None or residual is None else x.new_empty(shape)
         ph, ldh = _rows(h, "hidden", shape, dtype, dev)
         rc = _LIB.ozaki2_rms_norm_i8(kind, p, q, px, ldx, pr, ldr, pw, eps, ph, ldh, levels.data_ptr(), q or 1,
@@ -858,16 +861,16 @@ def rms_norm_backward(dy, h, weight=None, dh=None, eps: float = 1e-6, needs=("x"
     unknown = set(needs) - {"x", "weight"}
     if unknown:
         raise ValueError(f"needs names {sorted(unknown)}: only x and weight have gradients here")
-    dtype, dev, device = dy.dtype, dy.get_device(), dy.device
+    dtype, dev = dy.dtype, dy.get_device()
     with _entered(dev, stream) as on:
         pdy, lddy = _rows(dy, "dy", shape, dtype, dev)
         ph, ldh = _rows(h, "h", shape, dtype, dev)
         pw = _vector(weight, "weight", q, dtype, dev)
         pdh, lddh = _rows(dh, "dh", shape, dtype, dev)
-        dx = torch.empty((p, q), dtype=dtype, device=device) if "x" in needs else None
-        dw = torch.empty((q,), dtype=dtype, device=device) if "weight" in needs else None
+        dx = dy.new_empty(shape) if "x" in needs else None
+        dw = dy.new_empty((q,)) if "weight" in needs else None
         n = _LIB.ozaki2_rms_norm_bwd_workspace_size(kind, p, q) if dw is not None else 0
-        work = torch.empty(n, dtype=torch.uint8, device=device) if n else None
+        work = dy.new_empty((n,), dtype=torch.uint8) if n else None
         rc = _LIB.ozaki2_rms_norm_bwd(kind, p, q, pdy, lddy, ph, ldh, pw, eps, pdh, lddh,
                                       dx.data_ptr() if dx is not None else None, q or 1,
                                       dw.data_ptr() if dw is not None else None, work.data_ptr() if n else None, n,
@@ -903,19 +906,19 @@ def token_logprobs(logits, tokens=None, top: int = 0, entropy: bool = False, str
     if _grad_enabled() and logits.requires_grad:
         raise ValueError("token_logprobs is not differentiated by autograd: call it under torch.no_grad() (or on detached "
                          "tensors) and take its gradient with token_logprobs_backward")
-    dev, device = logits.get_device(), logits.device
+    dev = logits.get_device()
     with _entered(dev, stream) as on:
         pl, ldl = _rows(logits, "logits", shape, logits.dtype, dev)
         pt = _vector(tokens, "tokens", p, torch.int64, dev)
         # the row's numbers in one allocation
-        made = torch.empty((1 + (tokens is not None) + bool(entropy), p), dtype=torch.float32, device=device)
+        made = logits.new_empty((1 + (tokens is not None) + bool(entropy), p), dtype=torch.float32)
         lse, *rest = made.unbind(0)
         logprobs = rest.pop(0) if tokens is not None else None
         h = rest.pop(0) if entropy else None
-        best = torch.empty((p, top), dtype=torch.float32, device=device) if top else None
-        which = torch.empty((p, top), dtype=torch.int64, device=device) if top else None
+        best = logits.new_empty((p, top), dtype=torch.float32) if top else None
+        which = logits.new_empty((p, top), dtype=torch.int64) if top else None
         n = _LIB.ozaki2_token_logprobs_workspace_size(p, v, top)
-        work = torch.empty(n, dtype=torch.uint8, device=device) if n else None
+        work = logits.new_empty((n,), dtype=torch.uint8) if n else None
         rc = _LIB.ozaki2_token_logprobs(kind, p, v, pl, ldl, pt, top, logprobs.data_ptr() if logprobs is not None else None,
                                         lse.data_ptr(), h.data_ptr() if h is not None else None,
                                         which.data_ptr() if top else None, best.data_ptr() if top else None,

@@ -86,41 +86,59 @@ __device__ __forceinline__ uint64_t key_of(float l, uint32_t index) {
 }
 __device__ __forceinline__ int64_t index_of(uint64_t key) { return 0xFFFFFFFFu - static_cast<uint32_t>(key); }
 
-__device__ __forceinline__ uint64_t lane_xor(uint64_t v, int mask) {
-  const uint32_t lo = __shfl_xor(static_cast<uint32_t>(v), mask, 64), hi = __shfl_xor(static_cast<uint32_t>(v >> 32), mask, 64);
-  return static_cast<uint64_t>(hi) << 32 | lo;
+// Lane l's value from lane l ^ MASK: within rows of 16 lanes by data-parallel primitives, whose
+// latency is a few cycles where a permute through LDS takes some 60 (a sort of 64 keys has 18 of its 21
+// exchanges there).
+template <int MASK>
+__device__ __forceinline__ uint32_t lane_xor32(uint32_t v) {
+  constexpr int kQuad1 = 0xB1, kQuad2 = 0x4E, kQuad3 = 0x1B, kMirror = 0x140, kHalfMirror = 0x141;  // xor 1, 2, 3, 15, 7
+  auto dpp = [](uint32_t x, auto ctrl) {
+    return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), decltype(ctrl)::value, 0xF, 0xF, true));
+  };
+  if constexpr (MASK == 1) return dpp(v, std::integral_constant<int, kQuad1>{});
+  else if constexpr (MASK == 2) return dpp(v, std::integral_constant<int, kQuad2>{});
+  else if constexpr (MASK == 4) return dpp(dpp(v, std::integral_constant<int, kHalfMirror>{}), std::integral_constant<int, kQuad3>{});
+  else if constexpr (MASK == 8) return dpp(dpp(v, std::integral_constant<int, kMirror>{}), std::integral_constant<int, kHalfMirror>{});
+  else return __shfl_xor(v, MASK, 64);
 }
-__device__ __forceinline__ uint64_t exchange(uint64_t v, int j, bool larger) {
-  const uint64_t o = lane_xor(v, j);
+template <int MASK>
+__device__ __forceinline__ uint64_t lane_xor(uint64_t v) {
+  return static_cast<uint64_t>(lane_xor32<MASK>(static_cast<uint32_t>(v >> 32))) << 32 | lane_xor32<MASK>(static_cast<uint32_t>(v));
+}
+template <int J>
+__device__ __forceinline__ uint64_t exchange(uint64_t v, bool larger) {
+  const uint64_t o = lane_xor<J>(v);
   return (v > o) == larger ? v : o;
 }
+// Exchanges at distances J, J / 2, ... 1; falls: whether the lane's run of 2 J is to fall.
+template <int J>
+__device__ __forceinline__ uint64_t exchanges(uint64_t v, bool falls) {
+  v = exchange<J>(v, ((threadIdx.x & J) == 0) == falls);
+  if constexpr (J > 1) v = exchanges<J / 2>(v, falls);
+  return v;
+}
 // One key per lane, into falling order (a bitonic sorting network).
+template <int K = 2>
 __device__ __forceinline__ uint64_t wave_sort(uint64_t v) {
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int k = 2; k <= 64; k *= 2)
-#pragma unroll
-    for (int j = k / 2; j > 0; j /= 2) v = exchange(v, j, ((lane & j) == 0) == ((lane & k) == 0));
+  v = exchanges<K / 2>(v, (threadIdx.x & K) == 0 || K == 64);
+  if constexpr (K < 64) v = wave_sort<2 * K>(v);
   return v;
 }
 // The 64 largest of two sorted waves, sorted.
 __device__ __forceinline__ uint64_t wave_merge(uint64_t a, uint64_t b) {
-  const int lane = threadIdx.x & 63;
-  b = lane_xor(b, 63);  // b in rising order
-  a = a > b ? a : b;
-#pragma unroll
-  for (int j = 32; j > 0; j /= 2) a = exchange(a, j, (lane & j) == 0);
-  return a;
+  b = lane_xor<63>(b);  // b in rising order
+  return exchanges<32>(a > b ? a : b, true);
 }
 // The 64 largest over the workgroup's sorted waves, sorted, in best[0 .. 63].
-__device__ __forceinline__ void group_top(uint64_t sorted, uint64_t (&best)[kWaves][64]) {
+template <int WAVES>
+__device__ __forceinline__ void group_top(uint64_t sorted, uint64_t (&best)[WAVES][64]) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   __syncthreads();
   best[wave][lane] = sorted;
-  __syncthreads();
-  if (wave == 0) {
-    for (int w = 1; w < kWaves; ++w) sorted = wave_merge(sorted, best[w][lane]);
-    best[0][lane] = sorted;
+#pragma unroll 1
+  for (int n = WAVES / 2; n > 0; n /= 2) {
+    __syncthreads();
+    if (wave < n && best[wave + n][0] != 0) best[wave][lane] = wave_merge(best[wave][lane], best[wave + n][lane]);
   }
   __syncthreads();
 }
@@ -142,24 +160,35 @@ __device__ __forceinline__ void load_logits(const T* row, int chunk, int v, floa
 
 struct Top {
   uint64_t best[kWaves][64];
+  uint64_t bounds[kWaves];
   uint64_t list[kList];
   unsigned count;
 };
 
 // The `top` largest logits of chunks c0 .. c1 - 1 of a row as sorted keys, in s.best[0]; a thread
 // has read every kThreads-th chunk from c0 + threadIdx.x on, and found its largest logit `most`
-// first in chunk `at` (negative: no chunk).  The top-th largest of the threads' maxima bounds the
-// top-th largest logit from below, so only the threads whose maximum reaches it look at their
-// chunks again (from a cache), and collect what reaches it: a few more than `top` of independent
-// logits.  Where there are more than the list holds (rows in rising order, a few runs of large
+// first in chunk `at` (negative: no chunk).  The top-th largest of the threads' maxima, of all or of
+// one wave's, bounds the top-th largest logit from below; only the threads whose maximum reaches it
+// look at their chunks again (from a cache), and collect what reaches it: a few times `top` of
+// independent logits.  Where there are more than the list holds (rows in rising order, a few runs of large
 // ones), the top-th largest of the 1024 collected is a better bound: at least 1024 - top of them
 // fall out, so the rounds end.
 template <typename T>
 __device__ __forceinline__ void top_of_chunks(Top& s, const T* row, int v, int c0, int c1, float most, int at, int top) {
   const uint64_t mine = at < 0 ? 0 : key_of(most, 8u * static_cast<unsigned>(at));  // no key of this thread is above
-  group_top(wave_sort(mine), s.best);
+  uint64_t bound;
+  if (top <= 32) {
+    const uint64_t sorted = wave_sort(mine);
+    if (static_cast<int>(threadIdx.x & 63) == top - 1) s.bounds[threadIdx.x >> 6] = sorted;
+    __syncthreads();
+    bound = s.bounds[0];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) bound = bound > s.bounds[w] ? bound : s.bounds[w];
+  } else {  // (the least of a wave's 64 maxima would let too many through)
+    group_top(wave_sort(mine), s.best);
+    bound = s.best[0][top - 1];
+  }
   // (the maximum may be any of its chunk's eight)
-  uint64_t bound = s.best[0][top - 1];
   bound = bound == 0 ? 1 : bound - 7;
   while (true) {
     if (threadIdx.x == 0) s.count = 0;
@@ -271,32 +300,35 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(Logprobs a, int per)
   }
 }
 
-// The parts of a row, joined in their order.
-constexpr int kMaxParts = 64;
+// The parts of a row, joined in their order; every wave merges the sorted keys of some parts.
+constexpr int kMaxParts = 64, kJoinWaves = 16;
 
 template <typename T>
-__global__ __launch_bounds__(kThreads) void logprobs_join_kernel(Logprobs a, int parts) {
-  __shared__ uint64_t best[kWaves][64];
+__global__ __launch_bounds__(64 * kJoinWaves) void logprobs_join_kernel(Logprobs a, int parts) {
+  __shared__ uint64_t best[kJoinWaves][64];
   const long row = blockIdx.x;
-  if (a.top > 0) {
-    const int n = parts * a.top;
-    const uint64_t* const keys = a.keys + row * n;
-    uint64_t sorted = 0;
-    for (int k = 0; k < n; k += kThreads) {
-      const uint64_t next = wave_sort(k + static_cast<int>(threadIdx.x) < n ? keys[k + threadIdx.x] : 0);
-      sorted = k == 0 ? next : wave_merge(sorted, next);
-    }
-    group_top(sorted, best);
-  }
-  if (threadIdx.x >= 64) return;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   Stats s = Stats::none();
-  if (static_cast<int>(threadIdx.x) < parts) {
-    const float4 f = a.stats[row * parts + threadIdx.x];
+  if (lane < parts && wave == 0) {
+    const float4 f = a.stats[row * parts + lane];
     s.m = f.x;
     s.s = f.y;
     s.t = f.z;
   }
-  finish_row<T>(a, row, wave_join(s), best[0]);
+  if (a.top > 0) {
+    const uint64_t* const keys = a.keys + row * parts * a.top;
+    uint64_t own[kMaxParts / kJoinWaves];
+#pragma unroll
+    for (int i = 0; i < kMaxParts / kJoinWaves; ++i) {
+      const int part = wave + kJoinWaves * i;
+      own[i] = part < parts && lane < a.top ? keys[part * a.top + lane] : 0;
+    }
+#pragma unroll
+    for (int i = 1; i < kMaxParts / kJoinWaves; ++i)
+      if (wave + kJoinWaves * i < parts) own[0] = wave_merge(own[0], own[i]);
+    group_top(own[0], best);
+  }
+  if (wave == 0) finish_row<T>(a, row, wave_join(s), best[0]);
 }
 
 // Few rows are divided among up to 1024 workgroups, each with at least two chunks per thread.
@@ -323,7 +355,7 @@ static hipError_t logprobs(const Logprobs& a, hipStream_t st) {
     a.top > 0 ? launch(std::false_type{}, std::true_type{}) : launch(std::false_type{}, std::false_type{});
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess || parts == 1) return err;
-  hipLaunchKernelGGL(logprobs_join_kernel<T>, dim3(a.p), dim3(kThreads), 0, st, a, parts);
+  hipLaunchKernelGGL(logprobs_join_kernel<T>, dim3(a.p), dim3(a.top > 0 ? 64 * kJoinWaves : 64), 0, st, a, parts);
   return hipGetLastError();
 }
 
@@ -361,9 +393,10 @@ __global__ __launch_bounds__(kThreads) void logprobs_bwd_kernel(LogprobsGrad a, 
     s = waves[0];
 #pragma unroll
     for (int w = 1; w < kWaves; ++w) s.join(waves[w]);
-    m = s.m;
-    logs = __builtin_amdgcn_logf(s.s) * kLn2;
+    // (every logit -Inf: a maximum above them leaves p = 0)
     none = s.s == 0.0f;
+    m = none ? FLT_MAX : s.m;
+    logs = none ? 0.0f : __builtin_amdgcn_logf(s.s) * kLn2;
   }
   float dlp = 0.0f;
   int token = -1;
@@ -372,14 +405,20 @@ __global__ __launch_bounds__(kThreads) void logprobs_bwd_kernel(LogprobsGrad a, 
     dlp = t < 0 ? 0.0f : t >= a.v ? __builtin_nanf("") : a.dlogprob[row];
     token = t >= 0 && t < a.v ? static_cast<int>(t) : -1;
   }
-  const float dh = a.dentropy != nullptr ? a.dentropy[row] : 0.0f, h = a.dentropy != nullptr ? a.entropy[row] : 0.0f;
+  const float dh = a.dentropy != nullptr ? a.dentropy[row] : 0.0f;
+  // dlogprob + dentropy entropy (an entropy whose gradient is 0 is left out: it may not be finite)
+  const float rest = dh == 0.0f ? dlp : __builtin_fmaf(dh, a.entropy[row] - logs, dlp);
+  const float logs2 = logs * kLog2e;
+  if (none) dlp = 0.0f;
   auto gradient = [&](float (&x)[8], int c) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float z = x[i] - m - logs, p = exp_of(z);
-      // (an entropy's gradient of 0 leaves an entropy that is not finite out)
-      const float g = dh == 0.0f ? dlp : __builtin_fmaf(dh, fmaxf(z, kGone) + h, dlp);
-      x[i] = none ? 0.0f : (8 * c + i == token ? dlp : 0.0f) - p * g;
+      const float d = x[i] - m, p = __builtin_amdgcn_exp2f(__builtin_fmaf(d, kLog2e, -logs2));
+      x[i] = -p * __builtin_fmaf(dh, fmaxf(d, kGone), rest);
+    }
+    if (c == token >> 3) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] += i == (token & 7) ? dlp : 0.0f;
     }
   };
   int c = c0 + static_cast<int>(threadIdx.x);
