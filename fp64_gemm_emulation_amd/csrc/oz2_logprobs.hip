@@ -245,7 +245,10 @@ __device__ __forceinline__ void finish_row(const Logprobs& a, long row, const St
   }
 }
 
-// One row, or the part blockIdx.y of it, per workgroup: one pass with running maximum and sums.
+// One row, or the part blockIdx.y of it, per workgroup: one pass with running maximum and sums, which
+// a step of 32 logits moves to its maximum at once.  Bound by memory: 4096 x 131072 bf16 with the
+// entropy in 167 us, 6.4 TB/s (non-temporal loads).  16 rows of 131072 with 20 of the largest, in 32
+// parts, take 9.0 us, of which the selection is about half, and the join 4.2.
 template <typename T, bool ENTROPY, bool TOP, bool NT>
 __global__ __launch_bounds__(kThreads) void logprobs_kernel(Logprobs a, int per) {
   __shared__ Stats waves[kWaves];
@@ -370,6 +373,8 @@ hipError_t launch_logprobs(const Logprobs& a, hipStream_t st) {
 // workgroup works the row's maximum and sum out anew, and takes (l - m) - log s.
 constexpr float kLseHeld = 64.0f;
 
+// Bound by memory: 4096 x 131072 bf16, read and written once, in 400 us, 5.4 TB/s (the runtime's copy
+// moves 5.1 both ways).
 template <typename T, bool NT>
 __global__ __launch_bounds__(kThreads) void logprobs_bwd_kernel(LogprobsGrad a, int per) {
   __shared__ Stats waves[kWaves];

@@ -97,7 +97,10 @@ __device__ __forceinline__ void norm_factors(const float (&v)[HELD][8], float su
 }
 
 // One row per THREADS threads (several rows to a workgroup of 256 where a wave holds one), HELD
-// groups of eight elements per thread, so a row is read once.
+// groups of eight elements per thread, so a row is read once and stays in registers between its
+// sum, its products and, for int8, its largest magnitude.  Bound by memory: 16384 x 8192 bf16 with a
+// residual in 174 us, 6.2 TB/s (157 with int8 rows); one row of 8192 in 3.7 us, mostly the launch and
+// two trips through LDS.
 template <typename T, int THREADS, int HELD, bool I8, bool NT>
 __global__ __launch_bounds__(THREADS < 256 ? 256 : THREADS) void rms_norm_kernel(Norm n) {
   constexpr int kGroup = THREADS < 256 ? 256 : THREADS, kRows = kGroup / THREADS;
@@ -179,16 +182,24 @@ static hipError_t rms_norm(const Norm& n, hipStream_t st) {
     const auto kernel = nt ? rms_norm_kernel<T, THREADS, HELD, I8, true> : rms_norm_kernel<T, THREADS, HELD, I8, false>;
     hipLaunchKernelGGL(kernel, grid, dim3(kGroup), 0, st, n);
   };
-  if (groups <= 256 && n.p >= 512)
-    launch(std::integral_constant<int, 64>{}, std::integral_constant<int, 4>{});
+  // As few threads as hold the row without idle ones, and for few long rows twice as many.  Times of
+  // 64 x 4, 256 x 1 and 512 x 2 threads x groups: 16384 x 512 15.3 (64 x 1: 13.2), 20.9 and 50 us; 777 x
+  // 1999 6.4, 5.5 and 7.1; 65536 x 1024 88 (64 x 2: 88), 102 and 226; 16384 x 2048 41.8, 41.4 and 56.
+  // Of 256 x 4, 512 x 2 and 1024 x 1: 64 x 8192 5.1, 4.1 and 4.3; 2048 x 8192 22.9, 22.0 and 24.2; 16384 x
+  // 8192 174, 175 and 174, with int8 rows 157, 159 and 265.
+  using std::integral_constant;
+  if (groups <= 64)
+    launch(integral_constant<int, 64>{}, integral_constant<int, 1>{});
+  else if (groups <= 128)
+    launch(integral_constant<int, 64>{}, integral_constant<int, 2>{});
   else if (groups <= 256)
-    launch(std::integral_constant<int, 256>{}, std::integral_constant<int, 1>{});
-  else if (groups <= 1024 && n.p >= 512)
-    launch(std::integral_constant<int, 256>{}, std::integral_constant<int, 4>{});
+    launch(integral_constant<int, 256>{}, integral_constant<int, 1>{});
+  else if (groups <= 1024 && n.p <= 2048)
+    launch(integral_constant<int, 512>{}, integral_constant<int, 2>{});
   else if (groups <= 1024)
-    launch(std::integral_constant<int, 1024>{}, std::integral_constant<int, 1>{});
+    launch(integral_constant<int, 256>{}, integral_constant<int, 4>{});
   else
-    launch(std::integral_constant<int, 1024>{}, std::integral_constant<int, 4>{});
+    launch(integral_constant<int, 1024>{}, integral_constant<int, 4>{});
   return hipGetLastError();
 }
 
@@ -203,7 +214,7 @@ hipError_t launch_rms_norm(const Norm& n, hipStream_t st) {
 // With n = h rstd and g = dy w: dx = rstd (g - n mean(g n)) + dh, dw = the sum of dy n over rows.
 // Both sums of a row come from one pass, as mean(g n) = rstd mean(g h); so the forward call leaves
 // nothing but h.  A workgroup takes every gridDim-th row (rows), and adds up its part of dw in
-// registers.
+// registers.  Bound by memory: 16384 x 8192 bf16 with dh in 177 us, 6.1 TB/s.
 template <typename T, int THREADS, int HELD, bool NT>
 __global__ __launch_bounds__(THREADS < 256 ? 256 : THREADS) void rms_norm_bwd_kernel(NormGrad n) {
   constexpr int kGroup = THREADS < 256 ? 256 : THREADS, kRows = kGroup / THREADS;
@@ -302,25 +313,34 @@ __global__ __launch_bounds__(THREADS < 256 ? 256 : THREADS) void rms_norm_bwd_ke
   }
 }
 
-// Threads per row and groups of eight they hold, by the row's length.
+// f(threads per row, groups of eight they hold, most workgroups), by the matrix's size.  More
+// workgroups mean shorter loops over rows and more partial sums of dw.  Times without the sums of the
+// parts: of 64 x 4 and 256 x 1 threads x groups, 256 x 2048 6.4 and 4.0 us, 16384 x 2048 45 and 58 (512
+// workgroups); of 256 x 4 and 512 x 2, 256 x 8192 8.0 and 7.2, 512 x 8192 11.6 and 10.3 (256
+// workgroups), 16384 x 8192 177 and 210 (512; 228 and 206 with 256).
 template <typename F>
-static void with_row(int q, F f) {
+static void with_grad_row(int p, int q, F f) {
+  using std::integral_constant;
   const int groups = (q + 7) / 8;
-  if (groups <= 256)
-    f(std::integral_constant<int, 64>{}, std::integral_constant<int, 4>{});
+  if (groups <= 128)
+    f(integral_constant<int, 64>{}, integral_constant<int, 2>{}, 512);
+  else if (groups <= 256 && p <= 1024)
+    f(integral_constant<int, 256>{}, integral_constant<int, 1>{}, 512);
+  else if (groups <= 256)
+    f(integral_constant<int, 64>{}, integral_constant<int, 4>{}, 512);
+  else if (groups <= 1024 && p <= 512)
+    f(integral_constant<int, 512>{}, integral_constant<int, 2>{}, 256);
   else if (groups <= 1024)
-    f(std::integral_constant<int, 256>{}, std::integral_constant<int, 4>{});
+    f(integral_constant<int, 256>{}, integral_constant<int, 4>{}, 512);
   else
-    f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 4>{});
+    f(integral_constant<int, 1024>{}, integral_constant<int, 4>{}, 512);
 }
-
-constexpr int kGradBlocks = 512;  // two workgroups to a CU
 
 int norm_grad_blocks(int p, int q) {
   int blocks = 0;
-  with_row(q, [&](auto threads, auto) {
+  with_grad_row(p, q, [&](auto threads, auto, int most) {
     constexpr int THREADS = decltype(threads)::value, kRows = THREADS < 256 ? 256 / THREADS : 1;
-    blocks = std::min((p + kRows - 1) / kRows, kGradBlocks);
+    blocks = std::min((p + kRows - 1) / kRows, most);
   });
   return blocks;
 }
@@ -330,7 +350,7 @@ static hipError_t rms_norm_bwd(const NormGrad& n, hipStream_t st) {
   const bool nt = static_cast<double>(n.p) * n.q * sizeof(T) > kStreamBytes;
   const int blocks = norm_grad_blocks(n.p, n.q);
   if (blocks > 0) {
-    with_row(n.q, [&](auto threads, auto held) {
+    with_grad_row(n.p, n.q, [&](auto threads, auto held, int) {
       constexpr int THREADS = decltype(threads)::value, HELD = decltype(held)::value;
       const auto kernel = nt ? rms_norm_bwd_kernel<T, THREADS, HELD, true> : rms_norm_bwd_kernel<T, THREADS, HELD, false>;
       hipLaunchKernelGGL(kernel, dim3(blocks), dim3(THREADS < 256 ? 256 : THREADS), 0, st, n);
