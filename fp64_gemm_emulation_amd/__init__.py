@@ -1,4 +1,4 @@
-"""Ozaki Scheme II FP64 GEMM emulation, and linear layers in 16 and 8 bits, for AMD MI355X (gfx950).
+"""Ozaki Scheme II FP64 GEMM emulation, linear layers in 16 and 8 bits and what stands around them, for AMD MI355X (gfx950).
 
 The compute path is the HIP library ``liboz2.so`` (sources in ``csrc/``, C ABI in
 ``include/oz2.h``); ``binding`` is its thin ctypes binding.  The binding is loaded

@@ -3,7 +3,8 @@
 Argument marshalling only: every step of the computation runs in the HIP library.
 The functions named like the C entry points take plain integers / device pointers;
 ``dgemm`` and ``dgemm_debug``, and ``linear``, ``linear_backward``, ``dropout_add``,
-``quantize_rows`` and ``linear_i8``, are conveniences over torch tensors (PyTorch supplies
+``quantize_rows``, ``linear_i8``, ``linear_adapters``, ``rms_norm`` and its kin and
+``token_logprobs`` with its gradient, are conveniences over torch tensors (PyTorch supplies
 device memory and the current stream, nothing else).
 
 Loading fails loudly if the library has not been built: there is no fallback.

@@ -311,6 +311,9 @@ __device__ __forceinline__ void product_tile(char* smem, unsigned wg, int part, 
   // Order matters: loads return in order, and the first stages' copies keep a tile's start busy.  The
   // rows' adapters and S (which no adapter's number is needed for) are asked for before the copies,
   // the first adapter's B behind the first stage's.
+  // Measured: 8192 x 8192 outputs at depth 2048, rank 64, 24 requests, bias and gelu, 275 to 290 us, where
+  // the product alone takes 228: bound by what a tile waits for before its first stage, four times.  37
+  // rows with adapters of their own, rank 32, 8192 -> 2048, 11.4 us (10.0 without).
   typedef i32x4 Frags[4][2];
   int own[ADAPT ? MB / 4 : 1];  // the adapter of row 64 h + lane of the wave's
   Frags sf;                     // S of four blocks, 64 elements of rank
@@ -488,7 +491,8 @@ __device__ __forceinline__ void product_tile(char* smem, unsigned wg, int part, 
     if constexpr (ADAPT) {
       // The condition holds whenever this kernel runs.  It is called unlikely so that the compiler, which
       // takes nested loops for the hot part, does not spill in the loop over the depth, where a reload
-      // waits for the copies under way, or between the epilogue's stores, where it waits for them.
+      // waits for the copies under way, or between the epilogue's stores, where it waits for them (490 us and
+      // more for 8192 x 8192 outputs).
       if (__builtin_expect_with_probability(ad->rank > 0, 0, 1.0)) adapters_term();
     }
     wait_copies(0, S::RING - 1);
@@ -918,7 +922,8 @@ __device__ __forceinline__ float adapter_sum(const Adapters& ad, int count, int 
 }
 
 // ADAPT: the adapters' term, S and B read behind the first loads of weights: a thread per output adds
-// up its row of B with its token's S, which goes through LDS.
+// up its row of B with its token's S, which goes through LDS.  One row on 8192 x 2048 weights, rank 16, takes as
+// long as without (9.1 us in a trace).
 template <typename M, typename T, int R, bool QUANT, int ACT, bool FULL, bool ADAPT = false>
 __device__ __forceinline__ void product_few(int rows, int cols, int depth, int per, const void* __restrict__ left, long left_ld,
                                             const typename M::elem* __restrict__ right, long right_ld, Epilogue e,
