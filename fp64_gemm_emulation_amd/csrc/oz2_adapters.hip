@@ -12,7 +12,7 @@ namespace oz2 {
 // under way.  Every token is computed and the adapter's own are stored.  RB: blocks of 16 rows of A
 // that share the tokens' fragments; ranks above 64 take several passes.  Bound by what a CU draws from
 // memory, some 40 GB/s: 8192 tokens of 24 requests at depth 2048, rank 64, 19.1 us (7 of them without
-// any loads); 37 tokens with 32 adapters or so at depth 8192, rank 32, 7.8; one token at depth 2048, rank
+// any loads); 37 tokens with adapters of their own at depth 8192, rank 32, 7.8; one token at depth 2048, rank
 // 16, 1.7.
 template <typename M, typename T, int RB, int TB, int WAVES, int DEEP>
 __global__ __launch_bounds__(64 * WAVES) void adapter_sums_kernel(int rows, int depth, int per, const T* __restrict__ x, long ldx,
