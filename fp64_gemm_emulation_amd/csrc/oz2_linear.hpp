@@ -79,22 +79,24 @@ struct Adapters {
   long ldb, stride_b;
   const int32_t* index;
   const float* scale;  // null: ones
-  // S, pitch() elements to a row; rows without an adapter are not written.  For a product of few rows
-  // as `parts` sums over parts of the depth, [part][row][pitch] in f32, for the others rounded to the
-  // operands' type.
+  // S, pitch() elements of four bytes to a row; rows without an adapter are not written.  `parts` sums over
+  // parts of the depth, [part][row][pitch] in f32, as a product of few rows takes them, or, `split`, the whole
+  // sums as two terms of the operands' type each, in the units of split_terms.
   void* s;
   int parts;
-  bool rounded;
+  bool split;
+  float* unit;  // f16: of the 64 elements k of the row m at [m blocks() + k / 64]
   // (a product of more than a few rows reads B in pieces of 8 elements of rank: ranks between are packed)
   __host__ __device__ int pitch() const { return (rank + 15) / 16 * 16; }
+  __host__ __device__ int blocks() const { return (rank + 63) / 64; }
 };
 // B with rows of ad.rank rounded up to a multiple of 8, zeros behind.
 hipError_t launch_pack_adapters(const Adapters& ad, int cols, void* dst, hipStream_t st);
 __host__ __device__ inline int packed_rank(int rank) { return (rank + 7) / 8 * 8; }
 // Workgroups that share the depth of S.
 int adapter_parts(long rows, long depth);
-// The sum of ad's parts of S, rounded to the type.
-hipError_t launch_join_adapter_sums(int type, int rows, const Adapters& ad, void* out, hipStream_t st);
+// The sum of ad's parts of S, split, in the place of the first part.
+hipError_t launch_join_adapter_sums(int type, int rows, const Adapters& ad, hipStream_t st);
 hipError_t launch_adapter_sums(int type, int rows, int depth, const void* x, long ldx, const Adapters& ad, hipStream_t st);
 
 // out[m][n] = epilogue(sum_k left(m, k) right(n, k)), m < rows, n < cols, k < depth.  An operand

@@ -43,7 +43,8 @@ oz2::Drop make_drop(const oz2_dropout_t* d) {
 struct FwdWork {
   oz2::Plan plan;
   void *x, *w, *partial;
-  void *s, *joined, *b;  // of adapters
+  void *s, *b;  // of adapters
+  float* unit;
 };
 
 FwdWork carve_fwd(Carver& c, long p, long q, long r, bool pack_x, bool pack_w, long adapters = 0, int rank = 0) {
@@ -52,9 +53,8 @@ FwdWork carve_fwd(Carver& c, long p, long q, long r, bool pack_x, bool pack_w, l
   if (adapters > 0 && rank > 0) {
     oz2::Adapters ad{};
     ad.rank = rank;
-    const int parts = oz2::adapter_parts(p, q);
-    w.s = c.take(sizeof(float) * parts * p * ad.pitch());
-    if (parts > 1 && !oz2::few_rows(w.plan)) w.joined = c.take(2 * p * ad.pitch());
+    w.s = c.take(sizeof(float) * oz2::adapter_parts(p, q) * p * ad.pitch());
+    if (!oz2::few_rows(w.plan)) w.unit = static_cast<float*>(c.take(sizeof(float) * p * ad.blocks()));
     if (rank % 8 != 0 && !oz2::few_rows(w.plan)) w.b = c.take(2 * adapters * r * oz2::packed_rank(rank));
   }
   if (oz2::few_rows(w.plan)) return w;  // takes any rows
@@ -180,15 +180,9 @@ int linear(int type, int p, int q, int r, const void* X, int ldx, const void* W,
   if (!adapted) return status(oz2::launch_product(pr, st));
   const oz2_adapters_t& a = *adapters;
   oz2::Adapters ad{a.count, a.rank, a.A, a.lda, a.stride_a, a.B, a.ldb, a.stride_b, a.index, a.scale, ws.s,
-                   oz2::adapter_parts(p, q), false};
-  ad.rounded = ad.parts == 1 && !oz2::few_rows(ws.plan);
+                   oz2::adapter_parts(p, q), !oz2::few_rows(ws.plan), ws.unit};
   if ((rc = status(oz2::launch_adapter_sums(type, p, q, X, ldx, ad, st))) != OZ2_OK) return rc;
-  if (ws.joined != nullptr) {
-    if ((rc = status(oz2::launch_join_adapter_sums(type, p, ad, ws.joined, st))) != OZ2_OK) return rc;
-    ad.s = ws.joined;
-    ad.parts = 1;
-    ad.rounded = true;
-  }
+  if (ad.split && ad.parts > 1 && (rc = status(oz2::launch_join_adapter_sums(type, p, ad, st))) != OZ2_OK) return rc;
   if (ws.b != nullptr) {
     if ((rc = status(oz2::launch_pack_adapters(ad, r, ws.b, st))) != OZ2_OK) return rc;
     ad.b = ws.b;

@@ -305,20 +305,24 @@ __device__ __forceinline__ void product_tile(char* smem, unsigned wg, int part, 
   // A wave goes through the adapters of its rows, 64 at a time; where the depth has several parts or the
   // tile two groups of waves, these share the adapters.  Fragments come straight from memory (a cache,
   // mostly), and their products go to the rows that are the adapter's by selection, not by zeros in S:
-  // an infinity in one request's adapter stays out of the others' rows.  S is rounded to the operands'
-  // type, which is what feeds the matrix cores: half a step, 2^-8 in bf16 and 2^-11 in f16, of this
-  // term alone.
+  // an infinity in one request's adapter stays out of the others' rows.  S comes as two terms of the operands'
+  // type (split_terms), each of which meets B.
   // Order matters: loads return in order, and the first stages' copies keep a tile's start busy.  The
   // rows' adapters and S (which no adapter's number is needed for) are asked for before the copies,
   // the first adapter's B behind the first stage's.
-  // Measured: 8192 x 8192 outputs at depth 2048, rank 64, 24 requests, bias and gelu, 275 to 290 us, where
-  // the product alone takes 228: bound by what a tile waits for before its first stage, four times.  37
-  // rows with adapters of their own, rank 32, 8192 -> 2048, 11.4 us (10.0 without).
-  typedef i32x4 Frags[4][2];
+  // The rank goes by in steps of 32; a 64-row tile, whose rows are those of many requests, holds two (64
+  // rows with adapters of their own, rank 64, 4096 -> 4096: 37.4 us for the call against 52.4 with one; 128- and
+  // 256-row tiles spill).
+  // Measured: 8192 x 8192 outputs at depth 2048, 24 requests, bias and gelu, 245 to 250 us at rank 16, 255 to
+  // 260 at 32 and 290 to 300 at 64, where the product alone takes 229: bound by what a tile waits for before
+  // its first stage, four times.  37 rows with adapters of their own, rank 32, 8192 -> 2048, 11.4 us (10.0 without).
+  constexpr bool kUnits = ADAPT && std::is_same_v<T, f16>;
   int own[ADAPT ? MB / 4 : 1];  // the adapter of row 64 h + lane of the wave's
-  Frags sf;                     // S of four blocks, 64 elements of rank
-  i32x4 bf[NB][2];              // B of `held`
-  int held = -1;
+  constexpr int kSteps = S::BM == 64 ? 2 : 1;  // of 32 elements of rank, held at a time
+  i32x4 sf[kSteps][4][2];       // S of four blocks of rows, both terms
+  float unit[4];
+  i32x4 bf[kSteps][NB];         // B of `held`
+  int held = -1, held_s = 0;    // S of 64 h + k0 / 32
   const int shares = static_cast<int>(gridDim.y) * S::GROUPS, share = part * S::GROUPS + group;
   constexpr bool kAlone = S::BM == 256;  // one part, one group of waves
   // (places beyond the rank are read inside it and set to zero; rows and columns outside the output are
@@ -329,22 +333,30 @@ __device__ __forceinline__ void product_tile(char* smem, unsigned wg, int part, 
     for (int nb = 0; nb < NB; ++nb) {
       const int col = min(n0 + wn * (16 * NB) + 32 * (nb >> 1) + 4 * (nb & 1) + 8 * (li >> 2) + (li & 3), cols - 1);
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int k = k0 + 32 * half + 8 * lg;
-        __builtin_memcpy(&bf[nb][half], b + col * ad->ldb + (k < ad->rank ? k : 0), 16);
+      for (int i = 0; i < kSteps; ++i) {
+        const int k = k0 + 32 * i + 8 * lg;
+        if (i == 0 || k0 + 32 * i < ad->rank) __builtin_memcpy(&bf[i][nb], b + col * ad->ldb + (k < ad->rank ? k : 0), 16);
       }
     }
     held = adapter;
   };
+  const int pitch = ADAPT ? ad->pitch() : 0;
+  const char* const s_base = ADAPT ? static_cast<const char*>(ad->s) + 4 * m0 * pitch : nullptr;
   auto load_s = [&](int h, int k0) {
 #pragma unroll
-    for (int mb = 0; mb < 4; ++mb)
+    for (int mb = 0; mb < 4; ++mb) {
+      const int m = min(wm * (16 * MB) + 64 * h + 16 * mb + li, last_m);  // of the tile's rows
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int k = k0 + 32 * half + 8 * lg, pitch = ad->pitch();
-        const long m = min(m0 + wm * (16 * MB) + 64 * h + 16 * mb + li, static_cast<long>(rows) - 1);
-        sf[mb][half] = *reinterpret_cast<const i32x4*>(static_cast<const T*>(ad->s) + m * pitch + (k < pitch ? k : 0));
+      for (int i = 0; i < kSteps; ++i) {
+        const int k = k0 + 32 * i + 8 * lg;
+        if (i > 0 && k0 + 32 * i >= ad->rank) continue;
+        const unsigned at = 4u * (m * pitch + (k < pitch ? k : 0));
+#pragma unroll
+        for (int term = 0; term < 2; ++term) sf[i][mb][term] = *reinterpret_cast<const i32x4*>(s_base + at + 16 * term);
       }
+      if constexpr (kUnits) unit[mb] = ad->unit[(m0 + m) * ad->blocks() + k0 / 64];
+    }
+    held_s = 64 * h + k0 / 32;
   };
   // rows of group h whose adapter is this part's and group of waves's to add
   auto shared_rows = [&](int h) {
@@ -364,36 +376,44 @@ __device__ __forceinline__ void product_tile(char* smem, unsigned wg, int part, 
   };
   auto adapters_term = [&]() {
     static_assert(!ADAPT || (E == 2 && LL == kAlongDepth && RL == kAlongDepth && MB % 4 == 0), "16-bit operands along the depth");
-    const int pitch = ad->pitch(), rank = ad->rank;
+    const int rank = ad->rank;
 #pragma unroll
     for (int h = 0; h < MB / 4; ++h) {
       for (unsigned long todo = shared_rows(h); todo != 0;) {
         const int adapter = __builtin_amdgcn_readlane(own[h], __builtin_ctzl(todo));
         const unsigned long match = __ballot(own[h] == adapter);
         todo &= ~match;
-        for (int k0 = 0; k0 < rank; k0 += 64) {
-          if (h > 0 || held != adapter || rank > 64) {  // (kept over the groups of rows they are spilled)
-            load_b(adapter, k0);
-            load_s(h, k0);
-          }
+        for (int k0 = 0; k0 < rank; k0 += 32 * kSteps) {
+          if (h > 0 || k0 > 0 || held != adapter) load_b(adapter, k0);  // (kept over the groups of rows it is spilled)
+          if (held_s != 64 * h + k0 / 32) load_s(h, k0);
           OZ2_SCHED_FENCE();
-          const int k = k0 + 8 * lg;
           const i32x4 zero = {0, 0, 0, 0};
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb) {
-            bf[nb][0] = k < rank ? bf[nb][0] : zero;
-            bf[nb][1] = k + 32 < rank ? bf[nb][1] : zero;
-          }
+          for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) bf[i][nb] = k0 + 32 * i + 8 * lg < rank ? bf[i][nb] : zero;
 #pragma unroll
           for (int mb = 0; mb < 4; ++mb) {
-            sf[mb][0] = k < pitch ? sf[mb][0] : zero;
-            sf[mb][1] = k + 32 < pitch ? sf[mb][1] : zero;
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+              for (int term = 0; term < 2; ++term) sf[i][mb][term] = k0 + 32 * i + 8 * lg < pitch ? sf[i][mb][term] : zero;
             const bool mine = match >> (16 * mb + li) & 1;
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
-              const Acc t = M::mma(bf[nb][1], sf[mb][1], M::mma(bf[nb][0], sf[mb][0], Acc{0, 0, 0, 0}));
+              Acc& a = acc[4 * h + mb][nb];
+              Acc t = kUnits ? Acc{0, 0, 0, 0} : a;
 #pragma unroll
-              for (int v = 0; v < 4; ++v) acc[4 * h + mb][nb][v] = mine ? acc[4 * h + mb][nb][v] + t[v] : acc[4 * h + mb][nb][v];
+              for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+                for (int term = 0; term < 2; ++term)
+                  if (i == 0 || k0 + 32 * i < rank) t = M::mma(bf[i][nb], sf[i][mb][term], t);
+#pragma unroll
+              for (int v = 0; v < 4; ++v) {
+                float sum = t[v];
+                if constexpr (kUnits) sum = __builtin_fmaf(t[v], unit[mb], a[v]);
+                a[v] = mine ? sum : a[v];
+              }
             }
             OZ2_SCHED_FENCE();
           }

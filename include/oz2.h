@@ -367,9 +367,10 @@ typedef struct oz2_adapters {
 
 /*
  * ozaki2_linear_adapters -- Y = R + act(A), A_i = X_i W^T + bias + scale_a (X_i A_a^T) B_a^T with
- * a = index[i]: ozaki2_linear with the adapters' term in its product, for serving.  X_i A_a^T is
- * summed in f32; on products of more than a few rows it is rounded to `type` before it meets B_a, as
- * the matrix cores' operands are.  An adapter reaches its own rows only, whatever it holds.
+ * a = index[i]: ozaki2_linear with the adapters' term in its product, for serving.  scale_a X_i A_a^T
+ * is summed in f32 and may be anywhere in its range; on products of more than a few rows it meets B_a as two
+ * terms of `type`, which hold it within 2^-16 of itself (bf16), or 2^-22 of itself or 2^-37 of the largest of 64
+ * elements of rank (f16).  An adapter reaches its own rows only, whatever it holds.
  * work / work_bytes: ozaki2_linear_adapters_workspace_size bytes, `aligned` 0 or, where rows are as
  * OZ2_LINEAR_ALIGNED says, 1.  (On products of more than a few rows a rank that is no multiple of 8 has
  * every B copied into it.)
