@@ -382,6 +382,22 @@ __global__ __launch_bounds__(kThreads) void logprobs_bwd_kernel(LogprobsGrad a, 
   const T* const l = static_cast<const T*>(a.logits) + row * a.ld;
   T* const d = static_cast<T*>(a.dlogits) + row * a.ldd;
   const int chunks = (a.v + 7) / 8, c0 = per * static_cast<int>(blockIdx.y), c1 = min(c0 + per, chunks);
+  float dlp = 0.0f;
+  int token = -1;
+  const float dh = a.dentropy != nullptr ? a.dentropy[row] : 0.0f;
+  bool reached = dh != 0.0f;
+  if (a.dlogprob != nullptr) {
+    const int64_t t = a.tokens[row];
+    dlp = t < 0 ? 0.0f : t >= a.v ? __builtin_nanf("") : a.dlogprob[row];
+    token = t >= 0 && t < a.v ? static_cast<int>(t) : -1;
+    reached = reached || t >= 0;
+  }
+  if (!reached) {  // whatever a padded place holds is not looked at
+    const float zeros[8] = {};
+    for (int c = c0 + static_cast<int>(threadIdx.x); c < c1; c += kThreads)
+      store8<T, NT>(d + 8 * static_cast<long>(c), a.v - 8 * c, zeros);
+    return;
+  }
   float m = a.lse[row], logs = 0.0f;
   bool none = false;  // every logit is -Inf: no gradient
   if (!(fabsf(m) <= kLseHeld)) {
@@ -403,14 +419,6 @@ __global__ __launch_bounds__(kThreads) void logprobs_bwd_kernel(LogprobsGrad a, 
     m = none ? FLT_MAX : s.m;
     logs = none ? 0.0f : __builtin_amdgcn_logf(s.s) * kLn2;
   }
-  float dlp = 0.0f;
-  int token = -1;
-  if (a.dlogprob != nullptr) {
-    const int64_t t = a.tokens[row];
-    dlp = t < 0 ? 0.0f : t >= a.v ? __builtin_nanf("") : a.dlogprob[row];
-    token = t >= 0 && t < a.v ? static_cast<int>(t) : -1;
-  }
-  const float dh = a.dentropy != nullptr ? a.dentropy[row] : 0.0f;
   // dlogprob + dentropy entropy (an entropy whose gradient is 0 is left out: it may not be finite)
   const float rest = dh == 0.0f ? dlp : __builtin_fmaf(dh, a.entropy[row] - logs, dlp);
   const float logs2 = logs * kLog2e;

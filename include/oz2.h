@@ -450,7 +450,9 @@ size_t ozaki2_token_logprobs_workspace_size(int p, int v, int top);
  * ozaki2_token_logprobs_bwd -- gradient of the logits from those of logprob and entropy (each may
  * be NULL), with lse and, for dentropy, entropy as the forward call gave them:
  *   dL_ij = dlogprob_i (delta_{j t_i} - p_ij) - dentropy_i p_ij (log p_ij + entropy_i)
- * Rows with t < 0 have no part of logprob, rows with t >= v give NaN, rows of -Inf alone zeros.
+ * Rows with t < 0 have no part of logprob, rows with t >= v give NaN, rows of -Inf alone zeros.  A row
+ * that neither reaches (t < 0 or no dlogprob, and dentropy 0 or NULL), as a padded place, gives zeros whatever
+ * it holds.
  * dL may be L itself (same pointer and leading dimension).
  */
 int ozaki2_token_logprobs_bwd(int type, int p, int v, const float* dlogprob, const void* L, int ldl, const int64_t* tokens,
