@@ -489,6 +489,11 @@ def _no_autograd(name):
                      "and take its gradients with linear_backward or dropout_add")
 
 
+def _no_second_gradient(name):
+    """The same for a gradient's operands."""
+    raise ValueError(f"{name} is not differentiated by autograd: call it under torch.no_grad() (or on detached tensors)")
+
+
 def _written(out):
     """`out` was written without torch's knowledge: autograd's check of saved tensors goes by
     its version."""
@@ -855,13 +860,16 @@ def rms_norm_i8(x, weight=None, residual=None, eps: float = 1e-6, hidden=None, s
 def rms_norm_backward(dy, h, weight=None, dh=None, eps: float = 1e-6, needs=("x", "weight"), stream=None):
     """(dx, dweight) of rms_norm from dy and its h (x itself without a residual); those not named in
     `needs` are None.  dh is the gradient that reaches h from its other uses; dx, which holds it
-    too, is the gradient of x and of residual alike."""
+    too, is the gradient of x and of residual alike.  No autograd, as linear."""
     torch = _torch or _use_torch()
     p, q = shape = _shape2(dy, "dy")
     kind = _kind(dy, "dy", f32=True)
     unknown = set(needs) - {"x", "weight"}
     if unknown:
         raise ValueError(f"needs names {sorted(unknown)}: only x and weight have gradients here")
+    if _grad_enabled() and (dy.requires_grad or (h is not None and h.requires_grad) or (weight is not None and weight.requires_grad)
+                            or (dh is not None and dh.requires_grad)):
+        _no_second_gradient("rms_norm_backward")
     dtype, dev = dy.dtype, dy.get_device()
     with _entered(dev, stream) as on:
         pdy, lddy = _rows(dy, "dy", shape, dtype, dev)
@@ -933,7 +941,8 @@ def token_logprobs(logits, tokens=None, top: int = 0, entropy: bool = False, str
 
 def token_logprobs_backward(dlogprobs, logits, tokens, lse, dentropy=None, entropy=None, out=None, stream=None):
     """The logits' gradient from dlogprobs [p] float32 (None: none) and dentropy [p] (None: none),
-    with lse and, for dentropy, entropy from token_logprobs.  `out` may be logits itself."""
+    with lse and, for dentropy, entropy from token_logprobs.  `out` may be logits itself.  A row that
+    neither reaches (a negative token, no dentropy) gives zeros whatever it holds.  No autograd, as linear."""
     torch = _torch or _use_torch()
     p, v = shape = _shape2(logits, "logits")
     kind = _kind(logits, "logits", f32=True)
@@ -943,8 +952,10 @@ def token_logprobs_backward(dlogprobs, logits, tokens, lse, dentropy=None, entro
         raise ValueError("the gradient of the entropy needs entropy")
     if lse is None:
         raise ValueError("lse, as token_logprobs gives it, is needed")
-    if out is not None and out.requires_grad and _grad_enabled():
-        raise ValueError("out requires a gradient: token_logprobs_backward is not differentiated by autograd")
+    if _grad_enabled() and (logits.requires_grad or lse.requires_grad or (dlogprobs is not None and dlogprobs.requires_grad)
+                            or (dentropy is not None and dentropy.requires_grad)
+                            or (entropy is not None and entropy.requires_grad) or (out is not None and out.requires_grad)):
+        _no_second_gradient("token_logprobs_backward")
     dtype, dev = logits.dtype, logits.get_device()
     f32 = torch.float32
     with _entered(dev, stream) as on:
