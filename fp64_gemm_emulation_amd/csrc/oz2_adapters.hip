@@ -50,10 +50,10 @@ __device__ __forceinline__ void split_terms(float s, T& first, T& second) {
 // instruction's rows are 16 of the adapter's, its columns 16 tokens.  Operands go straight from
 // memory to registers: a wave has a piece of the depth, in steps of 32 elements, DEEP of them
 // under way.  Every token is computed and the adapter's own are stored.  RB: blocks of 16 rows of A
-// that share the tokens' fragments; ranks above 64 take several passes.  Bound by what a CU draws from
-// memory, some 40 GB/s: 8192 tokens of 24 requests at depth 2048, rank 64, 19.1 us (7 of them without
-// any loads); 37 tokens with adapters of their own at depth 8192, rank 32, 7.8; one token at depth 2048, rank
-// 16, 1.7.
+// that share the tokens' fragments; ranks above 64 take several passes.  SPLIT: the sums go out as split_terms
+// has them.  Bound by what a CU draws from memory, some 40 GB/s: 8192 tokens of 24 requests at depth 2048, rank
+// 64, 19.5 us (7 of them without any loads); 37 tokens with adapters of their own at depth 8192, rank 32, 8.0;
+// one token at depth 2048, rank 16, 1.6.
 template <typename M, typename T, bool SPLIT, int RB, int TB, int WAVES, int DEEP>
 __global__ __launch_bounds__(64 * WAVES) void adapter_sums_kernel(int rows, int depth, int per, const T* __restrict__ x, long ldx,
                                                                   Adapters ad) {
@@ -186,9 +186,11 @@ __global__ __launch_bounds__(64 * WAVES) void adapter_sums_kernel(int rows, int 
 constexpr int kFewTokens = 256;  // rows up to which a workgroup takes 16 tokens and a part of the depth
 
 // A CU draws some 40 GB/s from memory, so few rows are spread over the CUs by parts of the depth (37 rows
-// with 32 adapters of rank 32 at depth 8192: 24 us in one part, 8.6 in 4, 7.0 in 16).  Many have
-// workgroups enough; dividing those made them no faster (8192 rows, rank 64, depth 2048: 19.6 us in one
-// part and in two, 25 in four).
+// with 32 adapters of rank 32 at depth 8192: 24 us in one part, 8.6 in 4, 7.0 in 16).  Dividing many made
+// them no faster (8192 rows, rank 64, depth 2048: 19.6 us in one part and in two, 25 in four).  Between,
+// a workgroup with 64 tokens and the whole depth takes as long as it does for 8192 rows, however few there are
+// beside it, so there is a step behind the last of the few: 256 and 257 rows, rank 64, take 10 and 19 us at
+// depth 2048 and 30 and 60 at depth 8192, rank 16 6 and 12, 14 and 38.
 int adapter_parts(long rows, long depth) {
   return rows <= kFewTokens ? static_cast<int>(std::max(1L, std::min({depth / 512, 1024 / std::max(rows, 1L), 16L}))) : 1;
 }
@@ -272,7 +274,9 @@ hipError_t launch_join_adapter_sums(int type, int rows, const Adapters& ad, hipS
   return hipGetLastError();
 }
 
-// A thread per 16 bytes; blockIdx.y the adapter.
+// A thread per 16 bytes; blockIdx.y the adapter.  Every adapter's B is copied, used or not, by each call: 17 rows,
+// 2048 -> 8192, rank 4 take 21.8 us with 8 adapters, 25.4 with 100 and 50 with 1000 (rank 8, whose B is read as
+// it lies, 19.5 with any number).
 __global__ __launch_bounds__(256) void pack_adapters_kernel(Adapters ad, int cols, uint16_t* dst) {
   const int per_row = packed_rank(ad.rank) / 8;
   const long n = static_cast<long>(blockIdx.x) * 256 + threadIdx.x, row = n / per_row;

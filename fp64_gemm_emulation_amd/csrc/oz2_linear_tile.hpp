@@ -313,9 +313,10 @@ __device__ __forceinline__ void product_tile(char* smem, unsigned wg, int part, 
   // The rank goes by in steps of 32; a 64-row tile, whose rows are those of many requests, holds two (64
   // rows with adapters of their own, rank 64, 4096 -> 4096: 37.4 us for the call against 52.4 with one; 128- and
   // 256-row tiles spill).
-  // Measured: 8192 x 8192 outputs at depth 2048, 24 requests, bias and gelu, 245 to 250 us at rank 16, 255 to
-  // 260 at 32 and 290 to 300 at 64, where the product alone takes 229: bound by what a tile waits for before
-  // its first stage, four times.  37 rows with adapters of their own, rank 32, 8192 -> 2048, 11.4 us (10.0 without).
+  // Measured: 8192 x 8192 outputs at depth 2048, 24 requests, bias and gelu, with S's 12 to 20 us in it, 266 us at
+  // rank 16, 278 at 32 and 317 at 64 (f16: 333), where the product alone takes 229: bound by what a tile waits for
+  // before its first stage, four times.  37 rows with adapters of their own, rank 32, 8192 -> 2048, 11.4 us (10.0
+  // without).
   constexpr bool kUnits = ADAPT && std::is_same_v<T, f16>;
   int own[ADAPT ? MB / 4 : 1];  // the adapter of row 64 h + lane of the wave's
   constexpr int kSteps = S::BM == 64 ? 2 : 1;  // of 32 elements of rank, held at a time
@@ -943,7 +944,10 @@ __device__ __forceinline__ float adapter_sum(const Adapters& ad, int count, int 
 
 // ADAPT: the adapters' term, S and B read behind the first loads of weights: a thread per output adds
 // up its row of B with its token's S, which goes through LDS.  One row on 8192 x 2048 weights, rank 16, takes as
-// long as without (9.1 us in a trace).
+// long as without (9.1 to 9.7 us in a trace).  B beyond the first 16 of rank is read behind the barrier, 8 elements at
+// a time, and every workgroup adds up S's parts for itself: on 4096 x 8192 weights, S before it included, one row
+// takes 17.4 us at rank 16, 18.4 at 32, 19.7 at 64 and 32 at 256 (12.9 without adapters); eight rows 20, 21, 23 and
+// 41 (15.2); sixteen 26, 28, 30 and 47 (16.5).
 template <typename M, typename T, int R, bool QUANT, int ACT, bool FULL, bool ADAPT = false>
 __device__ __forceinline__ void product_few(int rows, int cols, int depth, int per, const void* __restrict__ left, long left_ld,
                                             const typename M::elem* __restrict__ right, long right_ld, Epilogue e,

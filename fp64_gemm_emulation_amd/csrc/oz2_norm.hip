@@ -99,8 +99,9 @@ __device__ __forceinline__ void norm_factors(const float (&v)[HELD][8], float su
 // One row per THREADS threads (several rows to a workgroup of 256 where a wave holds one), HELD
 // groups of eight elements per thread, so a row is read once and stays in registers between its
 // sum, its products and, for int8, its largest magnitude.  Bound by memory: 16384 x 8192 bf16 with a
-// residual in 174 us, 6.2 TB/s (157 with int8 rows); one row of 8192 in 3.7 us, mostly the launch and
-// two trips through LDS.
+// residual in 174 us, 6.2 TB/s (157 with int8 rows); one row of 8192 in 4.4 us in a trace, mostly the launch and
+// two trips through LDS.  f32: 8192 x 8192 in 222 us, 4.8 TB/s, 2048 x 2048 14.2.  Rows above 8192, by 1024 threads:
+// 8192 x 16384 bf16 in 196 us (240 with int8 rows), f32 425 (403); 256 x 32768 bf16 14.4.
 template <typename T, int THREADS, int HELD, bool I8, bool NT>
 __global__ __launch_bounds__(THREADS < 256 ? 256 : THREADS) void rms_norm_kernel(Norm n) {
   constexpr int kGroup = THREADS < 256 ? 256 : THREADS, kRows = kGroup / THREADS;
@@ -214,7 +215,10 @@ hipError_t launch_rms_norm(const Norm& n, hipStream_t st) {
 // With n = h rstd and g = dy w: dx = rstd (g - n mean(g n)) + dh, dw = the sum of dy n over rows.
 // Both sums of a row come from one pass, as mean(g n) = rstd mean(g h); so the forward call leaves
 // nothing but h.  A workgroup takes every gridDim-th row (rows), and adds up its part of dw in
-// registers.  Bound by memory: 16384 x 8192 bf16 with dh in 177 us, 6.1 TB/s.
+// registers.  Bound by memory: 16384 x 8192 bf16 with dh in 177 us, 6.1 TB/s; f32 8192 x 8192, with the sums
+// of dw's parts, 211.  Rows above 8192 are not: 1024 threads have 128 registers each, which w, dw, h and dy of 32
+// columns outgrow, and 472 to 484 bytes of scratch memory a lane hold the rest: 8192 x 16384 820 us (f32 1185), 4096 x
+// 32768 684, 256 x 16384 52.
 template <typename T, int THREADS, int HELD, bool NT>
 __global__ __launch_bounds__(THREADS < 256 ? 256 : THREADS) void rms_norm_bwd_kernel(NormGrad n) {
   constexpr int kGroup = THREADS < 256 ? 256 : THREADS, kRows = kGroup / THREADS;
